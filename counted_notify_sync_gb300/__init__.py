@@ -1,4 +1,5 @@
-"""counted_notify_sync_gb300: SYNCALL epoch barrier and CntNotify on GB300.
+"""counted_notify_sync_gb300: SYNCALL epoch barrier and CntNotify on GB300, and device-wide steps of a
+training step built like the barrier's persistent kernels (routing to experts, gradient norm and clipping).
 
 The C ABI (include/cns.h, libcns.so) does all the work; this package is the
 thin Python side: ``_native`` mirrors the C entry points one to one, and the
@@ -11,6 +12,8 @@ from ._native import *  # noqa: F401,F403  (C names and constants)
 
 __all__ = [n for n in dir(_native) if not n.startswith("_")] + [
     "build", "new_workspace", "run_syncall", "run_statemachine", "run_pipeline",
+    "new_step_workspace", "new_route", "run_route", "run_route_backward", "new_grad_clip", "run_grad_norm",
+    "run_grad_clip",
 ]
 
 
@@ -125,3 +128,210 @@ def run_pipeline(done, ack, tiles: int, tile_words: int, rounds: int, producer_s
     cfg.consumer_wait = consumer_wait
     rc = _native.cns_pipeline_run(cfg)
     return cfg, rc, checksums, released
+
+
+# --- device-wide steps of a training step ------------------------------------------------------------------
+
+def _dtype_code(t):
+    torch = _torch()
+    codes = {torch.float32: _native.CNS_DT_F32, torch.bfloat16: _native.CNS_DT_BF16, torch.float16: _native.CNS_DT_F16}
+    if t.dtype not in codes:
+        raise TypeError(f"float32, bfloat16 or float16 expected, got {t.dtype}")
+    return codes[t.dtype]
+
+
+def new_step_workspace(nbytes: int, device=None, stream=None):
+    """An initialised workspace of `nbytes` for cns_route, cns_grad_norm and cns_grad_clip.  Calls that follow
+    one another on a stream may share one; calls that may overlap need one each."""
+    torch = _torch()
+    nbytes = max(nbytes, _native.CNS_STEP_WORKSPACE_HEADER_BYTES)
+    ws = torch.empty((nbytes + 15) // 16 * 4, dtype=torch.int32, device=device or "cuda")   # torch aligns to 512 bytes
+    _native.check(_native.cns_step_workspace_init(ws, ws.numel() * 4, stream), "cns_step_workspace_init")
+    return ws
+
+
+def new_route(tokens: int, experts: int, top_k: int, *, score: int = _native.CNS_SCORE_SOFTMAX, groups: int = 1,
+              top_groups: int = 0, group_top: int = 1, renorm: bool = True, scale: float = 1.0, plan: bool = True,
+              scores: bool = False, workspace=None, timeout_ms: int = 0, device=None, stream=None):
+    """A routing of up to `tokens` tokens (cns_route_t, see cns.h for the rules), with the tensors that
+    run_route fills:
+      ids [tokens, top_k] int32, weights [tokens, top_k] float32;
+      with plan: offsets [experts + 1], order [tokens * top_k], places [tokens, top_k], all int32;
+      with scores: scores [tokens, experts] float32."""
+    torch = _torch()
+    r = _native.Route()
+    device = torch.device(device or "cuda")
+    rc, nbytes = _native.cns_route_workspace_bytes(tokens, experts, top_k)
+    _native.check(rc, "new_route")
+    i32 = dict(dtype=torch.int32, device=device)
+    r.ids = torch.empty((tokens, top_k), **i32)
+    r.weights = torch.empty((tokens, top_k), dtype=torch.float32, device=device)
+    r.scores = torch.empty((tokens, experts), dtype=torch.float32, device=device) if scores else None
+    r.offsets = torch.empty(experts + 1, **i32) if plan else None
+    r.order = torch.empty(tokens * top_k, **i32) if plan else None
+    r.places = torch.empty((tokens, top_k), **i32) if plan else None
+    r.workspace = workspace
+    if plan and workspace is None:
+        r.workspace = new_step_workspace(nbytes, device, stream)
+    r.capacity = tokens
+    r.ids_dev, r.weights_dev, r.scores_dev = _native.ptr(r.ids), _native.ptr(r.weights), _native.ptr(r.scores)
+    r.offsets_dev, r.order_dev, r.places_dev = _native.ptr(r.offsets), _native.ptr(r.order), _native.ptr(r.places)
+    r.workspace_dev = _native.ptr(r.workspace)
+    r.workspace_bytes = r.workspace.numel() * r.workspace.element_size() if r.workspace is not None else 0
+    r.experts, r.top_k, r.score = experts, top_k, score
+    r.groups, r.top_groups, r.group_top = groups, top_groups, group_top
+    r.renorm, r.scale, r.timeout_ms = int(renorm), scale, timeout_ms
+    return r
+
+
+def _check_logits(route, logits, what):
+    t, e = route.capacity, route.experts
+    shape, stride = logits.shape, logits.stride()
+    if not (len(shape) == 2 and shape[1] == e and shape[0] <= t and logits.device == route.ids.device and
+            (stride[1] == 1 or e == 1) and (shape[0] <= 1 or stride[0] >= e)):
+        raise ValueError(f"{what}: [tokens <= {t}, {e}] on {route.ids.device}, rows apart and of unit stride, expected; "
+                         f"got {tuple(shape)}, strides {stride}, on {logits.device}")
+
+
+def _check_rows(x, name, rows, cols, dtype, device):
+    if not (x.is_contiguous() and x.dim() == 2 and x.shape[0] >= rows and x.shape[1] == cols and x.dtype == dtype and
+            x.device == device):
+        raise ValueError(f"{name}: contiguous {dtype} [tokens, {cols}] on {device} expected")
+
+
+def run_route(route, logits, bias=None, stream=None, sync: bool = False):
+    """Route the rows of `logits` ([tokens, experts], float32, bfloat16 or float16, rows at any stride) on
+    `stream` (None: the default stream).  Returns `route`, whose tensors hold the results: the first
+    logits.shape[0] rows, and of `order` the first logits.shape[0] * top_k."""
+    _check_logits(route, logits, "logits")
+    if bias is not None:
+        if not (bias.is_contiguous() and bias.numel() == route.experts and bias.dtype == route.weights.dtype and
+                bias.device == logits.device):
+            raise ValueError("bias: contiguous float32 [experts] on the logits' device expected")
+    route.dtype = _dtype_code(logits)
+    route.logits_dev, route.tokens = logits.data_ptr(), logits.shape[0]
+    route.logits_stride = logits.stride(0) if logits.shape[0] > 1 else 0
+    route.bias_dev = None if bias is None else bias.data_ptr()
+    route.stream = _native.stream_handle(stream)
+    route.sync = 1 if sync else 0
+    _native.check(_native.cns_route(route), "cns_route")
+    return route
+
+
+def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogits=None, stream=None):
+    """dL/dlogits of run_route(route, logits): from dL/dweights [tokens, top_k] float32 and, if given,
+    dL/dscores [tokens, experts] float32.  `ids` are the chosen experts (default: route.ids); the result goes to
+    `dlogits` (default: a new tensor) in the logits' type."""
+    torch = _torch()
+    _check_logits(route, logits, "logits")
+    t = logits.shape[0]
+    ids = route.ids if ids is None else ids
+    if dlogits is None:
+        dlogits = torch.empty((t, route.experts), dtype=logits.dtype, device=logits.device)
+    _check_logits(route, dlogits, "dlogits")
+    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+        raise ValueError("dlogits: the logits' type and shape expected")
+    _check_rows(ids, "ids", t, route.top_k, torch.int32, logits.device)
+    _check_rows(dweights, "dweights", t, route.top_k, torch.float32, logits.device)
+    if dscores is not None:
+        _check_rows(dscores, "dscores", t, route.experts, torch.float32, logits.device)
+    g = _native.RouteGrad()
+    g.logits_dev, g.ids_dev, g.dweights_dev = logits.data_ptr(), ids.data_ptr(), dweights.data_ptr()
+    g.dscores_dev = None if dscores is None else dscores.data_ptr()
+    g.dlogits_dev, g.stream = dlogits.data_ptr(), _native.stream_handle(stream)
+    g.tokens, g.experts, g.top_k = t, route.experts, route.top_k
+    g.logits_stride = logits.stride(0) if t > 1 else 0
+    g.dlogits_stride = dlogits.stride(0) if t > 1 else 0
+    g.dtype, g.score, g.renorm, g.scale = _dtype_code(logits), route.score, route.renorm, route.scale
+    _native.check(_native.cns_route_backward(g), "cns_route_backward")
+    return dlogits
+
+
+def _dense(t):
+    """Whether the tensor's elements fill one stretch of memory, in whatever order of the axes."""
+    at = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != at:
+            return False
+        at *= size
+    return True
+
+
+def new_grad_clip(grads, max_norm: float = float("inf"), *, outs=None, eps: float = 1e-6,
+                  norm_type: int = _native.CNS_NORM_L2, workspace=None, timeout_ms: int = 0, device=None, stream=None):
+    """The gradients of a step (a list of dense tensors, float32, bfloat16 or float16 mixed as they come) and
+    where their clipped values go: `outs`, tensors of the same shapes and strides, or in place.  Holds the
+    tensors' addresses, so it stands for these tensors for as long as they live; make another one for others.
+    `norm` is the float32 scalar that run_grad_norm and run_grad_clip fill."""
+    torch = _torch()
+    g = _native.GradClip()
+    n = len(grads)
+    device = torch.device(device or (grads[0].device if n else "cuda"))
+    if outs is not None and len(outs) != n:
+        raise ValueError("outs: one for each gradient expected")
+    spans = []
+
+    def table(tensors):
+        a = (_native.Tensor * max(n, 1))()
+        for i, t in enumerate(tensors):
+            if t.device.type != "cuda" or (device.index is not None and t.device != device):
+                raise ValueError(f"tensor {i}: on {t.device}, {device} expected")
+            if t.numel() and not _dense(t):
+                raise ValueError(f"tensor {i}: not dense (strides {t.stride()})")
+            a[i].data_dev, a[i].elems, a[i].dtype = t.data_ptr(), t.numel(), _dtype_code(t)
+        return a
+
+    g.grad_table = table(grads)
+    g.out_table = None if outs is None else table(outs)
+    for i, t in enumerate(grads):
+        span = (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+        if outs is not None and t.numel():
+            o = outs[i]
+            if t.shape != o.shape or t.stride() != o.stride():
+                raise ValueError(f"outs[{i}]: the gradient's shape and strides expected")
+            spans.append((o.data_ptr(), o.data_ptr() + o.numel() * o.element_size(), True, i))
+            if spans[-1][:2] == span and t.dtype == o.dtype:
+                continue   # in place
+        elif outs is not None and t.shape != outs[i].shape:
+            raise ValueError(f"outs[{i}]: the gradient's shape expected")
+        if t.numel():
+            spans.append((*span, outs is None, i))
+    spans.sort()
+    end, written = (0, 0), (0, 0)   # how far the tensors so far reach, and those of them that are written
+    for first, last, writes, i in spans:
+        if first < written[0] or (writes and first < end[0]):
+            raise ValueError(f"tensors {i} and {(written if first < written[0] else end)[1]} overlap")
+        end = max(end, (last, i))
+        if writes:
+            written = max(written, (last, i))
+    g.tensors = (list(grads), None if outs is None else list(outs))   # alive as long as the table
+    g.grads = g.grad_table
+    if g.out_table is not None:
+        g.outs = g.out_table
+    g.count, g.max_norm, g.eps, g.norm_type, g.timeout_ms = n, max_norm, eps, norm_type, timeout_ms
+    g.norm = torch.empty((), dtype=torch.float32, device=device)
+    if workspace is None:
+        rc, nbytes = _native.cns_grad_workspace_bytes(n)
+        _native.check(rc, "new_grad_clip")
+        workspace = new_step_workspace(nbytes, device, stream)
+    g.workspace = workspace
+    g.norm_dev, g.workspace_dev = g.norm.data_ptr(), workspace.data_ptr()
+    g.workspace_bytes = workspace.numel() * workspace.element_size()
+    return g
+
+
+def run_grad_norm(plan, stream=None, sync: bool = False):
+    """The global norm of new_grad_clip's gradients on `stream` (None: the default stream); returns plan.norm."""
+    plan.stream = _native.stream_handle(stream)
+    plan.sync = 1 if sync else 0
+    _native.check(_native.cns_grad_norm(plan), "cns_grad_norm")
+    return plan.norm
+
+
+def run_grad_clip(plan, stream=None, sync: bool = False):
+    """Clip new_grad_clip's gradients by their global norm on `stream`; returns plan.norm, the norm before
+    clipping."""
+    plan.stream = _native.stream_handle(stream)
+    plan.sync = 1 if sync else 0
+    _native.check(_native.cns_grad_clip(plan), "cns_grad_clip")
+    return plan.norm

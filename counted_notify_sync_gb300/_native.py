@@ -78,6 +78,20 @@ CNS_OUT_INVALID = 3
 CNS_PIPE_WAIT_STREAM = 0
 CNS_PIPE_WAIT_IN_KERNEL = 1
 
+CNS_DT_F32 = 0
+CNS_DT_BF16 = 1
+CNS_DT_F16 = 2
+CNS_SCORE_SIGMOID = 0
+CNS_SCORE_SOFTMAX = 1
+CNS_NORM_L2 = 0
+CNS_NORM_INF = 1
+CNS_STEP_WORKSPACE_HEADER_BYTES = 8192
+CNS_STEP_WORKSPACE_ALIGN = 128
+CNS_ROUTE_MAX_EXPERTS = 512
+CNS_ROUTE_MAX_TOP_K = 32
+CNS_ROUTE_MAX_GROUPS = 32
+CNS_GRAD_MAX_TENSORS = 1048576
+
 
 class CnsError(RuntimeError):
     def __init__(self, code: int, what: str = ""):
@@ -116,6 +130,39 @@ class Pipeline(Structure):
     ]
 
 
+class Route(Structure):
+    _fields_ = [
+        ("logits_dev", c_void_p), ("bias_dev", c_void_p), ("ids_dev", c_void_p), ("weights_dev", c_void_p),
+        ("scores_dev", c_void_p), ("offsets_dev", c_void_p), ("order_dev", c_void_p), ("places_dev", c_void_p),
+        ("workspace_dev", c_void_p), ("workspace_bytes", c_uint64), ("stream", c_void_p), ("tokens", c_int64),
+        ("logits_stride", c_int64), ("experts", c_int32), ("top_k", c_int32), ("dtype", c_int32), ("score", c_int32),
+        ("groups", c_int32), ("top_groups", c_int32), ("group_top", c_int32), ("renorm", c_int32),
+        ("scale", c_float), ("timeout_ms", c_uint32), ("sync", c_int32), ("device_status", c_int32),
+    ]
+
+
+class RouteGrad(Structure):
+    _fields_ = [
+        ("logits_dev", c_void_p), ("ids_dev", c_void_p), ("dweights_dev", c_void_p), ("dscores_dev", c_void_p),
+        ("dlogits_dev", c_void_p), ("stream", c_void_p), ("tokens", c_int64), ("logits_stride", c_int64),
+        ("dlogits_stride", c_int64), ("experts", c_int32), ("top_k", c_int32), ("dtype", c_int32), ("score", c_int32),
+        ("renorm", c_int32), ("scale", c_float),
+    ]
+
+
+class Tensor(Structure):
+    _fields_ = [("data_dev", c_void_p), ("elems", c_int64), ("dtype", c_int32), ("reserved", c_int32)]
+
+
+class GradClip(Structure):
+    _fields_ = [
+        ("grads", POINTER(Tensor)), ("outs", POINTER(Tensor)), ("count", c_int64), ("norm_dev", c_void_p),
+        ("workspace_dev", c_void_p), ("workspace_bytes", c_uint64), ("stream", c_void_p), ("norm_type", c_int32),
+        ("max_norm", c_float), ("eps", c_float), ("timeout_ms", c_uint32), ("sync", c_int32),
+        ("device_status", c_int32),
+    ]
+
+
 _SIGS = {
     "syncall_workspace_init": (c_int, [c_void_p, c_size_t, c_uint32, c_void_p]),
     "syncall_workspace_bytes": (c_int, [c_int32, c_int64, POINTER(c_size_t)]),
@@ -143,6 +190,13 @@ _SIGS = {
     "cns_probe_notify_pingpong": (c_int, [c_int, c_int32, c_void_p, c_void_p, c_void_p]),
     "cns_probe_round_phases": (c_int, [c_int32, c_int32, c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_size_t,
                                        c_void_p, c_void_p]),
+    "cns_step_workspace_init": (c_int, [c_void_p, c_size_t, c_void_p]),
+    "cns_route_workspace_bytes": (c_int, [c_int64, c_int32, c_int32, POINTER(c_size_t)]),
+    "cns_route": (c_int, [POINTER(Route)]),
+    "cns_route_backward": (c_int, [POINTER(RouteGrad)]),
+    "cns_grad_workspace_bytes": (c_int, [c_int64, POINTER(c_size_t)]),
+    "cns_grad_norm": (c_int, [POINTER(GradClip)]),
+    "cns_grad_clip": (c_int, [POINTER(GradClip)]),
     "cns_version": (c_int, [POINTER(c_int32), POINTER(c_int32)]),
     "cns_error_string": (c_char_p, [c_int]),
 }
@@ -342,6 +396,40 @@ def cns_probe_round_phases(ctas: int, threads: int, rounds: int, stamp_rounds: i
         workspace_bytes = workspace.numel() * workspace.element_size() if hasattr(workspace, "numel") else 0
     return lib().cns_probe_round_phases(ctas, threads, rounds, stamp_rounds, ptr(buf0), ptr(buf1), ptr(workspace),
                                         workspace_bytes, ptr(stamps), stream_handle(stream))
+
+
+def cns_step_workspace_init(ws, nbytes: int, stream=None) -> int:
+    return lib().cns_step_workspace_init(ptr(ws), nbytes, stream_handle(stream))
+
+
+def cns_route_workspace_bytes(tokens: int, experts: int, top_k: int, out: bool = True):
+    """(code, bytes); out=False passes a NULL bytes pointer."""
+    v = c_size_t(0)
+    rc = lib().cns_route_workspace_bytes(tokens, experts, top_k, ctypes.byref(v) if out else None)
+    return rc, v.value
+
+
+def cns_route(r: Route) -> int:
+    return lib().cns_route(ctypes.byref(r))
+
+
+def cns_route_backward(g: RouteGrad) -> int:
+    return lib().cns_route_backward(ctypes.byref(g))
+
+
+def cns_grad_workspace_bytes(count: int, out: bool = True):
+    """(code, bytes); out=False passes a NULL bytes pointer."""
+    v = c_size_t(0)
+    rc = lib().cns_grad_workspace_bytes(count, ctypes.byref(v) if out else None)
+    return rc, v.value
+
+
+def cns_grad_norm(g: GradClip) -> int:
+    return lib().cns_grad_norm(ctypes.byref(g))
+
+
+def cns_grad_clip(g: GradClip) -> int:
+    return lib().cns_grad_clip(ctypes.byref(g))
 
 
 def cns_version():

@@ -692,6 +692,194 @@ typedef struct {
  */
 int cns_pipeline_run(cns_pipeline_t *cfg);
 
+/* ========================================================================= */
+/* Device-wide steps of a training step                                       */
+/* ========================================================================= */
+
+/* Operators in which every CTA needs a part from every other CTA before any
+ * can go on, run as the library's persistent kernels are: data phase; all
+ * CTAs meet; data phase.  Routing tokens to experts (choose and count; meet;
+ * place the entries by expert) with its gradient, and the global gradient
+ * norm over many tensors with clipping (sum; meet; scale). */
+
+/* Element types of the tensors below. */
+typedef enum { CNS_DT_F32 = 0, CNS_DT_BF16 = 1, CNS_DT_F16 = 2 } cns_dtype_t;
+
+/* A workspace of these operators: a header that carries what the CTAs of a
+ * call exchange, then scratch that needs no initial content.  Line 1 (byte
+ * 128) is a status line as in a SYNCALL workspace (syncall_read_workspace
+ * reads its status).  cns_step_workspace_init zeroes the header once, before
+ * the first use; calls that follow one another on a stream may then share the
+ * workspace, whatever their sizes, but calls that may overlap on the GPU need
+ * one each.  A call that fails on the device (a bounded wait that ran out)
+ * leaves its status, and later calls on the workspace do nothing but report
+ * it, until it is initialised again. */
+#define CNS_STEP_WORKSPACE_HEADER_BYTES 8192
+#define CNS_STEP_WORKSPACE_ALIGN 128
+
+/*
+ * cns_step_workspace_init -- zero the header of a workspace (asynchronous).
+ *   ws_dev  CNS_STEP_WORKSPACE_ALIGN-aligned, `bytes` long
+ *   bytes   >= CNS_STEP_WORKSPACE_HEADER_BYTES
+ * Errors: NULL_PTR, INVALID_VALUE (size or alignment), ARCH, CUDA.
+ */
+int cns_step_workspace_init(void *ws_dev, size_t bytes, cns_stream_t stream);
+
+/* ---- Routing to experts -------------------------------------------------- */
+
+/* The scores of a token's logits l: sigmoid(l), or softmax over its experts. */
+typedef enum { CNS_SCORE_SIGMOID = 0, CNS_SCORE_SOFTMAX = 1 } cns_score_t;
+
+#define CNS_ROUTE_MAX_EXPERTS 512
+#define CNS_ROUTE_MAX_TOP_K 32
+#define CNS_ROUTE_MAX_GROUPS 32
+
+/* One routing of `tokens` rows of logits.
+ *   Choice.  An expert's choice value is its logit if there is no bias and
+ * group_top is 1 (scores rise with logits), else its score in 32 bits plus
+ * its bias.  An expert whose logit is -inf, or whose choice value is -inf, is
+ * masked and never chosen.  With groups > 1, group g is the experts / groups
+ * neighbouring experts from g * (experts / groups) on; it is worth the sum of
+ * its group_top best choice values (of those that are not masked; -inf when
+ * all are), and only the experts of the top_groups worthiest groups can be
+ * chosen.  The top_k best are chosen, best first.  Equals go to the lower
+ * index; NaN ranks above every number, so a NaN logit shows in the weights.
+ *   Weights.  The chosen experts' scores (the bias takes no part).  With
+ * renorm, sigmoid scores are divided by (their sum + 1e-20) and softmax
+ * scores by their sum, which is the softmax over the chosen logits.  Then
+ * times scale.
+ *   Fewer than top_k experts left (masks): the remaining places hold id -1
+ * and weight 0 and make no entry; a row that is all -inf (a padded token)
+ * makes none at all, and its scores are 0.
+ *   Plan.  Entry t * top_k + j is token t's place j.  order lists the entries
+ * expert by expert, by rising entry number within each, then -1; expert e's
+ * are order[offsets[e] .. offsets[e+1]), so offsets[e+1] - offsets[e] is its
+ * load.  places is the inverse: where an entry stands in order, -1 for a
+ * place without an expert.  The results do not depend on timing. */
+typedef struct {
+    const void *logits_dev;  /* (in) [tokens][experts] */
+    const float *bias_dev;   /* (in, optional) [experts] */
+    int32_t *ids_dev;        /* (out) [tokens][top_k] */
+    float *weights_dev;      /* (out) [tokens][top_k] */
+    float *scores_dev;       /* (out, optional) [tokens][experts], all experts' scores */
+    int32_t *offsets_dev;    /* (out, optional) [experts + 1]; NULL: no plan */
+    int32_t *order_dev;      /* (out) [tokens * top_k]; NULL if offsets_dev is */
+    int32_t *places_dev;     /* (out, optional) [tokens][top_k]; NULL if offsets_dev is */
+    void *workspace_dev;     /* (in) needed with a plan */
+    uint64_t workspace_bytes;/* (in) >= cns_route_workspace_bytes */
+    cns_stream_t stream;     /* (in) stream to run on */
+    int64_t tokens;          /* (in) >= 0; tokens * top_k < 2^31 */
+    int64_t logits_stride;   /* (in) elements from row to row, >= experts; 0 = experts */
+    int32_t experts;         /* (in) 1 .. CNS_ROUTE_MAX_EXPERTS */
+    int32_t top_k;           /* (in) 1 .. CNS_ROUTE_MAX_TOP_K, <= experts of top_groups groups */
+    int32_t dtype;           /* (in) cns_dtype_t of the logits */
+    int32_t score;           /* (in) cns_score_t */
+    int32_t groups;          /* (in) 1 .. CNS_ROUTE_MAX_GROUPS, divides experts; 0 = 1 */
+    int32_t top_groups;      /* (in) 1 .. groups; 0 = groups */
+    int32_t group_top;       /* (in) 1 or 2; 0 = 1 */
+    int32_t renorm;          /* (in) 0 or 1 */
+    float scale;             /* (in) finite */
+    uint32_t timeout_ms;     /* (in) bound on each wait; 0 = library default, as in syncall_run */
+    int32_t sync;            /* (in) 1: wait for the call and return its status; 0: enqueue and return */
+    int32_t device_status;   /* (out, sync=1) 0 or CNS_ERR_TIMEOUT */
+} cns_route_t;
+
+/* Workspace bytes for a plan of up to `tokens` tokens.  Host only.
+ * Errors: NULL_PTR (bytes), INVALID_VALUE (tokens < 0, experts or top_k out of range). */
+int cns_route_workspace_bytes(int64_t tokens, int32_t experts, int32_t top_k, size_t *bytes);
+
+/*
+ * cns_route -- choose the experts, weigh them and, with offsets_dev, place the
+ * entries by expert.  Asynchronous on `stream` unless sync; with sync = 0 the
+ * call may be captured into a CUDA graph.
+ * Errors: NULL_PTR, INVALID_VALUE (sizes, enums, alignment to the element,
+ * workspace), ARCH, NOT_RESIDENT, CUDA; with sync=1 also TIMEOUT.
+ */
+int cns_route(cns_route_t *r);
+
+/* The gradient of a routing with respect to its logits, the chosen experts
+ * held fixed: from dL/dweights, and optionally dL/dscores for losses on the
+ * scores (a load-balancing loss).  Experts that no gradient reaches get 0; a
+ * place whose id is outside 0 .. experts - 1 (-1) contributes nothing. */
+typedef struct {
+    const void *logits_dev;    /* (in) as in the forward call */
+    const int32_t *ids_dev;    /* (in) [tokens][top_k], the forward call's */
+    const float *dweights_dev; /* (in) [tokens][top_k] */
+    const float *dscores_dev;  /* (in, optional) [tokens][experts] */
+    void *dlogits_dev;         /* (out) [tokens][experts], dtype's type; not logits_dev */
+    cns_stream_t stream;       /* (in) */
+    int64_t tokens;            /* (in) */
+    int64_t logits_stride;     /* (in) elements from row to row of logits and dlogits each; 0 = experts */
+    int64_t dlogits_stride;    /* (in) */
+    int32_t experts;           /* (in) */
+    int32_t top_k;             /* (in) */
+    int32_t dtype;             /* (in) */
+    int32_t score;             /* (in) */
+    int32_t renorm;            /* (in) */
+    float scale;               /* (in) */
+} cns_route_grad_t;
+
+/*
+ * cns_route_backward -- asynchronous; may be captured into a CUDA graph.
+ * Errors: NULL_PTR, INVALID_VALUE, ARCH, CUDA.
+ */
+int cns_route_backward(const cns_route_grad_t *g);
+
+/* ---- Global gradient norm and clipping ------------------------------------ */
+
+/* A dense tensor: `elems` elements in a row from data_dev. */
+typedef struct {
+    void *data_dev;   /* aligned to its element; may be NULL when elems is 0 */
+    int64_t elems;    /* >= 0 */
+    int32_t dtype;    /* cns_dtype_t */
+    int32_t reserved; /* 0 */
+} cns_tensor_t;
+
+/* L2: sqrt(sum of squares); INF: largest magnitude. */
+typedef enum { CNS_NORM_L2 = 0, CNS_NORM_INF = 1 } cns_norm_t;
+
+/* The gradients of a step, and where the clipped ones go.  norm is taken over
+ * all elements of all tensors together; every element is then multiplied by
+ * min(1, max_norm / (norm + eps)) in 32 bits and rounded once to the output's
+ * type.  A norm of NaN makes the factor NaN, one of inf makes it 0.  Squares
+ * are summed in 32 bits and joined in 64 (so the norm overflows where a square
+ * does, above 1.8e19), in an order that depends on the sizes alone.
+ * Tensors must not overlap, except an output with its own gradient when the
+ * two are the same tensor. */
+typedef struct {
+    const cns_tensor_t *grads; /* (in) host array [count], read during the call */
+    const cns_tensor_t *outs;  /* (in, optional) host array [count], elems as grads'; NULL: in place */
+    int64_t count;             /* (in) tensors, 0 .. CNS_GRAD_MAX_TENSORS */
+    float *norm_dev;           /* (out) the norm */
+    void *workspace_dev;       /* (in) */
+    uint64_t workspace_bytes;  /* (in) >= cns_grad_workspace_bytes */
+    cns_stream_t stream;       /* (in) */
+    int32_t norm_type;         /* (in) cns_norm_t */
+    float max_norm;            /* (in) >= 0 (cns_grad_clip only) */
+    float eps;                 /* (in) >= 0, finite (cns_grad_clip only) */
+    uint32_t timeout_ms;       /* (in) as cns_route_t */
+    int32_t sync;              /* (in) as cns_route_t */
+    int32_t device_status;     /* (out, sync=1) as cns_route_t */
+} cns_grad_clip_t;
+
+#define CNS_GRAD_MAX_TENSORS 1048576
+
+/* Workspace bytes for up to `count` tensors.  Host only.
+ * Errors: NULL_PTR (bytes), INVALID_VALUE (count out of range). */
+int cns_grad_workspace_bytes(int64_t count, size_t *bytes);
+
+/*
+ * cns_grad_norm -- norm_dev = the global norm; outs, max_norm and eps are
+ * ignored.  cns_grad_clip -- the same, then the clipped gradients.  Both are
+ * asynchronous on `stream` unless sync; with sync = 0 they may be captured
+ * into a CUDA graph (the tensors' addresses are then the capture's).
+ * Errors: NULL_PTR, INVALID_VALUE (count, sizes, enums, alignment, workspace,
+ * max_norm or eps out of range), ARCH, NOT_RESIDENT, CUDA; with sync=1 also
+ * TIMEOUT.
+ */
+int cns_grad_norm(cns_grad_clip_t *g);
+int cns_grad_clip(cns_grad_clip_t *g);
+
 /* ------------------------------------------------------------------------- */
 /* Latency and throughput probes (roofline denominators)                      */
 /* ------------------------------------------------------------------------- */
