@@ -4,10 +4,34 @@
 //   norm = sqrt(sum over all tensors of x^2)   (or the largest |x|)
 //   out  = x * min(1, max_norm / (norm + eps))
 //
-// Tensors are cut into tiles of kTileBytes at 16-byte boundaries of the
-// address space (so a tile's vectors are aligned wherever its tensor starts;
-// only a tensor's first and last vector can be partial).  One warp takes one
-// tile.
+// One cooperative launch, one CTA an SM: read everything once and sum; exchange
+// the CTAs' parts (step_device.cuh); scale.
+//
+// Layout.  A tile is `vecs` 16-byte vectors a lane of one warp (512 B to 4 KB,
+// all tiles of a call alike), cut at 16-byte boundaries of the address space:
+// its vectors are aligned wherever its tensor starts, and only a tensor's
+// first and last vector can be partial.  A round is one tile for each warp of
+// the GPU, neighbours to a CTA, so that the rounds sweep through memory; `vecs`
+// is chosen so that the last round is as full as the others.
+//
+// Bound.  The norm reads its bytes once: HBM (400M bf16 elements: 117 us, 6.85
+// TB/s, 103 % of the measured copy rate).  Clipping has to read everything
+// before it can write anything, so a set larger than the chip is read twice
+// and written once: 400M bf16 to bf16 367 us, 6.5 TB/s over 2.4 GB.  What the
+// chip holds it reads once:
+//   - the last round stays in the registers it was summed from (20 MB over the
+//     GPU) and the one before it in shared memory (20 MB);
+//   - the three before those are loaded with an L2 evict-last hint (60 MB), all
+//     others and all stores with evict-first, and the rounds are scaled
+//     backwards.
+// 25M f32 (100 MB in, 100 MB out): 54 us with neither, 47 us with all of this
+// (50 us with streaming stores alone; 48 us without shared memory).  Keeping
+// two rounds in shared memory instead (224 KB) took 54 us: loads in flight
+// need L1, and too little of it was left.  Filling shared memory by bulk
+// copies, which do not, was no faster at 3.5 KB a copy (46 us here, but the
+// norm fell to 6.5 TB/s) and slower below: a bulk copy costs its SM some 50 ns.
+// Small sets are a launch, a trip to memory and the exchange: 0.2M f32
+// elements 4.7 us in a CUDA graph.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -23,9 +47,9 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTileBytes = 4096;
-constexpr int kTileVecs = kTileBytes / 16;      // 16-byte vectors of a tile
-constexpr int kLaneVecs = kTileVecs / 32;       // of one lane
+constexpr int kRowBytes = 512;     // one 16-byte vector a lane
+constexpr int kLaneVecs = 8;       // vectors of a lane in the largest tile
+constexpr uint32_t kKeepL2 = 3;    // rounds that L2 is asked to keep, before the two that stay on the SM
 
 // One tensor of the table.
 struct GradEntry {
@@ -44,7 +68,9 @@ struct GradParams {
     uint64_t timeout_ns;
     int32_t count;
     uint32_t tiles;
+    int32_t vecs;             // of a lane in a tile: the tile is vecs * kRowBytes
     float max_norm, eps;
+    uint32_t start[kStepMaxCtas];   // the tensor that each CTA's first tile lies in
 };
 
 // The kernel's arguments: the table of up to N tensors among them (N = 0: in
@@ -91,12 +117,11 @@ __global__ void grad_table_kernel(const __grid_constant__ TableChunk c)
         c.to[i] = c.e[i];
 }
 
-// Largest i with tile0 <= tile (tensors without elements have
-// no tiles and are not in the table).
+// The tensor that `tile` lies in, between tensors lo and hi (tensors without
+// elements have no tiles and are not in the table).
 template <int N>
-__device__ __forceinline__ int find_tensor(const GradArgs<N> &a, uint32_t tile)
+__device__ __forceinline__ int find_tensor(const GradArgs<N> &a, int lo, int hi, uint32_t tile)
 {
-    int lo = 0, hi = a.p.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (tile0_of(a, mid) <= tile)
@@ -107,13 +132,37 @@ __device__ __forceinline__ int find_tensor(const GradArgs<N> &a, uint32_t tile)
     return lo;
 }
 
-__device__ __forceinline__ uint4 ld_stream(uint64_t a)
+// What L2 does with a line: kNormal as it likes; else a createpolicy value.
+constexpr uint64_t kNormal = 0;
+
+__device__ __forceinline__ uint64_t policy_evict_first()
+{
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ uint64_t policy_evict_last()
+{
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+template <bool HINT>
+__device__ __forceinline__ uint4 ld_stream(uint64_t a, uint64_t policy)
 {
     uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(a)
-                 : "memory");
+    if constexpr (HINT)
+        asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(a), "l"(policy)
+                     : "memory");
+    else
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(a)
+                     : "memory");
     return v;
 }
 
@@ -144,42 +193,50 @@ template <int D> struct Vec {
     }
 };
 
-// The calling lane's vectors of a tile.  Vectors that the tensor covers only in
-// part are loaded element by element; what the tensor does not cover is 0.
+// One tile: where it starts, where its first byte's value goes, and which of
+// its bytes, lo .. len - 1, the tensor has.
+struct Tile {
+    uint64_t base, dst;
+    int lo, len;
+    uint32_t types;
+};
+
+// The calling lane's vectors of a tile.  A vector that the tensor covers only
+// in part is loaded element by element; what it does not cover is 0.
 template <int D>
-__device__ __forceinline__ uint4 load_part(uint64_t a, uint64_t src, uint64_t end)
+__device__ __forceinline__ uint4 load_part(const Tile &t, int o)
 {
     using T = typename Elem<D>::type;
     union { uint4 v; uint16_t h[8]; uint32_t w[4]; } u;
     u.v = make_uint4(0u, 0u, 0u, 0u);
-    if (a + 16 <= src || a >= end)
-        return u.v;
 #pragma unroll
     for (int i = 0; i < Vec<D>::N; ++i) {
-        const uint64_t at = a + i * sizeof(T);
-        if (at >= src && at < end) {
+        const int at = o + i * static_cast<int>(sizeof(T));
+        if (at >= t.lo && at < t.len) {
             if constexpr (sizeof(T) == 4)
-                u.w[i] = *reinterpret_cast<const uint32_t *>(at);
+                u.w[i] = *reinterpret_cast<const uint32_t *>(t.base + at);
             else
-                u.h[i] = *reinterpret_cast<const uint16_t *>(at);
+                u.h[i] = *reinterpret_cast<const uint16_t *>(t.base + at);
         }
     }
     return u.v;
 }
 
-template <int D>
-__device__ __forceinline__ void load_tile(uint64_t base, uint64_t src, uint64_t end, uint4 *v)
+template <int D, bool HINT>
+__device__ __forceinline__ void load_tile(const Tile &t, int vecs, uint4 *v, uint64_t policy)
 {
-    const uint64_t mine = base + (threadIdx.x & 31u) * 16u;
-    if (base >= src && base + kTileBytes <= end) {
+    const int mine = (threadIdx.x & 31u) * 16;
+    if (t.lo == 0 && t.len == vecs * kRowBytes) {
 #pragma unroll
         for (int j = 0; j < kLaneVecs; ++j)
-            v[j] = ld_stream(mine + j * 512);
+            if (j < vecs)
+                v[j] = ld_stream<HINT>(t.base + mine + j * kRowBytes, policy);
     } else {
 #pragma unroll
         for (int j = 0; j < kLaneVecs; ++j) {
-            const uint64_t a = mine + j * 512;
-            v[j] = a >= src && a + 16 <= end ? ld_stream(a) : load_part<D>(a, src, end);
+            const int o = mine + j * kRowBytes;
+            if (j < vecs)
+                v[j] = o >= t.lo && o + 16 <= t.len ? ld_stream<HINT>(t.base + o, policy) : load_part<D>(t, o);
         }
     }
 }
@@ -187,11 +244,13 @@ __device__ __forceinline__ void load_tile(uint64_t base, uint64_t src, uint64_t 
 // A tile's part of the norm for the calling lane: the sum of its squares, or
 // its largest magnitude (as integers, so that NaN is above inf).
 template <int NORM, int D>
-__device__ __forceinline__ float tile_part(const uint4 *v)
+__device__ __forceinline__ float tile_part(const uint4 *v, int vecs)
 {
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < kLaneVecs; ++j) {
+        if (j >= vecs)
+            break;
         float f[Vec<D>::N];
         Vec<D>::unpack(v[j], f);
 #pragma unroll
@@ -209,23 +268,14 @@ __device__ __forceinline__ float tile_part(const uint4 *v)
                                    max(__float_as_uint(acc[2]), __float_as_uint(acc[3]))));
 }
 
-// The running part over tiles, warps and CTAs: in 64 bits.
+// A warp's part from its lanes'.
 template <int NORM>
-__device__ __forceinline__ double join(double a, double b)
+__device__ __forceinline__ float warp_part(float v)
 {
     if constexpr (NORM == CNS_NORM_L2)
-        return a + b;
-    else   // non-negative: ordered as integers, NaN above inf
-        return __longlong_as_double(max(__double_as_longlong(a), __double_as_longlong(b)));
-}
-
-template <int NORM>
-__device__ __forceinline__ double warp_join(double v)
-{
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        v = join<NORM>(v, __shfl_xor_sync(kFullWarp, v, d));
-    return v;
+        return warp_sum(v);
+    else
+        return __uint_as_float(__reduce_max_sync(kFullWarp, __float_as_uint(v)));
 }
 
 template <int D>
@@ -240,78 +290,74 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     }
 }
 
-// Store n = N (4 or 8) values to dst in type D, as wide as its alignment lets;
-// `from` and `to` bound the values that the tensor has.
+// Store N (4 or 8) values in type D to an address that is a multiple of what
+// they take there; they are not read again soon.
 template <int D, int N>
-__device__ __forceinline__ void store_vec(uint64_t dst, const float *f, int from, int to)
+__device__ __forceinline__ void store_aligned(uint64_t dst, const float *f)
+{
+    if constexpr (D == CNS_DT_F32 && N == 8)
+        asm volatile("st.global.cs.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(f[0]), "f"(f[1]),
+                     "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                     : "memory");
+    else if constexpr (D == CNS_DT_F32)
+        __stcs(reinterpret_cast<float4 *>(dst), make_float4(f[0], f[1], f[2], f[3]));
+    else if constexpr (N == 8)
+        __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(pack2<D>(f[0], f[1]), pack2<D>(f[2], f[3]),
+                                                          pack2<D>(f[4], f[5]), pack2<D>(f[6], f[7])));
+    else
+        __stcs(reinterpret_cast<uint2 *>(dst), make_uint2(pack2<D>(f[0], f[1]), pack2<D>(f[2], f[3])));
+}
+
+// The same for values first .. last - 1 only, at any address of D's type.
+template <int D, int N>
+__device__ __forceinline__ void store_vec(uint64_t dst, const float *f, int first, int last)
 {
     using T = typename Elem<D>::type;
-    if (from == 0 && to == N && dst % 16 == 0) {
-        if constexpr (D == CNS_DT_F32) {
-            if constexpr (N == 8) {
-                if (dst % 32 == 0) {   // one 32-byte sector
-                    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(f[0]),
-                                 "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
-                                 : "memory");
-                    return;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < N; i += 4)
-                *reinterpret_cast<float4 *>(dst + 4 * i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-            return;
-        } else if constexpr (N == 8) {
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<D>(f[0], f[1]), pack2<D>(f[2], f[3]),
-                                                         pack2<D>(f[4], f[5]), pack2<D>(f[6], f[7]));
-            return;
-        }
-    }
-    if constexpr (D != CNS_DT_F32 && N == 4) {
-        if (from == 0 && to == N && dst % 8 == 0) {
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<D>(f[0], f[1]), pack2<D>(f[2], f[3]));
-            return;
-        }
+    if (first == 0 && last == N && dst % (N * sizeof(T)) == 0) {
+        store_aligned<D, N>(dst, f);
+        return;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        if (i >= from && i < to)
+        if (i >= first && i < last)
             reinterpret_cast<T *>(dst)[i] = Elem<D>::put(f[i]);
 }
 
 template <int DS, int DD>
-__device__ __forceinline__ void scale_tile(const GradEntry &t, uint64_t base, uint64_t end, const uint4 *v, float factor)
+__device__ __forceinline__ void scale_tile(const Tile &t, int vecs, const uint4 *v, float factor)
 {
-    using S = typename Elem<DS>::type;
-    using T = typename Elem<DD>::type;
+    constexpr int S = static_cast<int>(sizeof(typename Elem<DS>::type));
+    constexpr int T = static_cast<int>(sizeof(typename Elem<DD>::type));
     constexpr int N = Vec<DS>::N;
-    const uint64_t mine = base + (threadIdx.x & 31u) * 16u;
+    const int mine = (threadIdx.x & 31u) * 16;
+    const bool whole = t.lo == 0 && t.len == vecs * kRowBytes && t.dst % (N * T) == 0;
 #pragma unroll
     for (int j = 0; j < kLaneVecs; ++j) {
-        const uint64_t a = mine + j * 512;
-        if (a + 16 <= t.src || a >= end)
-            continue;
+        if (j >= vecs)
+            break;
+        const int o = mine + j * kRowBytes;
         float f[N];
         Vec<DS>::unpack(v[j], f);
 #pragma unroll
         for (int i = 0; i < N; ++i)
             f[i] *= factor;
-        const int from = a < t.src ? static_cast<int>((t.src - a) / sizeof(S)) : 0;
-        const int to = a + 16 > end ? static_cast<int>((end - a) / sizeof(S)) : N;
-        // the vector's first element may lie before the tensor: its place is then never written
-        const int64_t first = (static_cast<int64_t>(a) - static_cast<int64_t>(t.src)) / static_cast<int64_t>(sizeof(S));
-        store_vec<DD, N>(t.dst + first * static_cast<int64_t>(sizeof(T)), f, from, to);
+        if (whole) {
+            store_aligned<DD, N>(t.dst + o / S * T, f);
+        } else if (o + 16 > t.lo && o < t.len) {
+            const int first = o < t.lo ? (t.lo - o) / S : 0;
+            const int last = o + 16 > t.len ? (t.len - o) / S : N;
+            store_vec<DD, N>(t.dst + o / S * T, f, first, last);
+        }
     }
 }
 
 template <int D>
-__device__ __forceinline__ void rescale_tile(const GradEntry &t, uint64_t base, uint64_t end, float factor)
+__device__ __forceinline__ void scale_into(const Tile &t, int vecs, const uint4 *v, float factor)
 {
-    uint4 v[kLaneVecs];
-    load_tile<D>(base, t.src, end, v);
     switch (t.types >> 8) {
-    case CNS_DT_F32: scale_tile<D, CNS_DT_F32>(t, base, end, v, factor); break;
-    case CNS_DT_BF16: scale_tile<D, CNS_DT_BF16>(t, base, end, v, factor); break;
-    default: scale_tile<D, CNS_DT_F16>(t, base, end, v, factor); break;
+    case CNS_DT_F32: scale_tile<D, CNS_DT_F32>(t, vecs, v, factor); break;
+    case CNS_DT_BF16: scale_tile<D, CNS_DT_BF16>(t, vecs, v, factor); break;
+    default: scale_tile<D, CNS_DT_F16>(t, vecs, v, factor); break;
     }
 }
 
@@ -319,73 +365,119 @@ template <int NORM, bool CLIP, int N>
 __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const __grid_constant__ GradArgs<N> a)
 {
     const GradParams &p = a.p;
-    __shared__ double s_part[kWarps];
+    extern __shared__ uint4 s_kept[];   // [vecs][kThreads], the last round but one
+    __shared__ float s_part[kWarps];
     __shared__ float s_factor;
     __shared__ int s_stop;
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    const uint32_t first = warp * gridDim.x + blockIdx.x, step = kWarps * gridDim.x;
-    uint64_t tag = 0;
+    // a round of tiles is one for each warp of the grid, neighbours to a CTA; the last one is shared out evenly
+    const uint32_t full = kWarps * gridDim.x;
+    const uint32_t rounds = (p.tiles + full - 1) / full;
+    auto tile_of = [&](uint32_t round) {
+        const uint32_t n = min(full, p.tiles - round * full);
+        const uint32_t begin = n * blockIdx.x / gridDim.x, end = n * (blockIdx.x + 1) / gridDim.x;
+        return begin + warp < end ? round * full + begin + warp : ~0u;
+    };
+    uint32_t tag = 0;
     bool stop = false;
     if (warp == 0) {
-        tag = static_cast<uint64_t>(ld_relaxed_gpu(p.header + kStepEpochWord)) + 1u;
+        tag = ld_relaxed_gpu(p.header + kStepEpochWord) + 1u;
         stop = ld_relaxed_gpu(p.header + kStepStatusWord + 1) != 0u;   // an earlier call failed
     }
 
-    double part = 0.0;
-    int at = 0;
-    uint32_t next = 0;   // first tile after tensor `at`
-    GradEntry t;
-    uint64_t base = 0, end = 0;
-    // move to `tile`'s tensor
-    auto seek = [&](uint32_t tile) {
-        at = find_tensor(a, tile);
-        t = entry_of(a, at);
-        next = at + 1 < p.count ? tile0_of(a, at + 1) : p.tiles;
-        end = t.src + static_cast<uint64_t>(t.elems) * ((t.types & 0xffu) == CNS_DT_F32 ? 4 : 2);
-    };
-    uint32_t tile = first;
-    for (; tile < p.tiles; tile += step) {
-        if (tile >= next)
-            seek(tile);
-        base = (t.src & ~15ull) + static_cast<uint64_t>(tile - t.tile0) * kTileBytes;
-        uint4 v[kLaneVecs];
-        float f;
-        switch (t.types & 0xffu) {
-        case CNS_DT_F32:
-            load_tile<CNS_DT_F32>(base, t.src, end, v);
-            f = tile_part<NORM, CNS_DT_F32>(v);
-            break;
-        case CNS_DT_BF16:
-            load_tile<CNS_DT_BF16>(base, t.src, end, v);
-            f = tile_part<NORM, CNS_DT_BF16>(v);
-            break;
-        default:
-            load_tile<CNS_DT_F16>(base, t.src, end, v);
-            f = tile_part<NORM, CNS_DT_F16>(v);
-            break;
+    uint4 v[kLaneVecs];
+    int at = static_cast<int>(p.start[blockIdx.x]);
+    uint32_t here = tile0_of(a, at);   // tensor `at` has the tiles here .. next - 1
+    uint32_t next = at + 1 < p.count ? tile0_of(a, at + 1) : p.tiles;
+    Tile tile{};
+    auto visit = [&](uint32_t i) {
+        if (i >= next || i < here) {
+            // every tensor of the table has a tile, so it lies at most as many tensors away as tiles
+            at = i >= next ? find_tensor(a, at + 1, static_cast<int>(min(p.count - 1u, at + (i - here))), i)
+                           : find_tensor(a, at - static_cast<int>(min(static_cast<uint32_t>(at), here - i)), at - 1, i);
+            here = tile0_of(a, at);
+            next = at + 1 < p.count ? tile0_of(a, at + 1) : p.tiles;
         }
-        part = join<NORM>(part, static_cast<double>(f));
+        const GradEntry t = entry_of(a, at);
+        const int S = (t.types & 0xffu) == CNS_DT_F32 ? 4 : 2, T = (t.types >> 8) == CNS_DT_F32 ? 4 : 2;
+        const int bytes = p.vecs * kRowBytes, ahead = static_cast<int>(t.src & 15u);
+        // from the tensor's first element to the tile's first byte; before the tensor in its first tile
+        const int64_t from = static_cast<int64_t>(i - here) * bytes - ahead;
+        tile.types = t.types;
+        tile.base = t.src + from;
+        tile.dst = t.dst + from / S * T;
+        tile.lo = i == here ? ahead : 0;
+        tile.len = static_cast<int>(min(static_cast<int64_t>(bytes), t.elems * S - from));
+    };
+    auto load = [&](uint64_t policy) {
+        switch (tile.types & 0xffu) {
+        case CNS_DT_F32: load_tile<CNS_DT_F32, CLIP>(tile, p.vecs, v, policy); break;
+        case CNS_DT_BF16: load_tile<CNS_DT_BF16, CLIP>(tile, p.vecs, v, policy); break;
+        default: load_tile<CNS_DT_F16, CLIP>(tile, p.vecs, v, policy); break;
+        }
+    };
+    const uint64_t fleeting = CLIP ? policy_evict_first() : kNormal, lasting = CLIP ? policy_evict_last() : kNormal;
+
+    // a lane's sum over its tiles, 64 tiles at a time
+    float part = 0.f, recent = 0.f;
+    for (uint32_t round = 0; round < rounds; ++round) {
+        const uint32_t i = tile_of(round);
+        if (i == ~0u)
+            continue;
+        visit(i);
+        const uint32_t left = rounds - 1 - round;
+        load(left >= 2 && left < 2 + kKeepL2 ? lasting : fleeting);
+        float f;
+        switch (tile.types & 0xffu) {
+        case CNS_DT_F32: f = tile_part<NORM, CNS_DT_F32>(v, p.vecs); break;
+        case CNS_DT_BF16: f = tile_part<NORM, CNS_DT_BF16>(v, p.vecs); break;
+        default: f = tile_part<NORM, CNS_DT_F16>(v, p.vecs); break;
+        }
+        if constexpr (NORM == CNS_NORM_L2) {
+            recent += f;
+            if ((round & 63u) == 63u) {
+                part += recent;
+                recent = 0.f;
+            }
+        } else {
+            part = __uint_as_float(max(__float_as_uint(part), __float_as_uint(f)));
+        }
+        if (CLIP && left == 1) {
+#pragma unroll
+            for (int j = 0; j < kLaneVecs; ++j)
+                if (j < p.vecs)
+                    s_kept[j * kThreads + threadIdx.x] = v[j];
+        }
     }
-    part = warp_join<NORM>(part);
+    part = warp_part<NORM>(NORM == CNS_NORM_L2 ? part + recent : part);
     if (lane == 0)
         s_part[warp] = part;
     __syncthreads();
     if (warp == 0) {
-        part = warp_join<NORM>(s_part[lane]);
+        part = warp_part<NORM>(s_part[lane]);
+        float norm = NORM == CNS_NORM_L2 ? sqrtf(part) : part;
         if (gridDim.x > 1 && !stop) {
-            if (lane == 0)
-                st_slot(p.header, blockIdx.x, static_cast<uint64_t>(__double_as_longlong(part)), tag);
-            part = 0.0;
-            // CTA c's part goes to lane c % 32 in the order of c: the same sum every time
-            stop = wait_slots(p.header, gridDim.x, tag, p.timeout_ns, [&](uint32_t, uint64_t v) {
-                part = join<NORM>(part, __longlong_as_double(static_cast<long long>(v)));
-            });
-            part = warp_join<NORM>(part);
+            // CTAs exchange roots: a sum of squares that is out of range for 32 bits may have a norm that is not
+            send_all(p.header, gridDim.x, tag, __float_as_uint(norm));
+            float r[kStepMaxCtas / 32] = {};
+            stop = receive_all(p.header, gridDim.x, tag, p.timeout_ns, r);
+            uint32_t most = 0;
+#pragma unroll
+            for (float x : r)
+                most = max(most, __float_as_uint(x));
+            norm = __uint_as_float(__reduce_max_sync(kFullWarp, most));
+            if (NORM == CNS_NORM_L2 && norm > 0.f && norm < INFINITY) {
+                // squares of the largest root's parts: nothing overflows
+                float sum = 0.f;
+#pragma unroll
+                for (float x : r)
+                    sum = fmaf(x / norm, x / norm, sum);
+                norm *= sqrtf(warp_sum(sum));
+            }
             if (!stop && blockIdx.x == 0 && lane == 0)
-                st_relaxed_gpu(p.header + kStepEpochWord, static_cast<uint32_t>(tag));
+                st_relaxed_gpu(p.header + kStepEpochWord, tag);
         }
         if (lane == 0) {
-            const float norm = static_cast<float>(NORM == CNS_NORM_L2 ? sqrt(part) : part);
             if (blockIdx.x == 0 && !stop)
                 *p.norm = norm;
             const float f = p.max_norm / (norm + p.eps);
@@ -399,24 +491,27 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const __grid_constant
     if (s_stop)
         return;
     const float factor = s_factor;
-    // backwards: the tiles read last are still in L2
-    if (tile == first)
-        return;
-    for (;;) {
-        tile -= step;
-        if (tile < t.tile0)
-            seek(tile);
-        base = (t.src & ~15ull) + static_cast<uint64_t>(tile - t.tile0) * kTileBytes;
-        // in place, a factor of 1 changes nothing
-        if (factor != 1.f || t.dst != t.src) {
-            switch (t.types & 0xffu) {
-            case CNS_DT_F32: rescale_tile<CNS_DT_F32>(t, base, end, factor); break;
-            case CNS_DT_BF16: rescale_tile<CNS_DT_BF16>(t, base, end, factor); break;
-            default: rescale_tile<CNS_DT_F16>(t, base, end, factor); break;
-            }
+    // backwards: the last round is still in v, the one before it in shared memory, some before them in L2
+    for (uint32_t left = 0; left < rounds; ++left) {
+        const uint32_t i = tile_of(rounds - 1 - left);
+        if (i == ~0u)
+            continue;
+        visit(i);
+        if (factor == 1.f && tile.dst == tile.base)
+            continue;   // in place, a factor of 1 changes nothing
+        if (left == 1) {
+#pragma unroll
+            for (int j = 0; j < kLaneVecs; ++j)
+                if (j < p.vecs)
+                    v[j] = s_kept[j * kThreads + threadIdx.x];
+        } else if (left > 1) {
+            load(fleeting);
         }
-        if (tile < step)
-            break;
+        switch (tile.types & 0xffu) {
+        case CNS_DT_F32: scale_into<CNS_DT_F32>(tile, p.vecs, v, factor); break;
+        case CNS_DT_BF16: scale_into<CNS_DT_BF16>(tile, p.vecs, v, factor); break;
+        default: scale_into<CNS_DT_F16>(tile, p.vecs, v, factor); break;
+        }
     }
 }
 
@@ -438,18 +533,25 @@ int check_tensor(const cns_tensor_t &t)
     return reinterpret_cast<uintptr_t>(t.data_dev) % elem_bytes(t.dtype) ? CNS_ERR_INVALID_VALUE : CNS_SUCCESS;
 }
 
-int64_t tiles_of(const cns_tensor_t &t)
+// Bytes of the 16-byte vectors that a tensor touches, and its tiles.
+int64_t span_of(const cns_tensor_t &t)
 {
     const uint64_t a = reinterpret_cast<uint64_t>(t.data_dev);
-    return static_cast<int64_t>(((a & 15u) + t.elems * elem_bytes(t.dtype) + kTileBytes - 1) / kTileBytes);
+    return static_cast<int64_t>(((a & 15u) + t.elems * elem_bytes(t.dtype) + 15) & ~15ull);
+}
+
+int64_t tiles_of(const cns_tensor_t &t, int vecs)
+{
+    const int64_t tile = vecs * kRowBytes;
+    return t.elems ? (span_of(t) + tile - 1) / tile : 0;
 }
 
 // Tensors that the arguments have room for (32,764 bytes of them in all).
-constexpr int kMostInline = 1000;
+constexpr int kMostInline = 960;
 
 // Fill the table, in the arguments or the workspace, and launch.
 template <int NORM, bool CLIP, int N>
-int launch(const cns_grad_clip_t &g, const GradParams &p, const DeviceInfo &dev)
+int launch(const cns_grad_clip_t &g, const GradParams &p, int ctas)
 {
     cudaStream_t s = to_stream(g.stream);
     GradArgs<N> a;
@@ -458,19 +560,23 @@ int launch(const cns_grad_clip_t &g, const GradParams &p, const DeviceInfo &dev)
     a.p.count = 0;
     TableChunk c;
     c.n = 0;
-    uint32_t tile0 = 0;
+    uint32_t tile0 = 0, cta = 0;
+    const uint32_t first_round = std::min<uint32_t>(p.tiles, kWarps * ctas);
     for (int64_t i = 0; i < g.count; ++i) {
         const cns_tensor_t &t = g.grads[i];
         if (t.elems) {
             const cns_tensor_t &o = CLIP && g.outs ? g.outs[i] : t;
             const GradEntry e{reinterpret_cast<uint64_t>(t.data_dev), reinterpret_cast<uint64_t>(o.data_dev), t.elems,
                               tile0, static_cast<uint32_t>(t.dtype | o.dtype << 8)};
-            tile0 += static_cast<uint32_t>(tiles_of(t));
-            if constexpr (N > 0) {
+            tile0 += static_cast<uint32_t>(tiles_of(t, p.vecs));
+            const int32_t index = a.p.count + c.n;
+            // CTAs whose first tile lies in this tensor
+            for (; cta < static_cast<uint32_t>(ctas) && first_round * cta / ctas < tile0; ++cta)
+                a.p.start[cta] = static_cast<uint32_t>(index);
+            if constexpr (N > 0)
                 a.e[a.p.count++] = e;
-            } else {
+            else
                 c.e[c.n++] = e;
-            }
         }
         if (N == 0 && (c.n == kChunkEntries || (c.n > 0 && i + 1 == g.count))) {
             c.to = const_cast<GradEntry *>(a.p.table) + a.p.count;
@@ -480,17 +586,21 @@ int launch(const cns_grad_clip_t &g, const GradParams &p, const DeviceInfo &dev)
             c.n = 0;
         }
     }
-    // one CTA an SM, fewer when there is not a tile for each
-    const int most = std::min<int>(dev.sm_count, kStepMaxCtas);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(std::max(1, static_cast<int>(std::min<int64_t>(p.tiles, most))));
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
+    if (CLIP && p.tiles > static_cast<uint32_t>(ctas) * kWarps) {   // more than one round
+        cfg.dynamicSmemBytes = static_cast<size_t>(p.vecs) * kRowBytes * kWarps;
+        CNS_CUDA(cudaFuncSetAttribute(grad_kernel<NORM, CLIP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      kLaneVecs * kRowBytes * kWarps));
+    }
     cudaLaunchAttribute coop;
     coop.id = cudaLaunchAttributeCooperative;
     coop.val.cooperative = 1;
     cfg.attrs = &coop;
-    cfg.numAttrs = cfg.gridDim.x > 1 ? 1 : 0;
+    
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
     void *args[] = {&a};
     const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(grad_kernel<NORM, CLIP, N>), args);
     if (e == cudaErrorCooperativeLaunchTooLarge) {
@@ -498,6 +608,15 @@ int launch(const cns_grad_clip_t &g, const GradParams &p, const DeviceInfo &dev)
         return CNS_ERR_NOT_RESIDENT;
     }
     return e == cudaSuccess ? CNS_SUCCESS : cuda_fail(e, "gradient launch");
+}
+
+template <int NORM, bool CLIP>
+int launch_sized(const cns_grad_clip_t &g, const GradParams &p, int ctas)
+{
+    // the arguments are copied with each launch: no more room in them than it takes
+    return g.count <= 64            ? launch<NORM, CLIP, 64>(g, p, ctas)
+           : g.count <= kMostInline ? launch<NORM, CLIP, kMostInline>(g, p, ctas)
+                                    : launch<NORM, CLIP, 0>(g, p, ctas);
 }
 
 template <bool CLIP>
@@ -515,7 +634,7 @@ int grad_run(cns_grad_clip_t *g)
         reinterpret_cast<uintptr_t>(g->workspace_dev) % CNS_STEP_WORKSPACE_ALIGN ||
         g->workspace_bytes < workspace_bytes(g->count))
         return CNS_ERR_INVALID_VALUE;
-    int64_t tiles = 0;
+    int64_t bytes = 0;
     for (int64_t i = 0; i < g->count; ++i) {
         if (int rc = check_tensor(g->grads[i]))
             return rc;
@@ -529,29 +648,33 @@ int grad_run(cns_grad_clip_t *g)
                 return CNS_ERR_INVALID_VALUE;
         }
         if (g->grads[i].elems)
-            tiles += tiles_of(g->grads[i]);
+            bytes += span_of(g->grads[i]);
     }
-    if (tiles > 0x7fffffff)
-        return CNS_ERR_INVALID_VALUE;
     DeviceInfo dev;
     if (int rc = current_device(&dev))
         return rc;
+    // tiles of equal size, so that every warp of the GPU takes the same number of them
+    const int most = std::min<int>(dev.sm_count, kStepMaxCtas);
+    const int64_t round = static_cast<int64_t>(most) * kWarps * kRowBytes;
+    const int64_t rounds = (bytes + round * kLaneVecs - 1) / (round * kLaneVecs);
     GradParams p = {};
+    p.vecs = rounds ? static_cast<int>((bytes + round * rounds - 1) / (round * rounds)) : 1;
+    int64_t tiles = 0;
+    for (int64_t i = 0; i < g->count; ++i)
+        tiles += tiles_of(g->grads[i], p.vecs);
+    if (tiles > 0x7fffffff)
+        return CNS_ERR_INVALID_VALUE;
     p.header = static_cast<uint32_t *>(g->workspace_dev);
     p.norm = g->norm_dev;
     p.timeout_ns = barrier_timeout_ns(g->timeout_ms);
     p.tiles = static_cast<uint32_t>(tiles);
     p.max_norm = g->max_norm;
     p.eps = g->eps;
-    int rc;
-    if (g->count <= 32)
-        rc = g->norm_type == CNS_NORM_L2 ? launch<CNS_NORM_L2, CLIP, 32>(*g, p, dev) : launch<CNS_NORM_INF, CLIP, 32>(*g, p, dev);
-    else if (g->count <= kMostInline)
-        rc = g->norm_type == CNS_NORM_L2 ? launch<CNS_NORM_L2, CLIP, kMostInline>(*g, p, dev)
-                                         : launch<CNS_NORM_INF, CLIP, kMostInline>(*g, p, dev);
-    else
-        rc = g->norm_type == CNS_NORM_L2 ? launch<CNS_NORM_L2, CLIP, 0>(*g, p, dev) : launch<CNS_NORM_INF, CLIP, 0>(*g, p, dev);
-    if (rc)
+    // one CTA an SM, fewer when there is not a tile for each
+    
+    const int ctas = std::max(1, static_cast<int>(std::min<int64_t>(tiles, most)));
+    if (int rc = g->norm_type == CNS_NORM_L2 ? launch_sized<CNS_NORM_L2, CLIP>(*g, p, ctas)
+                                             : launch_sized<CNS_NORM_INF, CLIP>(*g, p, ctas))
         return rc;
     if (!g->sync)
         return CNS_SUCCESS;

@@ -513,7 +513,9 @@ extern "C" int cns_route(cns_route_t *r)
         CNS_CUDA(cudaStreamSynchronize(s));
         return CNS_SUCCESS;
     }
-    return syncall_read_workspace(r->workspace_dev, r->stream, nullptr, nullptr, &r->device_status);
+    if (int rc = syncall_read_workspace(r->workspace_dev, r->stream, nullptr, nullptr, &r->device_status))
+        return rc;
+    return r->device_status;
 }
 
 extern "C" int cns_route_backward(const cns_route_grad_t *g)

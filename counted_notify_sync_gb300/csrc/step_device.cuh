@@ -15,8 +15,9 @@ namespace cns {
 // Workspace header (cns_step_workspace_init zeroes it), in 32-bit words.
 constexpr uint32_t kStepEpochWord = 0;                             // line 0: calls done on this workspace
 constexpr uint32_t kStepStatusWord = CNS_SYNCALL_LINE_BYTES / 4;   // line 1: status, abort, round, CTA
-constexpr uint32_t kStepSlotWord = 512;                            // byte 2048: one 16-byte slot per CTA
-constexpr uint32_t kStepMaxCtas = (CNS_STEP_WORKSPACE_HEADER_BYTES - 2048) / 16;
+constexpr uint32_t kStepBoxWord = 2048;                            // byte 8192: the mailboxes
+constexpr uint32_t kStepMaxCtas = 160;
+static_assert(4 * kStepBoxWord + 8 * kStepMaxCtas * kStepMaxCtas == CNS_STEP_WORKSPACE_HEADER_BYTES, "header layout");
 
 constexpr unsigned kFullWarp = 0xffffffffu;
 
@@ -37,91 +38,97 @@ __device__ __forceinline__ double warp_sum(double v)
 }
 
 // ---------------------------------------------------------------------------
-// The exchange: every CTA publishes one 64-bit value, every CTA gets them all
+// The exchange: every CTA sends one 32-bit value, every CTA gets them all
 // ---------------------------------------------------------------------------
 //
 // A reduction that every CTA needs the result of is a barrier that carries a
-// value.  Each CTA stores {value, tag} to its own 16-byte slot (one 128-bit
-// access, so a tag never shows without its value) and polls all slots until
-// each shows the call's tag.  The tag is the workspace's count of calls plus
-// one: whatever grid sizes came before, no older slot carries it, and nothing
-// has to be reset.  CTA 0 advances the count once it has seen every slot --
-// every CTA had read the count by then.
+// value.  Each CTA has a row of mailboxes, one 64-bit word {tag, value} from
+// each CTA; a CTA stores its word into every row and then polls its own until
+// every box shows the call's tag.  The tag is the workspace's count of calls
+// plus one: whatever grid sizes came before, no older word carries it, and
+// nothing has to be reset.  CTA 0 advances the count once it has seen every
+// box -- every CTA had read the count by then.
 //
-// Against the soft SYNCALL barrier with the values stored beside it this saves
-// the release fence, the atomic's round trip and the values' loads behind it.
+// Nobody polls a line that another SM polls.  (With one slot per CTA that all
+// CTAs poll, 152 x 19 lines of requests met at the L2 slices of those 19
+// lines, and the exchange took 2.0-2.8 us.)  Against the soft SYNCALL barrier
+// with the values stored beside it, it saves the release fence, the atomic's
+// round trip and the loads of the values behind the barrier.
 
-struct Slot {
-    uint64_t value, tag;
-};
-
-__device__ __forceinline__ void st_slot(uint32_t *header, uint32_t cta, uint64_t value, uint64_t tag)
+__device__ __forceinline__ uint64_t ld_relaxed_gpu_u64(const uint64_t *p)
 {
-    asm volatile("{\n\t.reg .b128 q;\n\tmov.b128 q, {%1, %2};\n\tst.relaxed.gpu.global.b128 [%0], q;\n\t}" ::"l"(
-                     header + kStepSlotWord + 4 * cta),
-                 "l"(value), "l"(tag)
-                 : "memory");
+    uint64_t v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
 }
 
-__device__ __forceinline__ Slot ld_slot(const uint32_t *header, uint32_t cta)
+__device__ __forceinline__ void st_relaxed_gpu_u64(uint64_t *p, uint64_t v)
 {
-    Slot s;
-    asm volatile("{\n\t.reg .b128 q;\n\tld.relaxed.gpu.global.b128 q, [%2];\n\tmov.b128 {%0, %1}, q;\n\t}"
-                 : "=l"(s.value), "=l"(s.tag)
-                 : "l"(header + kStepSlotWord + 4 * cta)
-                 : "memory");
-    return s;
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
 
-// One warp waits for the slots of `ctas` CTAs and calls take(cta, value) for
-// each, CTA c on lane c % 32, in rising order.  The slots of a batch are all
-// in flight at once.  Bounded: true when the wait gave up (then the
-// workspace's status is CNS_ERR_TIMEOUT).
-template <class Take>
-__device__ __forceinline__ bool wait_slots(uint32_t *header, uint32_t ctas, uint64_t tag, uint64_t timeout_ns, Take take)
+__device__ __forceinline__ uint64_t *mailbox(uint32_t *header, uint32_t to, uint32_t from)
 {
-    constexpr uint32_t kBatch = 5;   // 160 CTAs: the GPU's 152 SMs in one
+    return reinterpret_cast<uint64_t *>(header + kStepBoxWord) + to * kStepMaxCtas + from;
+}
+
+// The calling warp stores its CTA's value into the rows of `ctas` CTAs.
+__device__ __forceinline__ void send_all(uint32_t *header, uint32_t ctas, uint32_t tag, uint32_t value)
+{
+    const uint64_t word = static_cast<uint64_t>(tag) << 32 | value;
+#pragma unroll
+    for (uint32_t c = 0; c < kStepMaxCtas; c += 32) {
+        const uint32_t to = c + (threadIdx.x & 31u);
+        if (to < ctas)
+            st_relaxed_gpu_u64(mailbox(header, to, blockIdx.x), word);
+    }
+}
+
+// The calling warp waits for its CTA's row: value[i] becomes the value of CTA
+// 32 i + lane (0 beyond the last).  Bounded: true when the wait gave up (then
+// the workspace's status is CNS_ERR_TIMEOUT).
+template <class T>
+__device__ __forceinline__ bool receive_all(uint32_t *header, uint32_t ctas, uint32_t tag, uint64_t timeout_ns, T *value)
+{
+    constexpr uint32_t kBatch = kStepMaxCtas / 32;
+    static_assert(sizeof(T) == 4, "values are 32-bit words");
     uint32_t *status = header + kStepStatusWord;
     const uint32_t lane = threadIdx.x & 31u;
+    const uint64_t *row = mailbox(header, blockIdx.x, lane);
     uint64_t deadline = 0;
     uint32_t spins = 0;
-    for (uint32_t first = 0; first < ctas; first += 32 * kBatch) {
-        Slot s[kBatch];
-        for (;;) {
-            bool all = true;
-#pragma unroll
-            for (uint32_t i = 0; i < kBatch; ++i) {
-                const uint32_t c = first + 32 * i + lane;
-                if (c < ctas)
-                    s[i] = ld_slot(header, c);
-            }
-#pragma unroll
-            for (uint32_t i = 0; i < kBatch; ++i)
-                all &= first + 32 * i + lane >= ctas || s[i].tag == tag;
-            if (__all_sync(kFullWarp, all))
-                break;
-            if ((++spins & 63u) == 0u) {
-                // the warp decides together, by lane 0's view
-                bool stop = false;
-                if (lane == 0) {
-                    const uint64_t now = globaltimer_ns();
-                    if (ld_relaxed_gpu(status + 1) != 0u) {
-                        stop = true;
-                    } else if (deadline == 0) {
-                        deadline = now + timeout_ns;
-                    } else if (now > deadline) {
-                        raise_timeout(status, 0u, blockIdx.x);
-                        stop = true;
-                    }
-                }
-                if (__any_sync(kFullWarp, stop))
-                    return true;
-            }
-        }
+    uint64_t s[kBatch];
+    for (;;) {
+        bool all = true;
 #pragma unroll
         for (uint32_t i = 0; i < kBatch; ++i)
-            if (first + 32 * i + lane < ctas)
-                take(first + 32 * i + lane, s[i].value);
+            s[i] = 32 * i + lane < ctas ? ld_relaxed_gpu_u64(row + 32 * i) : static_cast<uint64_t>(tag) << 32;
+#pragma unroll
+        for (uint32_t i = 0; i < kBatch; ++i)
+            all &= static_cast<uint32_t>(s[i] >> 32) == tag;
+        if (__all_sync(kFullWarp, all))
+            break;
+        if ((++spins & 63u) == 0u) {
+            bool stop = false;   // the warp decides together, by lane 0's view
+            if (lane == 0) {
+                const uint64_t now = globaltimer_ns();
+                if (ld_relaxed_gpu(status + 1) != 0u) {
+                    stop = true;
+                } else if (deadline == 0) {
+                    deadline = now + timeout_ns;
+                } else if (now > deadline) {
+                    raise_timeout(status, 0u, blockIdx.x);
+                    stop = true;
+                }
+            }
+            if (__any_sync(kFullWarp, stop))
+                return true;
+        }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kBatch; ++i) {
+        const uint32_t v = static_cast<uint32_t>(s[i]);
+        value[i] = *reinterpret_cast<const T *>(&v);
     }
     return false;
 }

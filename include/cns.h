@@ -714,7 +714,7 @@ typedef enum { CNS_DT_F32 = 0, CNS_DT_BF16 = 1, CNS_DT_F16 = 2 } cns_dtype_t;
  * one each.  A call that fails on the device (a bounded wait that ran out)
  * leaves its status, and later calls on the workspace do nothing but report
  * it, until it is initialised again. */
-#define CNS_STEP_WORKSPACE_HEADER_BYTES 8192
+#define CNS_STEP_WORKSPACE_HEADER_BYTES 212992
 #define CNS_STEP_WORKSPACE_ALIGN 128
 
 /*
@@ -842,8 +842,9 @@ typedef enum { CNS_NORM_L2 = 0, CNS_NORM_INF = 1 } cns_norm_t;
  * all elements of all tensors together; every element is then multiplied by
  * min(1, max_norm / (norm + eps)) in 32 bits and rounded once to the output's
  * type.  A norm of NaN makes the factor NaN, one of inf makes it 0.  Squares
- * are summed in 32 bits and joined in 64 (so the norm overflows where a square
- * does, above 1.8e19), in an order that depends on the sizes alone.
+ * are summed in 32 bits, a CTA's part at a time (so the norm overflows where
+ * such a part does, when gradients near 1e19 come in numbers), and the parts
+ * joined without overflow, in an order that depends on the sizes alone.
  * Tensors must not overlap, except an output with its own gradient when the
  * two are the same tensor. */
 typedef struct {
