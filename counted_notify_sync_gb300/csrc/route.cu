@@ -1,9 +1,9 @@
 // route.cu -- routing tokens to experts (cns_route) and its gradient
 // (cns_route_backward).
 //
-// One warp takes one token: lane l holds experts l * V .. l * V + V - 1 (V a
-// power of two with 32 * V >= experts), so "lower index first" is "lower lane
-// first, then lower element".
+// The entry points, and the gradient's kernel: one warp takes one token, lane l
+// holds experts l * V .. l * V + V - 1.  The routing kernel is in
+// route_kernels.cuh.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -12,47 +12,12 @@
 
 #include "cns.h"
 #include "cns_host.h"
-#include "step_device.cuh"
+#include "route_kernels.cuh"
 
 namespace cns {
 namespace {
 
 constexpr int kWarps = 8;   // tokens of a CTA at a time
-
-struct RouteParams {
-    const void *logits;
-    const float *bias;
-    int32_t *ids;
-    float *weights;
-    float *scores;
-    int32_t *offsets;
-    int32_t *order;
-    int32_t *places;
-    int64_t tokens;
-    int64_t stride;
-    int32_t experts, top_k, score, groups, top_groups, group_top, renorm;
-    float scale;
-};
-
-// Floats as integers in the same order: NaN above inf, -0 as 0, 0 for masked.
-__device__ __forceinline__ uint32_t choice_key(float v)
-{
-    v += 0.f;   // -0 and 0 are equal
-    const uint32_t u = __float_as_uint(v);
-    if (v != v)
-        return 0xffffffffu;
-    if (u == 0xff800000u)
-        return 0u;
-    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
-}
-
-__device__ __forceinline__ float warp_max(float v)
-{
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(kFullWarp, v, d));
-    return v;
-}
 
 // Scores of the warp's row: sigmoid, or softmax over the row.  A row without
 // an unmasked logit scores 0.
@@ -84,190 +49,6 @@ __device__ __forceinline__ void row_scores(const float *x, float *s, int score)
 #pragma unroll
     for (int i = 0; i < V; ++i)
         s[i] = s[i] / sum;
-}
-
-template <int D, int V>
-__global__ void __launch_bounds__(kWarps * 32) route_choose_kernel(const RouteParams p)
-{
-    using T = typename Elem<D>::type;
-    extern __shared__ float s_value[];   // [kWarps][experts], with groups
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.tokens;
-         t += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const T *row = static_cast<const T *>(p.logits) + t * p.stride;
-        float x[V], s[V];
-        uint32_t key[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            x[i] = e < p.experts ? Elem<D>::get(row[e]) : -INFINITY;
-        }
-        row_scores<V>(x, s, p.score);
-        if (p.scores) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (lane * V + i < p.experts)
-                    p.scores[t * p.experts + lane * V + i] = s[i];
-        }
-        const bool by_logit = !p.bias && p.group_top == 1;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            float v = by_logit ? x[i] : s[i];
-            if (p.bias && e < p.experts)
-                v += p.bias[e];
-            if (x[i] == -INFINITY)
-                v = -INFINITY;
-            key[i] = choice_key(v);
-            if (p.groups > 1 && e < p.experts)
-                s_value[warp * p.experts + e] = v;
-        }
-        if (p.groups > 1) {
-            __syncwarp();
-            // lane g: what group g is worth
-            const int size = p.experts / p.groups;
-            uint32_t worth = 0;
-            if (lane < p.groups) {
-                const float *v = s_value + warp * p.experts + lane * size;
-                float a = -INFINITY, b = -INFINITY;   // the two best
-                for (int i = 0; i < size; ++i) {
-                    const float c = v[i];
-                    if (choice_key(c) > choice_key(a)) {
-                        b = a;
-                        a = c;
-                    } else if (choice_key(c) > choice_key(b)) {
-                        b = c;
-                    }
-                }
-                worth = choice_key(p.group_top == 2 && b != -INFINITY ? a + b : a);
-            }
-            int before = 0;   // groups that go before this one
-            for (int g = 0; g < p.groups; ++g) {
-                const uint32_t o = __shfl_sync(kFullWarp, worth, g);
-                before += (o > worth || (o == worth && g < lane)) ? 1 : 0;
-            }
-            const uint32_t kept = __ballot_sync(kFullWarp, lane < p.groups && before < p.top_groups);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane * V + i;
-                if (e < p.experts && !((kept >> (e / size)) & 1u))
-                    key[i] = 0u;
-            }
-            __syncwarp();
-        }
-        // the top_k best; lane j keeps place j
-        int my_id = -1;
-        float my_x = -INFINITY, my_s = 0.f;
-        for (int j = 0; j < p.top_k; ++j) {
-            uint32_t best = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                best = max(best, key[i]);
-            const uint32_t top = __reduce_max_sync(kFullWarp, best);
-            if (top == 0u)
-                break;
-            const int from = __ffs(__ballot_sync(kFullWarp, best == top)) - 1;
-            int e = 0;
-            float ex = 0.f, es = 0.f;
-            if (lane == from) {
-                bool found = false;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    if (!found && key[i] == top) {
-                        found = true;
-                        key[i] = 0u;
-                        e = lane * V + i;
-                        ex = x[i];
-                        es = s[i];
-                    }
-                }
-            }
-            e = __shfl_sync(kFullWarp, e, from);
-            ex = __shfl_sync(kFullWarp, ex, from);
-            es = __shfl_sync(kFullWarp, es, from);
-            if (lane == j) {
-                my_id = e;
-                my_x = ex;
-                my_s = es;
-            }
-        }
-        float w = my_s;
-        if (p.renorm) {
-            if (p.score == CNS_SCORE_SOFTMAX)
-                row_scores<1>(&my_x, &w, CNS_SCORE_SOFTMAX);
-            else
-                w = my_s / (warp_sum(my_s) + 1e-20f);
-        }
-        if (lane < p.top_k) {
-            p.ids[t * p.top_k + lane] = my_id;
-            p.weights[t * p.top_k + lane] = my_id < 0 ? 0.f : w * p.scale;
-        }
-    }
-}
-
-// The plan, one CTA per expert: count the entries of lower experts (where
-// this expert's list starts) and its own, then place its own in order.
-__global__ void __launch_bounds__(256) route_place_kernel(const RouteParams p)
-{
-    __shared__ int s_count[8], s_lower[8];
-    const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t n = p.tokens * p.top_k;
-    int lower = 0, own = 0;
-    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
-        const int id = p.ids[i];
-        lower += id >= 0 && id < e;
-        own += id == e;
-    }
-    lower = __reduce_add_sync(kFullWarp, lower);
-    own = __reduce_add_sync(kFullWarp, own);
-    if (lane == 0) {
-        s_lower[warp] = lower;
-        s_count[warp] = own;
-    }
-    __syncthreads();
-    lower = own = 0;
-    for (int w = 0; w < 8; ++w) {
-        lower += s_lower[w];
-        own += s_count[w];
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        p.offsets[e] = lower;
-        if (e == p.experts - 1)
-            p.offsets[p.experts] = lower + own;
-    }
-    int at = lower;
-    for (int64_t first = 0; first < n; first += blockDim.x) {
-        const int64_t i = first + threadIdx.x;
-        const bool mine = i < n && p.ids[i] == e;
-        const uint32_t m = __ballot_sync(kFullWarp, mine);
-        if (lane == 0)
-            s_count[warp] = __popc(m);
-        __syncthreads();
-        int here = at, all = 0;
-        for (int w = 0; w < 8; ++w) {
-            if (w < warp)
-                here += s_count[w];
-            all += s_count[w];
-        }
-        if (mine) {
-            const int place = here + __popc(m & ((1u << lane) - 1u));
-            p.order[place] = static_cast<int32_t>(i);
-            if (p.places)
-                p.places[i] = place;
-        }
-        at += all;
-        __syncthreads();
-    }
-    if (e == p.experts - 1) {
-        // the rest of order, and the places without an expert
-        for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
-            if (i >= at)
-                p.order[i] = -1;
-            if (p.places && p.ids[i] < 0)
-                p.places[i] = -1;
-        }
-    }
 }
 
 struct RouteGradParams {
@@ -396,14 +177,6 @@ void by_width(int experts, F f)
         f.template operator()<16>();
 }
 
-template <int D> struct LaunchChoose {
-    const RouteParams &p;
-    int grid;
-    size_t smem;
-    cudaStream_t s;
-    template <int V> void operator()() { route_choose_kernel<D, V><<<grid, kWarps * 32, smem, s>>>(p); }
-};
-
 template <int D> struct LaunchBackward {
     const RouteGradParams &p;
     int grid;
@@ -411,7 +184,13 @@ template <int D> struct LaunchBackward {
     template <int V> void operator()() { route_backward_kernel<D, V><<<grid, kWarps * 32, 0, s>>>(p); }
 };
 
-size_t workspace_bytes(int64_t, int32_t, int32_t) { return CNS_STEP_WORKSPACE_HEADER_BYTES; }
+size_t workspace_bytes(int64_t, int32_t experts, int32_t)
+{
+    return CNS_STEP_WORKSPACE_HEADER_BYTES + sizeof(uint32_t) * kStepMaxCtas * static_cast<size_t>(experts);
+}
+
+// Up to this many tokens one CTA routes them all and needs no exchange.
+constexpr int64_t kOneCtaTokens = 64;
 
 bool sizes_ok(int64_t tokens, int32_t experts, int32_t top_k)
 {
@@ -488,24 +267,36 @@ extern "C" int cns_route(cns_route_t *r)
     p.stride = stride;
     p.experts = r->experts;
     p.top_k = r->top_k;
-    p.score = r->score;
+    p.softmax = r->score == CNS_SCORE_SOFTMAX;
+    p.plan = plan;
     p.groups = groups;
     p.top_groups = top_groups;
     p.group_top = r->group_top ? r->group_top : 1;
     p.renorm = r->renorm;
     p.scale = r->scale;
-    const int grid = static_cast<int>(std::min<int64_t>((r->tokens + kWarps - 1) / kWarps, dev.sm_count * 8));
-    const size_t smem = groups > 1 ? sizeof(float) * kWarps * r->experts : 0;
-    if (grid > 0) {
-        switch (r->dtype) {
-        case CNS_DT_F32: by_width(r->experts, LaunchChoose<CNS_DT_F32>{p, grid, smem, s}); break;
-        case CNS_DT_BF16: by_width(r->experts, LaunchChoose<CNS_DT_BF16>{p, grid, smem, s}); break;
-        default: by_width(r->experts, LaunchChoose<CNS_DT_F16>{p, grid, smem, s}); break;
+    p.timeout_ns = barrier_timeout_ns(r->timeout_ms);
+    p.header = static_cast<uint32_t *>(r->workspace_dev);
+    p.counts = p.header + CNS_STEP_WORKSPACE_HEADER_BYTES / 4;
+    if (r->tokens > 0 || plan) {
+        int ctas, warps;
+        if (r->tokens <= kOneCtaTokens) {
+            ctas = 1;
+            warps = static_cast<int>(std::min<int64_t>(kRouteWarps, std::max<int64_t>(r->tokens, 4)));
+        } else {
+            ctas = static_cast<int>(std::min<int64_t>((r->tokens + kRouteWarps - 1) / kRouteWarps,
+                                                      std::min<int>(dev.sm_count, kStepMaxCtas)));
+            warps = kRouteWarps;
         }
+        const cudaError_t e = r->dtype == CNS_DT_F32    ? launch_route_f32(p, ctas, warps, s)
+                              : r->dtype == CNS_DT_BF16 ? launch_route_bf16(p, ctas, warps, s)
+                                                        : launch_route_f16(p, ctas, warps, s);
+        if (e == cudaErrorCooperativeLaunchTooLarge) {
+            (void)cudaGetLastError();
+            return CNS_ERR_NOT_RESIDENT;
+        }
+        if (e != cudaSuccess)
+            return cuda_fail(e, "route launch");
     }
-    if (plan)
-        route_place_kernel<<<r->experts, 256, 0, s>>>(p);
-    CNS_CUDA(cudaGetLastError());
     if (!r->sync)
         return CNS_SUCCESS;
     r->device_status = 0;

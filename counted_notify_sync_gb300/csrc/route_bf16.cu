@@ -1,0 +1,12 @@
+// route_bf16.cu -- the routing kernel for logits of type CNS_DT_BF16.
+#define CNS_ROUTE_KERNELS
+#include "route_kernels.cuh"
+
+namespace cns {
+
+cudaError_t launch_route_bf16(const RouteParams &p, int ctas, int warps, cudaStream_t s)
+{
+    return launch_route<CNS_DT_BF16>(p, ctas, warps, s);
+}
+
+}  // namespace cns

@@ -29,11 +29,11 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ double warp_sum(double v)
+__device__ __forceinline__ float warp_max(float v)
 {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
-        v += __shfl_xor_sync(kFullWarp, v, d);
+        v = fmaxf(v, __shfl_xor_sync(kFullWarp, v, d));
     return v;
 }
 
