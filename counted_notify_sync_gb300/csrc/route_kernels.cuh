@@ -6,11 +6,24 @@
 // load of a row is coalesced whatever its alignment, and among equal choice
 // values the lower expert is the lower element, then the lower lane.
 //
-// Choice.  Each lane keeps the two best of its elements; a round takes the best
-// of the lanes' heads with one redux, and the lane that had it moves its
-// second one up.  A lane that gives a third one rescans its elements (a rare,
-// warp-uniform branch), so a round costs a dozen instructions whatever the
-// number of experts.
+// Choice.  What a token costs is instructions (ncu: 66 % of the issue slots at
+// 1970 instructions a token when every choice value was computed exactly and
+// carried beside its index), so the common path works on 32-bit keys: 23 bits
+// of value over the expert's number, the lower expert above.
+//   - 16-bit logits chosen by logit: their 16 or 19 bits, in order.  Exact.
+//   - 32-bit logits chosen by logit: their distance below the row's largest in
+//     units of 16 * 2^-23, rounded.  Rounding keeps the order or makes equals.
+//   - scores: fixed point over the range that the biases allow, from the
+//     hardware's approximate exponential and reciprocal.
+// In the last two the chosen values (and the groups') must lie further apart
+// than they may be off; a token where they do not (ties; one in a hundred at
+// random), and NaN, takes the exact path.  The weights come from the exact
+// scores of the chosen either way.
+//   The best eight of a row: each lane keeps its three best keys, the lanes'
+// first and second ones go through a sorting network (23 exchanges), and if a
+// third one belongs in, or more than eight places are asked for, the places
+// are filled in rounds, one redux each.  Four tokens' weights (eight lanes
+// each) are computed together.
 //
 // Plan.  CTA b has a stretch of tokens and each of its warps a stretch of
 // those, so that entries in order are warps in order.  Phase 1 chooses and
@@ -65,46 +78,26 @@ constexpr uint32_t kMaskedKey = 0x007fffffu;   // of -inf; what was taken has ke
 
 __device__ __forceinline__ float sigmoid_of(float x) { return 1.f / (1.f + expf(-x)); }
 
-// The two best of a lane's elements that are not in `taken`, the lower
-// element first among equals; key 0 where there is none.
-struct Heads {
-    uint32_t key1, key2;
-    int i1, i2;
-};
-
-template <int V>
-__device__ __forceinline__ Heads heads_of(const uint32_t *key, uint32_t taken)
-{
-    Heads h{0u, 0u, 0, 0};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const uint32_t k = (taken >> i) & 1u ? 0u : key[i];
-        const bool first = k > h.key1, second = k > h.key2;
-        h.i2 = first ? h.i1 : second ? i : h.i2;
-        h.key2 = first ? h.key1 : second ? k : h.key2;
-        h.i1 = first ? i : h.i1;
-        h.key1 = first ? k : h.key1;
-    }
-    return h;
-}
-
 // The choice value of a key (not NaN's payload, not 0's sign).
 __device__ __forceinline__ float value_of(uint32_t key)
 {
     return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// What a group is worth, as a key, from the keys of its best and second best.
-__device__ __forceinline__ uint32_t worth_of(uint32_t best, uint32_t second, int group_top)
+// What a group is worth, as a key, from the keys of its best and second best
+// (keys up to `masked` are of experts that cannot be chosen).
+__device__ __forceinline__ uint32_t worth_of(uint32_t best, uint32_t second, int group_top, uint32_t masked)
 {
-    return group_top == 2 && second > kMaskedKey ? choice_key(value_of(best) + value_of(second)) : best;
+    return group_top == 2 && second > masked ? choice_key(value_of(best) + value_of(second)) : best;
 }
 
-// Bit g: group g is among the top_groups worthiest.  Groups of whole elements
+// Bit g: group g is among the top_groups worthiest; *worth_of_lane: of group
+// `lane`.  Groups of whole elements
 // of the warp (32, 64, ... experts) are valued by redux; of other sizes by one
 // lane each, from shared memory.
 template <int V>
-__device__ __forceinline__ uint32_t kept_groups(const RouteParams &p, const uint32_t *key, uint32_t *s_key)
+__device__ __forceinline__ uint32_t kept_groups(const RouteParams &p, const uint32_t *key, uint32_t *s_key,
+                                                uint32_t masked, uint32_t *worth_of_lane)
 {
     const int lane = threadIdx.x & 31, size = p.experts / p.groups;
     uint32_t worth = 0u;   // of group `lane`
@@ -125,7 +118,7 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteParams &p, const uint
                                               : __reduce_max_sync(kFullWarp, one == best ? two : one);
                 }
                 if (lane == g)
-                    worth = worth_of(best, second, p.group_top);
+                    worth = worth_of(best, second, p.group_top, masked);
                 one = two = 0u;
                 in = 0;
                 ++g;
@@ -144,10 +137,11 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteParams &p, const uint
                 two = max(two, min(one, k));
                 one = max(one, k);
             }
-            worth = worth_of(one, two, p.group_top);
+            worth = worth_of(one, two, p.group_top, masked);
         }
         __syncwarp();
     }
+    *worth_of_lane = worth;
     int before = 0;   // groups that go before this one
     for (int g = 0; g < p.groups; ++g) {
         const uint32_t o = __shfl_sync(kFullWarp, worth, g);
@@ -156,129 +150,443 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteParams &p, const uint
     return __ballot_sync(kFullWarp, lane < p.groups && before < p.top_groups);
 }
 
-// Choose and weigh the experts of the tokens first .. last - 1, one after the
-// other, by the calling warp; counts each expert's in s_count if there is a plan.
+// What the fast path's keys are (see the top of the file).
+struct KeyRules {
+    uint32_t never;   // keys up to this one cannot be chosen
+    uint32_t apart;   // quanta between values that are surely in order; 0: keys are exact
+    uint32_t zero;    // the quanta of value 0 (scores)
+    float scale, offset;
+};
+
+constexpr float kNever = -1e30f;   // the value of what cannot be chosen
+constexpr float kMostBias = 1e6f;
+constexpr float kQuanta = 8388608.f;   // 2^23: a float from there to 2^24 has its integer in its low 23 bits
+
+// Scores lie in [0, 1], biases in [1 - reach, reach - 1].  A score's
+// approximation is within 1e-6 (__expf's error is a few units of 2^-23 where
+// s (1 - s) is not small), the exact score in 32 bits within 2^-22; the sums
+// round to 2^-24 of reach each.
+__device__ __forceinline__ KeyRules score_rules(float reach)
+{
+    KeyRules r;
+    r.never = 511u;
+    r.scale = (kQuanta - 64.f) / (2.f * reach - 1.f);
+    r.zero = 8u + static_cast<uint32_t>((reach - 1.f) * r.scale);
+    r.offset = kQuanta + static_cast<float>(r.zero);
+    r.apart = 3u + static_cast<uint32_t>(2.f * (2e-6f + 3e-7f * reach) * r.scale);
+    return r;
+}
+
+__device__ __forceinline__ KeyRules logit_rules()
+{
+    // the row's largest is 0, what lies 16 below it is out of reach
+    return KeyRules{511u, 1u, 0u, (kQuanta - 64.f) / 16.f, 2.f * kQuanta - 32.f};
+}
+
+__device__ __forceinline__ KeyRules packed_rules() { return KeyRules{kMaskedKey | 511u, 0u, 0u, 0.f, 0.f}; }
+
+// Whether keys a >= b are surely in this order.
+__device__ __forceinline__ bool surely_above(uint32_t a, uint32_t b, uint32_t apart)
+{
+    return (a >> 9) - (b >> 9) >= apart;
+}
+
+// Bit g: group g is among the top_groups worthiest, from the fast path's keys,
+// which are all different: one redux finds a group's best and a second one,
+// without it, the next.  *sure becomes false where the last group that is in
+// and the first that is not are too near.
+template <int V>
+__device__ __forceinline__ uint32_t kept_groups_near(const RouteParams &p, const uint32_t *key, uint32_t *s_key,
+                                                     int row_groups, const KeyRules &rules, bool *sure)
+{
+    const uint32_t lane = threadIdx.x & 31u;
+    uint32_t best = 0u, second = 0u;   // of group `lane`
+    if (row_groups) {
+        uint32_t one = 0u, two = 0u, g = 0u;
+        int in = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            two = max(two, min(one, key[i]));
+            one = max(one, key[i]);
+            if (++in == row_groups) {
+                const uint32_t top = __reduce_max_sync(kFullWarp, one);
+                best = lane == g ? top : best;
+                if (p.group_top == 2) {
+                    const uint32_t next = __reduce_max_sync(kFullWarp, one == top ? two : one);
+                    second = lane == g ? next : second;
+                }
+                one = two = 0u;
+                in = 0;
+                ++g;
+            }
+        }
+    } else {
+        const int size = p.experts / p.groups;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (32 * i + static_cast<int>(lane) < p.experts)
+                s_key[32 * i + lane] = key[i];
+        __syncwarp();
+        if (lane < static_cast<uint32_t>(p.groups)) {
+            const uint32_t *mine = s_key + lane * size;
+#pragma unroll 4
+            for (int i = 0; i < size; ++i) {
+                second = max(second, min(best, mine[i]));
+                best = max(best, mine[i]);
+            }
+        }
+        __syncwarp();
+    }
+    uint32_t worth = best;
+    if (p.group_top == 2) {   // in quanta, of two values; a masked one adds nothing
+        const uint32_t sum = best <= rules.never ? 0u : (best >> 9) + (second <= rules.never ? rules.zero : second >> 9);
+        worth = sum << 5 | (31u - lane);
+    }
+    if (lane >= static_cast<uint32_t>(p.groups))
+        worth = 0u;
+    // the worthiest, one after the other, and the one after them
+    uint32_t kept = 0u, least = 0u;
+    for (int j = 0; j < p.top_groups; ++j) {
+        least = __reduce_max_sync(kFullWarp, worth);
+        kept |= __ballot_sync(kFullWarp, worth == least);
+        worth = worth == least ? 0u : worth;
+    }
+    if (rules.apart) {
+        const uint32_t most = __reduce_max_sync(kFullWarp, worth);
+        *sure = p.group_top == 2 ? (least >> 5) - (most >> 5) >= 2u * rules.apart : surely_above(least, most, rules.apart);
+    }
+    return kept;
+}
+
+// One exchange of a sorting network: the larger value goes to the lanes that
+// have `larger`.
+__device__ __forceinline__ uint32_t exchange(uint32_t v, int distance, bool larger)
+{
+    const uint32_t o = __shfl_xor_sync(kFullWarp, v, distance);
+    return larger ? max(v, o) : min(v, o);
+}
+
+// Sort the bitonic eights of the warp (lanes 0-7, 8-15, ...), falling where `fall`.
+__device__ __forceinline__ uint32_t merge_eights(uint32_t v, bool fall)
+{
+    const uint32_t lane = threadIdx.x & 31u;
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+        v = exchange(v, d, ((lane & d) == 0) == fall);
+    return v;
+}
+
+// Sort the eights of the warp.
+__device__ __forceinline__ uint32_t sort_eights(uint32_t v, bool fall)
+{
+    const uint32_t lane = threadIdx.x & 31u;
+    v = exchange(v, 1, ((lane & 1) == 0) == ((lane & 2) == 0));
+    v = exchange(v, 2, ((lane & 2) == 0) == ((lane & 4) == 0));
+    v = exchange(v, 1, ((lane & 1) == 0) == ((lane & 4) == 0));
+    return merge_eights(v, fall);
+}
+
+// The eight largest of the lanes' `one` and `two`, falling, in each eight of
+// the warp; *rest: the largest of the others.
+__device__ __forceinline__ uint32_t best_eight(uint32_t one, uint32_t two, uint32_t *rest)
+{
+    const uint32_t lane = threadIdx.x & 31u;
+    one = sort_eights(one, true);
+    two = sort_eights(two, false);
+    uint32_t v = max(one, two), other = min(one, two);   // falling against rising: the eight larger, bitonic
+    v = merge_eights(v, (lane & 8) == 0);
+    uint32_t o = __shfl_xor_sync(kFullWarp, v, 8);
+    other = max(other, min(v, o));
+    v = merge_eights(max(v, o), (lane & 16) == 0);
+    o = __shfl_xor_sync(kFullWarp, v, 16);
+    other = max(other, min(v, o));
+    *rest = other;
+    return merge_eights(max(v, o), true);
+}
+
+// One element's exact choice value as a key.
+__device__ __forceinline__ uint32_t exact_key(const RouteParams &p, float x, float bias, float top, float sum)
+{
+    float v = x;
+    if (p.bias || p.group_top == 2) {
+        v = p.softmax ? expf(x - top) / sum : sigmoid_of(x);
+        if (p.bias)
+            v += bias;
+        v = x == -INFINITY ? -INFINITY : v;
+    }
+    return choice_key(v);
+}
+
+// The exact path: lane j gets place j's expert (-1: none).
+template <int D, int V>
+__device__ __noinline__ int choose_exact(const RouteParams &p, const typename Elem<D>::type *row, uint32_t *s_key,
+                                         float top, float sum)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = 32 * i + lane;
+        key[i] = e < p.experts ? exact_key(p, Elem<D>::get(row[e]), p.bias ? p.bias[e] : 0.f, top, sum) : 0u;
+    }
+    if (p.groups > p.top_groups) {
+        const int size = p.experts / p.groups;
+        uint32_t worth;
+        const uint32_t kept = kept_groups<V>(p, key, s_key, kMaskedKey, &worth);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (32 * i + lane < p.experts && !((kept >> ((32 * i + lane) / size)) & 1u))
+                key[i] = 0u;
+    }
+    int mine = -1;
+    for (int j = 0; j < p.top_k; ++j) {
+        uint32_t best = 0u;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            best = max(best, key[i]);
+        best = __reduce_max_sync(kFullWarp, best);
+        if (best <= kMaskedKey)
+            break;
+        uint32_t e = ~0u;   // the lowest expert that has it
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+            e = key[i] == best ? 32u * i + lane : e;
+        e = __reduce_min_sync(kFullWarp, e);
+        if (lane == j)
+            mine = static_cast<int>(e);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            key[i] = 32u * i + lane == e ? 0u : key[i];
+    }
+    return mine;
+}
+
+// The sum, or the largest, over the calling lane's `seg` lanes.
+__device__ __forceinline__ float seg_sum(float v, int seg)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        if (d < seg)
+            v += __shfl_xor_sync(kFullWarp, v, d);
+    return v;
+}
+
+__device__ __forceinline__ float seg_max(float v, int seg)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        if (d < seg)
+            v = fmaxf(v, __shfl_xor_sync(kFullWarp, v, d));
+    return v;
+}
+
+// Lanes that a token's places take when tokens are handled several at a time.
+__device__ __forceinline__ int place_lanes(const RouteParams &p) { return p.top_k <= 8 ? 8 : 32; }
+
+// Choose and weigh the experts of the tokens first .. last - 1 by the calling
+// warp; counts each expert's in s_count if there is a plan.  s_bias: of expert
+// e, 0 if there is no bias, kNever where it is -inf and beyond the last expert;
+// reach: 1 plus the largest magnitude among the others, or NaN if they are
+// nothing that the fast path is made for.
 template <int D, int V>
 __device__ __forceinline__ void choose_tokens(const RouteParams &p, int64_t first, int64_t last, const float *s_bias,
-                                              uint32_t *s_key, uint32_t *s_count)
+                                              float reach, uint32_t *s_key, uint32_t *s_count)
 {
     using T = typename Elem<D>::type;
     const int lane = threadIdx.x & 31;
     const bool by_logit = !p.bias && p.group_top == 1;
     const bool whole = p.softmax && (p.scores || !p.renorm || !by_logit);   // needs the softmax over all experts
+    const bool packs = D != CNS_DT_F32 && by_logit;
+    const KeyRules rules = packs ? packed_rules() : by_logit ? logit_rules() : score_rules(reach);
     // e / size by a product: exact for e < 512 and sizes up to 256
-    const uint32_t inverse = ((1u << 20) + p.experts / p.groups - 1u) / (p.experts / p.groups);
-    float x[V];
+    const int size = p.experts / p.groups;
+    const uint32_t inverse = ((1u << 20) + size - 1u) / size;
+    const int row_groups = size % 32 == 0 ? size / 32 : 0;   // rows of 32 experts in a group
+    const int seg = place_lanes(p), per = 32 / seg;
+    const int place = lane & (seg - 1);
     const T *row = static_cast<const T *>(p.logits) + first * p.stride;
-    auto load_row = [&](const T *from) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            x[i] = 32 * i + lane < p.experts ? Elem<D>::get(from[32 * i + lane]) : -INFINITY;
-    };
-    if (first < last)
-        load_row(row);
-    for (int64_t t = first; t < last; ++t) {
+    int held = 0;            // tokens of the batch
+    int mine = -1;           // of the lane's token, its place's expert
+    float its_top = 0.f, its_sum = 1.f;
+    for (int64_t t = first; t < last; ++t, row += p.stride) {
+        // the next row is on its way to L1 while this one's experts are chosen
+        if (t + 1 < last && lane < V)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(row + p.stride + min(32 * lane, p.experts - 1)));
+        uint32_t key[V];
+        bool sure = by_logit || (!p.softmax && reach == reach);
+        bool none = false;
         float top = 0.f, sum = 1.f;
-        if (whole) {
-            top = x[0];
-#pragma unroll
-            for (int i = 1; i < V; ++i)
-                top = fmaxf(top, x[i]);
-            top = value_of(__reduce_max_sync(kFullWarp, top == top ? choice_key(top) : 0u));
-            if (!(top > -INFINITY))
-                top = 0.f;   // every expert masked (or NaN)
-            sum = 0.f;
+        {
+            float x[V];
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                sum += expf(x[i] - top);
-            sum = warp_sum(sum);
-            if (sum == 0.f)
-                sum = 1.f;
-        }
-        uint32_t key[V];
+                x[i] = 32 * i + lane < p.experts ? Elem<D>::get(row[32 * i + lane]) : -INFINITY;
+            if (whole || (by_logit && !packs)) {
+                top = x[0];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float v = x[i];
-            if (!by_logit || p.scores) {
-                const float s = p.softmax ? expf(x[i] - top) / sum : sigmoid_of(x[i]);
-                if (p.scores && 32 * i + lane < p.experts)
-                    p.scores[t * p.experts + 32 * i + lane] = s;
-                if (!by_logit) {
-                    v = p.bias ? s + s_bias[32 * i + lane] : s;
-                    v = x[i] == -INFINITY ? -INFINITY : v;
+                for (int i = 1; i < V; ++i)
+                    top = fmaxf(top, x[i]);
+                top = value_of(__reduce_max_sync(kFullWarp, top == top ? choice_key(top) : 0u));
+                if (!(top > -INFINITY))
+                    top = 0.f;   // every expert masked (or NaN)
+            }
+            if (whole) {
+                sum = 0.f;
+                // __expf is off by a relative 2^-22 + 2^-23 |x - top|, which e^(x - top) makes small where it is large
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    sum += __expf(x[i] - top);
+                sum = warp_sum(sum);
+                if (sum == 0.f)
+                    sum = 1.f;
+            }
+            if (p.scores) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (32 * i + lane < p.experts)
+                        p.scores[t * p.experts + 32 * i + lane] =
+                            p.softmax ? expf(x[i] - top) / sum : sigmoid_of(x[i]);
+            }
+            if (packs) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    key[i] = (choice_key(x[i]) & ~511u) | (511u - (32 * i + lane));
+            } else {
+                float all = 0.f;   // NaN if any value is
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float v = x[i] - top;
+                    if (!by_logit) {
+                        float s;
+                        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + __expf(-x[i])));
+                        v = s + s_bias[32 * i + lane];
+                    }
+                    v = x[i] == -INFINITY ? kNever : v;
+                    all += v;
+                    key[i] = (__float_as_uint(fmaxf(fmaf(v, rules.scale, rules.offset), kQuanta)) << 9) |
+                             (511u - (32 * i + lane));
+                }
+                sure = sure && !__any_sync(kFullWarp, !(all == all));
+                none = __all_sync(kFullWarp, all <= 0.9f * V * kNever);   // every expert masked: a padded token
+            }
+        }
+        if (p.groups > p.top_groups && sure && !none) {
+            const uint32_t kept = kept_groups_near<V>(p, key, s_key, row_groups, rules, &sure);
+            if (row_groups) {
+                uint32_t bits = kept;
+                int in = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    key[i] = bits & 1u ? key[i] : 0u;
+                    if (++in == row_groups) {
+                        bits >>= 1;
+                        in = 0;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const uint32_t g = ((32 * i + lane) * inverse) >> 20;   // beyond the groups: never chosen
+                    key[i] = (kept >> (g & 31u)) & 1u ? key[i] : 0u;
                 }
             }
-            key[i] = choice_key(v);
         }
-        // the next row is on its way while this one's experts are chosen
-        const T *here = row;
-        row += p.stride;
-        if (t + 1 < last)
-            load_row(row);
-        if (p.groups > 1) {
-            const uint32_t kept = kept_groups<V>(p, key, s_key);
+        int chosen = -1;   // of place `place`
+        if (sure && !none) {
+            uint32_t one = 0u, two = 0u, three = 0u;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const uint32_t g = ((32 * i + lane) * inverse) >> 20;   // beyond the groups: already masked
-                key[i] = (kept >> (g & 31u)) & 1u ? key[i] : 0u;
+                const uint32_t k = key[i], a = min(one, k), b = min(two, a);
+                one = max(one, k);
+                two = max(two, a);
+                three = max(three, b);
+            }
+            // the best key that place `place` can have, and the best one after the last place
+            uint32_t got, after = 0u;
+            bool rounds = seg != 8;
+            if (!rounds) {
+                uint32_t rest;
+                got = best_eight(one, two, &rest);
+                const uint32_t third = V > 2 ? __reduce_max_sync(kFullWarp, three) : 0u;
+                const uint32_t last_one = __shfl_sync(kFullWarp, got, p.top_k - 1);
+                rounds = third > last_one;   // it belongs in
+                if (rules.apart)
+                    after = max(max(third, __reduce_max_sync(kFullWarp, rest)),
+                                p.top_k < 8 ? __shfl_sync(kFullWarp, got, p.top_k & 7) : 0u);
+            }
+            if (rounds) {
+                got = 0u;
+                for (int j = 0; j < p.top_k; ++j) {
+                    const uint32_t best = __reduce_max_sync(kFullWarp, one);
+                    if (best <= rules.never)
+                        break;
+                    got = place == j ? best : got;
+                    const bool owner = one == best;
+                    if (owner) {
+                        one = two;
+                        two = 0u;
+                    }
+                    if (V > 2 && __any_sync(kFullWarp, owner && one == 0u)) {
+                        // its second one is gone too: look again, below what it gave
+                        if (owner) {
+#pragma unroll
+                            for (int i = 0; i < V; ++i) {
+                                const uint32_t k = key[i] < best ? key[i] : 0u;
+                                two = max(two, min(one, k));
+                                one = max(one, k);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+                after = __reduce_max_sync(kFullWarp, one);
+            }
+            chosen = place < p.top_k && got > rules.never ? static_cast<int>(511u - (got & 511u)) : -1;
+            if (rules.apart) {
+                // nothing that ranks by less than it may be off, and nothing but experts
+                const uint32_t down = __shfl_down_sync(kFullWarp, got, 1);
+                const uint32_t next = place + 1 < p.top_k ? down : after;
+                sure = !__any_sync(kFullWarp, place < p.top_k && (chosen < 0 || !surely_above(got, next, rules.apart)));
             }
         }
-        // rounds; lane j keeps place j
-        int mine = -1;
-        uint32_t taken = 0u;
-        Heads h = heads_of<V>(key, 0u);
-        for (int j = 0; j < p.top_k; ++j) {
-            const uint32_t best = __reduce_max_sync(kFullWarp, h.key1);
-            if (best <= kMaskedKey)
-                break;
-            const uint32_t at = __ballot_sync(kFullWarp, h.key1 == best);
-            int e = 32 * h.i1 + lane;
-            if (at & (at - 1u)) {   // equals on several lanes: the lowest expert
-                e = static_cast<int>(__reduce_min_sync(kFullWarp, h.key1 == best ? static_cast<uint32_t>(e) : ~0u));
-            } else {
-                e = __shfl_sync(kFullWarp, e, __ffs(at) - 1);
-            }
-            if (lane == j)
-                mine = e;
-            if (lane == (e & 31)) {
-                taken |= 1u << (e >> 5);
-                h.key1 = h.key2;
-                h.i1 = h.i2;
-                h.key2 = 0u;
-            }
-            if constexpr (V > 2) {
-                // a lane whose second one is gone too has to look again
-                const bool empty = h.key1 == 0u && taken != 0u;
-                if (__any_sync(kFullWarp, empty && lane == (e & 31)))
-                    h = heads_of<V>(key, taken);
-            }
+        if (!sure) {
+            chosen = choose_exact<D, V>(p, row, s_key, top, sum);
+            chosen = __shfl_sync(kFullWarp, chosen, place);
         }
-        // weights
-        const bool there = mine >= 0;
-        const float xm = there ? Elem<D>::get(here[mine]) : -INFINITY;
+        // the lanes of the token's turn take it over
+        const bool turn = seg == 32 || (lane >> 3) == held;
+        mine = turn ? chosen : mine;
+        its_top = turn ? top : its_top;
+        its_sum = turn ? sum : its_sum;
+        if (++held < per && t + 1 < last)
+            continue;
+        // weights of the batch
+        const int64_t its = t + 1 - held + lane / seg;   // the lane's token
+        const bool token = lane / seg < held && place < p.top_k, there = token && mine >= 0;
+        const float xm =
+            there ? Elem<D>::get(static_cast<const T *>(p.logits)[its * p.stride + mine]) : -INFINITY;
         float w;
         if (p.softmax) {
             if (p.renorm) {
-                top = warp_max(xm);
-                w = there ? expf(xm - top) : 0.f;
-                w = w / warp_sum(w);
+                const float best = seg_max(xm, seg);
+                w = there ? expf(xm - best) : 0.f;
+                w = w / seg_sum(w, seg);
             } else {
-                w = expf(xm - top) / sum;
+                w = expf(xm - its_top) / its_sum;
             }
         } else {
             w = there ? sigmoid_of(xm) : 0.f;
             if (p.renorm)
-                w = w / (warp_sum(w) + 1e-20f);
+                w = w / (seg_sum(w, seg) + 1e-20f);
         }
-        if (lane < p.top_k) {
-            p.ids[t * p.top_k + lane] = mine;
-            p.weights[t * p.top_k + lane] = there ? w * p.scale : 0.f;
+        if (token) {
+            p.ids[its * p.top_k + place] = mine;
+            p.weights[its * p.top_k + place] = there ? w * p.scale : 0.f;
         }
-        if (p.plan) {
-            if (there)
-                ++s_count[mine];
-            __syncwarp();
-        }
+        if (p.plan && there)
+            atomicAdd(&s_count[mine], 1u);
+        held = 0;
+        mine = -1;
     }
 }
 
@@ -295,7 +603,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     float *s_bias = reinterpret_cast<float *>(s_sums + 4096);          // [32 V]
     uint32_t *s_keys = reinterpret_cast<uint32_t *>(s_bias) + 32 * V;  // [warps][E], groups of odd sizes
     __shared__ uint32_t s_chunk[16];
-    __shared__ int s_stop;
+    __shared__ int s_stop, s_reach;
 
     uint32_t tag = 0;
     bool stop = false;
@@ -303,18 +611,33 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
         tag = ld_relaxed_gpu(p.header + kStepEpochWord) + 1u;
         stop = ld_relaxed_gpu(p.header + kStepStatusWord + 1) != 0u;   // an earlier call failed
     }
-    if (p.bias)
-        for (int e = threadIdx.x; e < 32 * V; e += blockDim.x)
-            s_bias[e] = e < E ? p.bias[e] : -INFINITY;
+    // the warp's stretch of tokens; its first row is on its way while the CTA sets up
+    const int64_t begin = p.tokens * cta / ctas, end = p.tokens * (cta + 1) / ctas;
+    const int64_t first = begin + (end - begin) * warp / warps, last = begin + (end - begin) * (warp + 1) / warps;
+    if (first < last && lane < V) {
+        const int e = min(lane * 32, E - 1);
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const typename Elem<D>::type *>(p.logits) +
+                                                      first * p.stride + e));
+    }
+    if (threadIdx.x == 0)
+        s_reach = 0;
     if (p.plan)
         for (int i = threadIdx.x; i < warps * E; i += blockDim.x)
             s_count[i] = 0u;
     __syncthreads();
+    for (int e = threadIdx.x; e < 32 * V; e += blockDim.x) {
+        const float b = e < E && p.bias ? p.bias[e] : 0.f;
+        const bool never = e >= E || b == -INFINITY;
+        s_bias[e] = never ? kNever : b;
+        // magnitudes compare as integers, NaN above all
+        const uint32_t most = __reduce_max_sync(kFullWarp, never ? 0u : __float_as_uint(fabsf(b)));
+        if (lane == 0 && most)
+            atomicMax(&s_reach, static_cast<int>(most));
+    }
+    __syncthreads();
 
-    // the warp's stretch of tokens
-    const int64_t begin = p.tokens * cta / ctas, end = p.tokens * (cta + 1) / ctas;
-    const int64_t first = begin + (end - begin) * warp / warps, last = begin + (end - begin) * (warp + 1) / warps;
-    choose_tokens<D, V>(p, first, last, s_bias, s_keys + warp * E, s_count + warp * E);
+    const float reach = 1.f + __int_as_float(s_reach);
+    choose_tokens<D, V>(p, first, last, s_bias, reach <= kMostBias ? reach : NAN, s_keys + warp * E, s_count + warp * E);
     if (!p.plan)
         return;
 
@@ -324,10 +647,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     const bool narrow = p.tokens <= static_cast<int64_t>(ctas) * 65535;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         uint32_t run = 0u;
-        for (int w = 0; w < warps; ++w) {
-            const uint32_t c = s_count[w * E + e];
-            s_count[w * E + e] = run;
-            run += c;
+        for (int w = 0; w < warps; w += 8) {
+            uint32_t c[8];   // loaded together, before any is stored
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                c[i] = w + i < warps ? s_count[(w + i) * E + e] : 0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (w + i < warps)
+                    s_count[(w + i) * E + e] = run;
+                run += c[i];
+            }
         }
         s_base[e] = run;
         if (ctas > 1) {
@@ -362,14 +692,23 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
         const int col = threadIdx.x % wide, part = threadIdx.x / wide;
         if (col < cols && part < rows) {
             uint32_t before0 = 0, before1 = 0, total0 = 0, total1 = 0;
-#pragma unroll 4
-            for (uint32_t r = part; r < ctas; r += rows) {
-                const uint32_t c = __ldcg(p.counts + r * cols + col);
-                const uint32_t c0 = narrow ? c & 0xffffu : c, c1 = narrow ? c >> 16 : 0u;
-                total0 += c0;
-                total1 += c1;
-                before0 += r < cta ? c0 : 0u;
-                before1 += r < cta ? c1 : 0u;
+            constexpr int kBatch = 10;   // rows in flight
+            for (uint32_t r0 = part; r0 < ctas; r0 += kBatch * rows) {
+                uint32_t c[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const uint32_t r = r0 + i * rows;
+                    c[i] = r < ctas ? __ldcg(p.counts + r * cols + col) : 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const bool earlier = r0 + i * rows < cta;
+                    const uint32_t c0 = narrow ? c[i] & 0xffffu : c[i], c1 = narrow ? c[i] >> 16 : 0u;
+                    total0 += c0;
+                    total1 += c1;
+                    before0 += earlier ? c0 : 0u;
+                    before1 += earlier ? c1 : 0u;
+                }
             }
             const int e = narrow ? 2 * col : col;
             s_before[part * E + e] = before0;
@@ -431,23 +770,27 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
         listed += s_chunk[c];
     __syncthreads();
 
-    // phase 2: the same tokens in the same order
+    // phase 2: the same tokens in the same order, a batch's entries of one expert ranked by their lanes
     uint32_t *count = s_count + warp * E;
-    int id = first < last && lane < p.top_k ? p.ids[first * p.top_k + lane] : -1;
-    for (int64_t t = first; t < last; ++t) {
-        const int64_t entry = t * p.top_k + lane;
-        const int next = t + 1 < last && lane < p.top_k ? p.ids[entry + p.top_k] : -1;
-        if (lane < p.top_k) {
-            int place = -1;
-            if (id >= 0) {
-                place = static_cast<int>(s_base[id] + count[id]++);
-                p.order[place] = static_cast<int32_t>(entry);
-            }
-            if (p.places)
-                p.places[entry] = place;
-        }
+    const int seg = place_lanes(p), per = 32 / seg, place = lane & (seg - 1);
+    for (int64_t t = first + lane / seg; t - lane / seg < last; t += per) {
+        const bool token = t < last && place < p.top_k;
+        const int64_t entry = t * p.top_k + place;
+        const int id = token ? p.ids[entry] : -1;
+        const uint32_t same = __match_any_sync(kFullWarp, id);
+        int at = -1;
+        if (id >= 0)
+            at = static_cast<int>(s_base[id] + count[id] + __popc(same & ((1u << lane) - 1u)));
         __syncwarp();
-        id = next;
+        if (id >= 0 && (same >> lane) == 1u)   // the last of them
+            count[id] += __popc(same);
+        __syncwarp();
+        if (token) {
+            if (id >= 0)
+                p.order[at] = static_cast<int32_t>(entry);
+            if (p.places)
+                p.places[entry] = at;
+        }
     }
     // places that no entry takes
     const int64_t n = p.tokens * p.top_k;
