@@ -132,12 +132,22 @@ def run_pipeline(done, ack, tiles: int, tile_words: int, rounds: int, producer_s
 
 # --- device-wide steps of a training step ------------------------------------------------------------------
 
+_CODES = {}   # torch dtype -> cns_dtype_t, filled by the first new_route or new_grad_clip
+
+
+def _dtype_codes():
+    if not _CODES:
+        torch = _torch()
+        _CODES.update({torch.float32: _native.CNS_DT_F32, torch.bfloat16: _native.CNS_DT_BF16,
+                       torch.float16: _native.CNS_DT_F16})
+    return _CODES
+
+
 def _dtype_code(t):
-    torch = _torch()
-    codes = {torch.float32: _native.CNS_DT_F32, torch.bfloat16: _native.CNS_DT_BF16, torch.float16: _native.CNS_DT_F16}
-    if t.dtype not in codes:
+    code = _CODES.get(t.dtype)
+    if code is None:
         raise TypeError(f"float32, bfloat16 or float16 expected, got {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
 def new_step_workspace(nbytes: int, device=None, stream=None):
@@ -159,6 +169,7 @@ def new_route(tokens: int, experts: int, top_k: int, *, score: int = _native.CNS
       with plan: offsets [experts + 1], order [tokens * top_k], places [tokens, top_k], all int32;
       with scores: scores [tokens, experts] float32."""
     torch = _torch()
+    _dtype_codes()
     r = _native.Route()
     device = torch.device(device or "cuda")
     rc, nbytes = _native.cns_route_workspace_bytes(tokens, experts, top_k)
@@ -173,7 +184,10 @@ def new_route(tokens: int, experts: int, top_k: int, *, score: int = _native.CNS
     r.workspace = workspace
     if plan and workspace is None:
         r.workspace = new_step_workspace(nbytes, device, stream)
-    r.capacity = tokens
+    r.capacity, r.index = tokens, r.ids.get_device()
+    r.types = (torch.int32, torch.float32)
+    b = r.backward = _native.RouteGrad()   # run_route_backward's, but for the call's own tensors
+    b.experts, b.top_k, b.score, b.renorm, b.scale = experts, top_k, score, int(renorm), scale
     r.ids_dev, r.weights_dev, r.scores_dev = _native.ptr(r.ids), _native.ptr(r.weights), _native.ptr(r.scores)
     r.offsets_dev, r.order_dev, r.places_dev = _native.ptr(r.offsets), _native.ptr(r.order), _native.ptr(r.places)
     r.workspace_dev = _native.ptr(r.workspace)
@@ -185,36 +199,41 @@ def new_route(tokens: int, experts: int, top_k: int, *, score: int = _native.CNS
 
 
 def _check_logits(route, logits, what):
-    t, e = route.capacity, route.experts
-    shape, stride = logits.shape, logits.stride()
-    if not (len(shape) == 2 and shape[1] == e and shape[0] <= t and logits.device == route.ids.device and
+    """(rows, elements from row to row) of a [tokens, experts] tensor."""
+    shape, stride, e = logits.shape, logits.stride(), route.experts
+    if not (len(shape) == 2 and shape[1] == e and shape[0] <= route.capacity and logits.get_device() == route.index and
             (stride[1] == 1 or e == 1) and (shape[0] <= 1 or stride[0] >= e)):
-        raise ValueError(f"{what}: [tokens <= {t}, {e}] on {route.ids.device}, rows apart and of unit stride, expected; "
-                         f"got {tuple(shape)}, strides {stride}, on {logits.device}")
+        raise ValueError(f"{what}: [tokens <= {route.capacity}, {e}] on {route.ids.device}, rows apart and of unit stride, "
+                         f"expected; got {tuple(shape)}, strides {stride}, on {logits.device}")
+    return shape[0], stride[0] if shape[0] > 1 else 0
 
 
-def _check_rows(x, name, rows, cols, dtype, device):
-    if not (x.is_contiguous() and x.dim() == 2 and x.shape[0] >= rows and x.shape[1] == cols and x.dtype == dtype and
-            x.device == device):
-        raise ValueError(f"{name}: contiguous {dtype} [tokens, {cols}] on {device} expected")
+def _check_rows(route, x, name, rows, cols, dtype):
+    shape = x.shape
+    if not (x.is_contiguous() and len(shape) == 2 and shape[0] >= rows and shape[1] == cols and x.dtype == dtype and
+            x.get_device() == route.index):
+        raise ValueError(f"{name}: contiguous {dtype} [tokens, {cols}] on {route.ids.device} expected")
 
 
 def run_route(route, logits, bias=None, stream=None, sync: bool = False):
     """Route the rows of `logits` ([tokens, experts], float32, bfloat16 or float16, rows at any stride) on
     `stream` (None: the default stream).  Returns `route`, whose tensors hold the results: the first
     logits.shape[0] rows, and of `order` the first logits.shape[0] * top_k."""
-    _check_logits(route, logits, "logits")
-    if bias is not None:
-        if not (bias.is_contiguous() and bias.numel() == route.experts and bias.dtype == route.weights.dtype and
-                bias.device == logits.device):
+    t, route.logits_stride = _check_logits(route, logits, "logits")
+    if bias is None:
+        route.bias_dev = None
+    else:
+        if not (bias.is_contiguous() and bias.numel() == route.experts and bias.dtype == route.types[1] and
+                bias.get_device() == route.index):
             raise ValueError("bias: contiguous float32 [experts] on the logits' device expected")
+        route.bias_dev = bias.data_ptr()
     route.dtype = _dtype_code(logits)
-    route.logits_dev, route.tokens = logits.data_ptr(), logits.shape[0]
-    route.logits_stride = logits.stride(0) if logits.shape[0] > 1 else 0
-    route.bias_dev = None if bias is None else bias.data_ptr()
+    route.logits_dev, route.tokens = logits.data_ptr(), t
     route.stream = _native.stream_handle(stream)
     route.sync = 1 if sync else 0
-    _native.check(_native.cns_route(route), "cns_route")
+    rc = _native.cns_route(route)
+    if rc:
+        raise _native.CnsError(rc, "cns_route")
     return route
 
 
@@ -222,28 +241,28 @@ def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogi
     """dL/dlogits of run_route(route, logits): from dL/dweights [tokens, top_k] float32 and, if given,
     dL/dscores [tokens, experts] float32.  `ids` are the chosen experts (default: route.ids); the result goes to
     `dlogits` (default: a new tensor) in the logits' type."""
-    torch = _torch()
-    _check_logits(route, logits, "logits")
-    t = logits.shape[0]
+    g = route.backward
+    t, g.logits_stride = _check_logits(route, logits, "logits")
     ids = route.ids if ids is None else ids
     if dlogits is None:
-        dlogits = torch.empty((t, route.experts), dtype=logits.dtype, device=logits.device)
-    _check_logits(route, dlogits, "dlogits")
-    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+        dlogits = logits.new_empty((t, route.experts))
+    elif dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
         raise ValueError("dlogits: the logits' type and shape expected")
-    _check_rows(ids, "ids", t, route.top_k, torch.int32, logits.device)
-    _check_rows(dweights, "dweights", t, route.top_k, torch.float32, logits.device)
-    if dscores is not None:
-        _check_rows(dscores, "dscores", t, route.experts, torch.float32, logits.device)
-    g = _native.RouteGrad()
+    _, g.dlogits_stride = _check_logits(route, dlogits, "dlogits")
+    i32, f32 = route.types
+    _check_rows(route, ids, "ids", t, route.top_k, i32)
+    _check_rows(route, dweights, "dweights", t, route.top_k, f32)
+    if dscores is None:
+        g.dscores_dev = None
+    else:
+        _check_rows(route, dscores, "dscores", t, route.experts, f32)
+        g.dscores_dev = dscores.data_ptr()
     g.logits_dev, g.ids_dev, g.dweights_dev = logits.data_ptr(), ids.data_ptr(), dweights.data_ptr()
-    g.dscores_dev = None if dscores is None else dscores.data_ptr()
     g.dlogits_dev, g.stream = dlogits.data_ptr(), _native.stream_handle(stream)
-    g.tokens, g.experts, g.top_k = t, route.experts, route.top_k
-    g.logits_stride = logits.stride(0) if t > 1 else 0
-    g.dlogits_stride = dlogits.stride(0) if t > 1 else 0
-    g.dtype, g.score, g.renorm, g.scale = _dtype_code(logits), route.score, route.renorm, route.scale
-    _native.check(_native.cns_route_backward(g), "cns_route_backward")
+    g.tokens, g.dtype = t, _dtype_code(logits)
+    rc = _native.cns_route_backward(g)
+    if rc:
+        raise _native.CnsError(rc, "cns_route_backward")
     return dlogits
 
 
@@ -264,6 +283,7 @@ def new_grad_clip(grads, max_norm: float = float("inf"), *, outs=None, eps: floa
     tensors' addresses, so it stands for these tensors for as long as they live; make another one for others.
     `norm` is the float32 scalar that run_grad_norm and run_grad_clip fill."""
     torch = _torch()
+    _dtype_codes()
     g = _native.GradClip()
     n = len(grads)
     device = torch.device(device or (grads[0].device if n else "cuda"))
@@ -324,7 +344,9 @@ def run_grad_norm(plan, stream=None, sync: bool = False):
     """The global norm of new_grad_clip's gradients on `stream` (None: the default stream); returns plan.norm."""
     plan.stream = _native.stream_handle(stream)
     plan.sync = 1 if sync else 0
-    _native.check(_native.cns_grad_norm(plan), "cns_grad_norm")
+    rc = _native.cns_grad_norm(plan)
+    if rc:
+        raise _native.CnsError(rc, "cns_grad_norm")
     return plan.norm
 
 
@@ -333,5 +355,7 @@ def run_grad_clip(plan, stream=None, sync: bool = False):
     clipping."""
     plan.stream = _native.stream_handle(stream)
     plan.sync = 1 if sync else 0
-    _native.check(_native.cns_grad_clip(plan), "cns_grad_clip")
+    rc = _native.cns_grad_clip(plan)
+    if rc:
+        raise _native.CnsError(rc, "cns_grad_clip")
     return plan.norm

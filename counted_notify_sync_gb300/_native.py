@@ -208,6 +208,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """The loaded libcns.so, with signatures set.  Raises if it was not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

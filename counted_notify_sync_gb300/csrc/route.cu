@@ -1,8 +1,7 @@
 // route.cu -- routing tokens to experts (cns_route) and its gradient
 // (cns_route_backward).
 //
-// The entry points, and the gradient's kernel: one warp takes one token, lane l
-// holds experts l * V .. l * V + V - 1.  The routing kernel is in
+// The entry points, and the gradient's kernel.  The routing kernel is in
 // route_kernels.cuh.
 #include <cuda_runtime.h>
 
@@ -17,40 +16,6 @@
 namespace cns {
 namespace {
 
-constexpr int kWarps = 8;   // tokens of a CTA at a time
-
-// Scores of the warp's row: sigmoid, or softmax over the row.  A row without
-// an unmasked logit scores 0.
-template <int V>
-__device__ __forceinline__ void row_scores(const float *x, float *s, int score)
-{
-    if (score == CNS_SCORE_SIGMOID) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            s[i] = 1.f / (1.f + expf(-x[i]));
-        return;
-    }
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        top = fmaxf(top, x[i]);
-    top = warp_max(top);
-    if (top == -INFINITY)
-        top = 0.f;
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        s[i] = expf(x[i] - top);
-        sum += s[i];
-    }
-    sum = warp_sum(sum);
-    if (sum == 0.f)
-        sum = 1.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        s[i] = s[i] / sum;
-}
-
 struct RouteGradParams {
     const void *logits;
     const int32_t *ids;
@@ -62,127 +27,219 @@ struct RouteGradParams {
     float scale;
 };
 
-// dL/dlogits of one token per warp.  With g_j = scale * dL/dw_j at the chosen
-// experts, s the scores and S their sum over the chosen:
-//   softmax             p_e (h_e - sum_i p_i h_i), h = g at the chosen + dL/ds
-//   softmax, renorm     q_j (g_j - sum_i q_i g_i) at the chosen, q the softmax
-//                       over the chosen; and the line above for dL/ds alone
-//   sigmoid             s (1 - s) h
-//   sigmoid, renorm     the same with g_j replaced by (g_j - sum_i g_i s_i / S) / S
-template <int D, int V>
-__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const RouteGradParams p)
+constexpr int kGradWarps = 8;
+
+template <int SEG>
+__device__ __forceinline__ float lanes_sum(float v)
+{
+#pragma unroll
+    for (int d = SEG / 2; d > 0; d >>= 1)
+        v += __shfl_xor_sync(kFullWarp, v, d);
+    return v;
+}
+
+template <int SEG>
+__device__ __forceinline__ float lanes_max(float v)
+{
+#pragma unroll
+    for (int d = SEG / 2; d > 0; d >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(kFullWarp, v, d));
+    return v;
+}
+
+// W elements in a row; 16 bytes of them or more at once, or one.
+template <int D, int W>
+__device__ __forceinline__ void load_elems(const typename Elem<D>::type *a, float *v)
 {
     using T = typename Elem<D>::type;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.tokens;
-         t += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const T *row = static_cast<const T *>(p.logits) + t * p.stride;
-        T *out = static_cast<T *>(p.dlogits) + t * p.dstride;
-        int id = -1;
-        float g = 0.f, gx = -INFINITY;
-        if (lane < p.top_k) {
-            id = p.ids[t * p.top_k + lane];
-            if (id >= p.experts)
-                id = -1;
-            if (id >= 0) {
-                g = p.dweights[t * p.top_k + lane] * p.scale;
-                gx = Elem<D>::get(row[id]);
-            }
+    if constexpr (W == 1) {
+        v[0] = Elem<D>::get(*a);
+    } else {
+        constexpr int N = 16 / static_cast<int>(sizeof(T));   // of a vector
+#pragma unroll
+        for (int j = 0; j < W; j += N) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(a + j);
+            const T *e = reinterpret_cast<const T *>(&u);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[j + i] = Elem<D>::get(e[i]);
         }
-        float x[V], s[V], h[V];
-        const bool whole = p.dscores || (p.score == CNS_SCORE_SOFTMAX && !p.renorm);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            x[i] = whole && e < p.experts ? Elem<D>::get(row[e]) : -INFINITY;
-            h[i] = p.dscores && e < p.experts ? p.dscores[t * p.experts + e] : 0.f;
-        }
-        float d = 0.f;   // the chosen expert's own part
-        bool spread = false;   // g joins h before the product with the score
-        if (p.score == CNS_SCORE_SOFTMAX) {
-            if (p.renorm) {
-                float q;
-                row_scores<1>(&gx, &q, CNS_SCORE_SOFTMAX);
-                d = q * (g - warp_sum(g * q));
-            } else {
-                spread = true;
-            }
-        } else {
-            const float e = expf(-fabsf(gx)), r = 1.f / (1.f + e);   // s and 1 - s without cancellation
-            const float sc = gx >= 0.f ? r : e * r, co = gx >= 0.f ? e * r : r;
-            const float sg = id >= 0 ? sc : 0.f;
-            if (p.renorm) {
-                const float sum = warp_sum(sg) + 1e-20f;
-                g = (g - warp_sum(g * sg) / sum) / sum;
-            }
-            d = id >= 0 ? g * sg * co : 0.f;
-        }
-        if (whole) {
-            if (spread) {
-                for (int j = 0; j < p.top_k; ++j) {
-                    const int e = __shfl_sync(kFullWarp, id, j);
-                    const float v = __shfl_sync(kFullWarp, g, j);
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        h[i] += lane * V + i == e ? v : 0.f;
-                }
-            }
-            if (p.score == CNS_SCORE_SOFTMAX) {
-                row_scores<V>(x, s, CNS_SCORE_SOFTMAX);
-                float mean = 0.f;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    mean += s[i] != 0.f ? s[i] * h[i] : 0.f;
-                mean = warp_sum(mean);
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    h[i] = s[i] != 0.f ? s[i] * (h[i] - mean) : 0.f;
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float e = expf(-fabsf(x[i])), r = 1.f / (1.f + e);
-                    h[i] = h[i] * r * (e * r);
-                }
-            }
-        }
-        if (!spread) {
-            for (int j = 0; j < p.top_k; ++j) {
-                const int e = __shfl_sync(kFullWarp, id, j);
-                const float v = __shfl_sync(kFullWarp, d, j);
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    h[i] += lane * V + i == e ? v : 0.f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (lane * V + i < p.experts)
-                out[lane * V + i] = Elem<D>::put(h[i]);
     }
 }
 
-// Calls f.template operator()<V>() for the smallest V with 32 * V >= experts.
-template <class F>
-void by_width(int experts, F f)
+template <int D, int W>
+__device__ __forceinline__ void store_elems(typename Elem<D>::type *a, const float *v)
 {
-    if (experts <= 32)
-        f.template operator()<1>();
-    else if (experts <= 64)
-        f.template operator()<2>();
-    else if (experts <= 128)
-        f.template operator()<4>();
-    else if (experts <= 256)
-        f.template operator()<8>();
-    else
-        f.template operator()<16>();
+    using T = typename Elem<D>::type;
+    if constexpr (W == 1) {
+        *a = Elem<D>::put(v[0]);
+    } else {
+        static_assert(W * sizeof(T) == 16, "one vector");
+        uint4 u;
+        T *e = reinterpret_cast<T *>(&u);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            e[i] = Elem<D>::put(v[i]);
+        *reinterpret_cast<uint4 *>(a) = u;
+    }
 }
 
-template <int D> struct LaunchBackward {
-    const RouteGradParams &p;
-    int grid;
-    cudaStream_t s;
-    template <int V> void operator()() { route_backward_kernel<D, V><<<grid, kWarps * 32, 0, s>>>(p); }
-};
+// dL/dlogits.  With g_j = scale * dL/dw_j at the chosen experts, h = dL/ds, s
+// the scores and S their sum over the chosen:
+//   softmax             p_e (h_e + g_e - sum_i p_i (h_i + g_i))
+//   softmax, renorm     p_e (h_e - sum_i p_i h_i), and q_j (g_j - sum_i q_i g_i)
+//                       at the chosen, q the softmax over the chosen
+//   sigmoid             s (1 - s) (h + g)
+//   sigmoid, renorm     the same with g_j replaced by (g_j - sum_i g_i s_i / S) / S
+// So a row is what holds for experts that were not chosen (without h, and unless
+// the gradient goes through the whole softmax, 0), with the chosen ones'
+// written over it.
+//
+// Bound by the bytes of dlogits, and of logits where the whole softmax takes
+// part.  SEG lanes take a token (8 for up to 8 places, so a warp has four
+// tokens and its reductions serve them together), W elements of 16 bytes a
+// lane; each lane also has one place.  The row is read from L1 a second and a
+// third time rather than held: any number of experts, few registers, and the
+// loads of many warps in flight.
+template <int D, int W, int SEG>
+__global__ void __launch_bounds__(kGradWarps * 32) route_backward_kernel(const RouteGradParams p)
+{
+    using T = typename Elem<D>::type;
+    const int lane = threadIdx.x & 31, place = lane & (SEG - 1);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kGradWarps * 32 / SEG);
+    const int64_t begin = (static_cast<int64_t>(blockIdx.x) * kGradWarps + (threadIdx.x >> 5)) * (32 / SEG);
+    const bool softmax = p.score == CNS_SCORE_SOFTMAX;
+    const bool whole = p.dscores || (softmax && !p.renorm);
+    for (int64_t t0 = begin; t0 < p.tokens; t0 += step) {
+        const int64_t t = t0 + lane / SEG;
+        const bool token = t < p.tokens;
+        const T *row = static_cast<const T *>(p.logits) + t * p.stride;
+        const float *ds = p.dscores ? p.dscores + t * p.experts : nullptr;
+        T *out = static_cast<T *>(p.dlogits) + t * p.dstride;
+        // the lane's place
+        int id = token && place < p.top_k ? p.ids[t * p.top_k + place] : -1;
+        if (id >= p.experts)
+            id = -1;
+        const bool there = id >= 0;
+        float g = there ? p.dweights[t * p.top_k + place] * p.scale : 0.f;
+        const float x = there ? Elem<D>::get(row[id]) : -INFINITY;
+        const float h = there && ds ? ds[id] : 0.f;
+
+        // the row's softmax: top and the sum under it, and sum_i e^(x_i - top) h_i
+        float top = 0.f, sum = 1.f, mean = 0.f;
+        if (whole && softmax) {
+            top = -INFINITY;
+            if (token) {
+#pragma unroll 4
+                for (int e = place * W; e < p.experts; e += SEG * W) {
+                    float v[W];
+                    load_elems<D, W>(row + e, v);
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        top = fmaxf(top, v[i]);
+                }
+            }
+            top = lanes_max<SEG>(top);
+            if (top == -INFINITY)
+                top = 0.f;   // every expert masked
+            sum = 0.f;
+            if (token) {
+                // __expf: off by a relative 2^-22 + 2^-23 |x - top|, most where e^(x - top) is least
+#pragma unroll 4
+                for (int e = place * W; e < p.experts; e += SEG * W) {
+                    float v[W], w[W];
+                    load_elems<D, W>(row + e, v);
+                    if (ds)
+                        load_elems<CNS_DT_F32, W>(ds + e, w);
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        const float ex = __expf(v[i] - top);
+                        sum += ex;
+                        mean = ds ? fmaf(ex, w[i], mean) : mean;
+                    }
+                }
+            }
+            sum = lanes_sum<SEG>(sum);
+            if (sum == 0.f)
+                sum = 1.f;
+            mean = lanes_sum<SEG>(mean) / sum;
+        }
+
+        // the chosen ones' values
+        float d;
+        if (softmax) {
+            const float pj = whole && there ? expf(x - top) / sum : 0.f;
+            if (p.renorm) {
+                const float best = lanes_max<SEG>(x);
+                float q = there ? expf(x - best) : 0.f;
+                q = q / lanes_sum<SEG>(q);
+                const float inner = lanes_sum<SEG>(there ? q * g : 0.f);
+                d = q * (g - inner) + pj * (h - mean);
+            } else {
+                mean += lanes_sum<SEG>(pj * g);
+                d = pj * (h + g - mean);
+            }
+        } else {
+            const float ex = expf(-fabsf(x)), r = 1.f / (1.f + ex);   // s and 1 - s without cancellation
+            const float s = there ? (x >= 0.f ? r : ex * r) : 0.f, rest = x >= 0.f ? ex * r : r;
+            if (p.renorm) {
+                const float total = lanes_sum<SEG>(s) + 1e-20f;
+                g = (g - lanes_sum<SEG>(g * s) / total) / total;
+            }
+            d = s * rest * (h + g);
+        }
+
+        // the row, then the chosen ones over it
+        if (token) {
+            const float scale = 1.f / sum;
+#pragma unroll 4
+            for (int e = place * W; e < p.experts; e += SEG * W) {
+                float v[W], w[W];
+                if (whole) {
+                    load_elems<D, W>(row + e, v);
+                    if (ds)
+                        load_elems<CNS_DT_F32, W>(ds + e, w);
+                }
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    if (!whole) {
+                        v[i] = 0.f;
+                    } else if (softmax) {
+                        v[i] = __expf(v[i] - top) * scale * ((ds ? w[i] : 0.f) - mean);
+                    } else {
+                        const float ex = __expf(-fabsf(v[i])), r = 1.f / (1.f + ex);
+                        v[i] = r * (ex * r) * w[i];
+                    }
+                }
+                store_elems<D, W>(out + e, v);
+            }
+        }
+        __syncwarp();   // orders the lanes' stores to one place
+        if (there)
+            out[id] = Elem<D>::put(d);
+    }
+}
+
+template <int D>
+void launch_backward(const RouteGradParams &p, int sms, cudaStream_t s)
+{
+    using T = typename Elem<D>::type;
+    constexpr int W = 16 / static_cast<int>(sizeof(T));
+    const int per = p.top_k <= 8 ? 4 : 1;   // tokens of a warp
+    const int64_t ctas = (p.tokens + kGradWarps * per - 1) / (kGradWarps * per);
+    const int grid = static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(sms) * 8 * 16));
+    const auto whole16 = [](const void *a) { return reinterpret_cast<uintptr_t>(a) % 16 == 0; };
+    const bool wide = p.experts % W == 0 && whole16(p.logits) && whole16(p.dlogits) && whole16(p.dscores) &&
+                      p.stride % W == 0 && p.dstride % W == 0;
+    if (wide && per == 4)
+        route_backward_kernel<D, W, 8><<<grid, kGradWarps * 32, 0, s>>>(p);
+    else if (wide)
+        route_backward_kernel<D, W, 32><<<grid, kGradWarps * 32, 0, s>>>(p);
+    else if (per == 4)
+        route_backward_kernel<D, 1, 8><<<grid, kGradWarps * 32, 0, s>>>(p);
+    else
+        route_backward_kernel<D, 1, 32><<<grid, kGradWarps * 32, 0, s>>>(p);
+}
 
 size_t workspace_bytes(int64_t, int32_t experts, int32_t)
 {
@@ -348,11 +405,10 @@ extern "C" int cns_route_backward(const cns_route_grad_t *g)
     p.renorm = g->renorm;
     p.scale = g->scale;
     cudaStream_t s = to_stream(g->stream);
-    const int grid = static_cast<int>(std::min<int64_t>((g->tokens + kWarps - 1) / kWarps, dev.sm_count * 8));
     switch (g->dtype) {
-    case CNS_DT_F32: by_width(g->experts, LaunchBackward<CNS_DT_F32>{p, grid, s}); break;
-    case CNS_DT_BF16: by_width(g->experts, LaunchBackward<CNS_DT_BF16>{p, grid, s}); break;
-    default: by_width(g->experts, LaunchBackward<CNS_DT_F16>{p, grid, s}); break;
+    case CNS_DT_F32: launch_backward<CNS_DT_F32>(p, dev.sm_count, s); break;
+    case CNS_DT_BF16: launch_backward<CNS_DT_BF16>(p, dev.sm_count, s); break;
+    default: launch_backward<CNS_DT_F16>(p, dev.sm_count, s); break;
     }
     CNS_CUDA(cudaGetLastError());
     return CNS_SUCCESS;

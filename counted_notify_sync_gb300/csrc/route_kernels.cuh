@@ -509,7 +509,7 @@ __device__ __forceinline__ void choose_tokens(const RouteParams &p, int64_t firs
                 got = best_eight(one, two, &rest);
                 const uint32_t third = V > 2 ? __reduce_max_sync(kFullWarp, three) : 0u;
                 const uint32_t last_one = __shfl_sync(kFullWarp, got, p.top_k - 1);
-                rounds = third > last_one;   // it belongs in
+                rounds = V > 2 && third > last_one;   // it belongs in
                 if (rules.apart)
                     after = max(max(third, __reduce_max_sync(kFullWarp, rest)),
                                 p.top_k < 8 ? __shfl_sync(kFullWarp, got, p.top_k & 7) : 0u);

@@ -800,7 +800,8 @@ int cns_route(cns_route_t *r);
 /* The gradient of a routing with respect to its logits, the chosen experts
  * held fixed: from dL/dweights, and optionally dL/dscores for losses on the
  * scores (a load-balancing loss).  Experts that no gradient reaches get 0; a
- * place whose id is outside 0 .. experts - 1 (-1) contributes nothing. */
+ * place whose id is outside 0 .. experts - 1 (-1) contributes nothing; a
+ * token's other ids are all different, as the forward call leaves them. */
 typedef struct {
     const void *logits_dev;    /* (in) as in the forward call */
     const int32_t *ids_dev;    /* (in) [tokens][top_k], the forward call's */
