@@ -76,6 +76,14 @@ __device__ __forceinline__ uint32_t choice_key(float v)
 }
 constexpr uint32_t kMaskedKey = 0x007fffffu;   // of -inf; what was taken has key 0
 
+// e^x for the near path and for sums: off by a relative 2^-22 + 2^-23 |x|; tiny results are 0.
+__device__ __forceinline__ float exp_near(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+
 __device__ __forceinline__ float sigmoid_of(float x) { return 1.f / (1.f + expf(-x)); }
 
 // The choice value of a key (not NaN's payload, not 0's sign).
@@ -163,7 +171,7 @@ constexpr float kMostBias = 1e6f;
 constexpr float kQuanta = 8388608.f;   // 2^23: a float from there to 2^24 has its integer in its low 23 bits
 
 // Scores lie in [0, 1], biases in [1 - reach, reach - 1].  A score's
-// approximation is within 1e-6 (__expf's error is a few units of 2^-23 where
+// approximation is within 1e-6 (exp_near is off by a few units of 2^-23 where
 // s (1 - s) is not small), the exact score in 32 bits within 2^-22; the sums
 // round to 2^-24 of reach each.
 __device__ __forceinline__ KeyRules score_rules(float reach)
@@ -201,40 +209,42 @@ __device__ __forceinline__ uint32_t kept_groups_near(const RouteParams &p, const
 {
     const uint32_t lane = threadIdx.x & 31u;
     uint32_t best = 0u, second = 0u;   // of group `lane`
-    if (row_groups) {
-        uint32_t one = 0u, two = 0u, g = 0u;
-        int in = 0;
+    if (row_groups == 1) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            two = max(two, min(one, key[i]));
-            one = max(one, key[i]);
-            if (++in == row_groups) {
-                const uint32_t top = __reduce_max_sync(kFullWarp, one);
-                best = lane == g ? top : best;
-                if (p.group_top == 2) {
-                    const uint32_t next = __reduce_max_sync(kFullWarp, one == top ? two : one);
-                    second = lane == g ? next : second;
-                }
-                one = two = 0u;
-                in = 0;
-                ++g;
+            const uint32_t top = __reduce_max_sync(kFullWarp, key[i]);
+            best = lane == i ? top : best;
+            if (p.group_top == 2) {
+                const uint32_t next = __reduce_max_sync(kFullWarp, key[i] == top ? 0u : key[i]);
+                second = lane == i ? next : second;
             }
         }
     } else {
+        // some lanes a group, from shared memory
         const int size = p.experts / p.groups;
+        const int lanes = p.groups > 16 ? 1 : p.groups > 8 ? 2 : p.groups > 4 ? 4 : 8;
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (32 * i + static_cast<int>(lane) < p.experts)
                 s_key[32 * i + lane] = key[i];
         __syncwarp();
-        if (lane < static_cast<uint32_t>(p.groups)) {
-            const uint32_t *mine = s_key + lane * size;
+        const int g = lane / lanes;
+        if (g < p.groups) {
+            const uint32_t *mine = s_key + g * size;
 #pragma unroll 4
-            for (int i = 0; i < size; ++i) {
+            for (int i = lane & (lanes - 1); i < size; i += lanes) {
                 second = max(second, min(best, mine[i]));
                 best = max(best, mine[i]);
             }
         }
+        for (int d = 1; d < lanes; d <<= 1) {
+            const uint32_t b = __shfl_xor_sync(kFullWarp, best, d), c = __shfl_xor_sync(kFullWarp, second, d);
+            second = max(min(best, b), max(second, c));
+            best = max(best, b);
+        }
+        // group g's from its first lane to lane g
+        best = __shfl_sync(kFullWarp, best, (lane * lanes) & 31);
+        second = __shfl_sync(kFullWarp, second, (lane * lanes) & 31);
         __syncwarp();
     }
     uint32_t worth = best;
@@ -388,8 +398,10 @@ __device__ __forceinline__ int place_lanes(const RouteParams &p) { return p.top_
 // e, 0 if there is no bias, kNever where it is -inf and beyond the last expert;
 // reach: 1 plus the largest magnitude among the others, or NaN if they are
 // nothing that the fast path is made for.
+// Returns the last batch's expert of the lane's place: of all tokens, if they
+// are one batch.
 template <int D, int V>
-__device__ __forceinline__ void choose_tokens(const RouteParams &p, int64_t first, int64_t last, const float *s_bias,
+__device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first, int64_t last, const float *s_bias,
                                               float reach, uint32_t *s_key, uint32_t *s_count)
 {
     using T = typename Elem<D>::type;
@@ -405,8 +417,8 @@ __device__ __forceinline__ void choose_tokens(const RouteParams &p, int64_t firs
     const int seg = place_lanes(p), per = 32 / seg;
     const int place = lane & (seg - 1);
     const T *row = static_cast<const T *>(p.logits) + first * p.stride;
-    int held = 0;            // tokens of the batch
-    int mine = -1;           // of the lane's token, its place's expert
+    int held = 0;                // tokens of the batch
+    int mine = -1, done = -1;    // of the lane's token, its place's expert
     float its_top = 0.f, its_sum = 1.f;
     for (int64_t t = first; t < last; ++t, row += p.stride) {
         // the next row is on its way to L1 while this one's experts are chosen
@@ -432,10 +444,10 @@ __device__ __forceinline__ void choose_tokens(const RouteParams &p, int64_t firs
             }
             if (whole) {
                 sum = 0.f;
-                // __expf is off by a relative 2^-22 + 2^-23 |x - top|, which e^(x - top) makes small where it is large
+                // off the most where e^(x - top) is the least
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    sum += __expf(x[i] - top);
+                    sum += exp_near(x[i] - top);
                 sum = warp_sum(sum);
                 if (sum == 0.f)
                     sum = 1.f;
@@ -458,7 +470,7 @@ __device__ __forceinline__ void choose_tokens(const RouteParams &p, int64_t firs
                     float v = x[i] - top;
                     if (!by_logit) {
                         float s;
-                        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + __expf(-x[i])));
+                        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + exp_near(-x[i])));
                         v = s + s_bias[32 * i + lane];
                     }
                     v = x[i] == -INFINITY ? kNever : v;
@@ -586,8 +598,10 @@ __device__ __forceinline__ void choose_tokens(const RouteParams &p, int64_t firs
         if (p.plan && there)
             atomicAdd(&s_count[mine], 1u);
         held = 0;
+        done = token ? mine : -1;
         mine = -1;
     }
+    return done;
 }
 
 template <int D, int V>
@@ -601,7 +615,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     uint32_t *s_base = s_count + (p.plan ? warps * E : 0);             // [E]
     uint32_t *s_sums = s_base + E;                                     // [2][rows at a time][E], up to 4096
     float *s_bias = reinterpret_cast<float *>(s_sums + 4096);          // [32 V]
-    uint32_t *s_keys = reinterpret_cast<uint32_t *>(s_bias) + 32 * V;  // [warps][E], groups of odd sizes
+    uint32_t *s_keys = reinterpret_cast<uint32_t *>(s_bias) + 32 * V;  // [warps][E], groups of other sizes than 32
     __shared__ uint32_t s_chunk[16];
     __shared__ int s_stop, s_reach;
 
@@ -611,7 +625,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
         tag = ld_relaxed_gpu(p.header + kStepEpochWord) + 1u;
         stop = ld_relaxed_gpu(p.header + kStepStatusWord + 1) != 0u;   // an earlier call failed
     }
-    // the warp's stretch of tokens; its first row is on its way while the CTA sets up
+    // the warp's stretch of tokens; its first row and the biases are on their way while the CTA sets up
     const int64_t begin = p.tokens * cta / ctas, end = p.tokens * (cta + 1) / ctas;
     const int64_t first = begin + (end - begin) * warp / warps, last = begin + (end - begin) * (warp + 1) / warps;
     if (first < last && lane < V) {
@@ -619,25 +633,30 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
         asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const typename Elem<D>::type *>(p.logits) +
                                                       first * p.stride + e));
     }
+    const bool scores = p.bias || p.group_top == 2;   // chosen by score
+    float b = p.bias && static_cast<int>(threadIdx.x) < E ? p.bias[threadIdx.x] : 0.f;
     if (threadIdx.x == 0)
         s_reach = 0;
     if (p.plan)
         for (int i = threadIdx.x; i < warps * E; i += blockDim.x)
             s_count[i] = 0u;
     __syncthreads();
-    for (int e = threadIdx.x; e < 32 * V; e += blockDim.x) {
-        const float b = e < E && p.bias ? p.bias[e] : 0.f;
-        const bool never = e >= E || b == -INFINITY;
-        s_bias[e] = never ? kNever : b;
-        // magnitudes compare as integers, NaN above all
-        const uint32_t most = __reduce_max_sync(kFullWarp, never ? 0u : __float_as_uint(fabsf(b)));
-        if (lane == 0 && most)
-            atomicMax(&s_reach, static_cast<int>(most));
+    if (scores) {
+        for (int e = threadIdx.x; e < 32 * V; e += blockDim.x) {
+            if (e >= static_cast<int>(blockDim.x))
+                b = p.bias && e < E ? p.bias[e] : 0.f;
+            const bool never = e >= E || b == -INFINITY;
+            s_bias[e] = never ? kNever : b;
+            // magnitudes compare as integers, NaN above all
+            const uint32_t most = __reduce_max_sync(kFullWarp, never ? 0u : __float_as_uint(fabsf(b)));
+            if (lane == 0 && most)
+                atomicMax(&s_reach, static_cast<int>(most));
+        }
+        __syncthreads();
     }
-    __syncthreads();
 
     const float reach = 1.f + __int_as_float(s_reach);
-    choose_tokens<D, V>(p, first, last, s_bias, reach <= kMostBias ? reach : NAN, s_keys + warp * E, s_count + warp * E);
+    const int done = choose_tokens<D, V>(p, first, last, s_bias, reach <= kMostBias ? reach : NAN, s_keys + warp * E, s_count + warp * E);
     if (!p.plan)
         return;
 
@@ -692,7 +711,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
         const int col = threadIdx.x % wide, part = threadIdx.x / wide;
         if (col < cols && part < rows) {
             uint32_t before0 = 0, before1 = 0, total0 = 0, total1 = 0;
-            constexpr int kBatch = 10;   // rows in flight
+            constexpr int kBatch = 20;   // rows in flight: 152 CTAs' in one for up to 256 experts
             for (uint32_t r0 = part; r0 < ctas; r0 += kBatch * rows) {
                 uint32_t c[kBatch];
 #pragma unroll
@@ -776,7 +795,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     for (int64_t t = first + lane / seg; t - lane / seg < last; t += per) {
         const bool token = t < last && place < p.top_k;
         const int64_t entry = t * p.top_k + place;
-        const int id = token ? p.ids[entry] : -1;
+        const int id = last - first <= per ? done : token ? p.ids[entry] : -1;
         const uint32_t same = __match_any_sync(kFullWarp, id);
         int at = -1;
         if (id >= 0)
@@ -801,7 +820,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
 
 inline size_t route_smem(const RouteParams &p, int V, int warps)
 {
-    const bool odd_groups = p.groups > 1 && p.experts / p.groups % 32 != 0;
+    const bool odd_groups = p.groups > 1 && p.experts / p.groups != 32;
     return sizeof(uint32_t) * ((p.plan ? warps * p.experts : 0) + p.experts + 4096 + 32 * V +
                                (odd_groups ? warps * p.experts : 0));
 }
