@@ -170,10 +170,11 @@ constexpr float kNever = -1e30f;   // the value of what cannot be chosen
 constexpr float kMostBias = 1e6f;
 constexpr float kQuanta = 8388608.f;   // 2^23: a float from there to 2^24 has its integer in its low 23 bits
 
-// Scores lie in [0, 1], biases in [1 - reach, reach - 1].  A score's
-// approximation is within 1e-6 (exp_near is off by a few units of 2^-23 where
-// s (1 - s) is not small), the exact score in 32 bits within 2^-22; the sums
-// round to 2^-24 of reach each.
+// Scores lie in [0, 1], biases in [1 - reach, reach - 1].  The approximate
+// score's error is s (1 - s) (2^-22 + 2^-23.4 |x|) from the exponential, and
+// (2^-24 + 2^-23) s from the sum and the reciprocal: below 2.7e-7.  The exact
+// score in 32 bits is within 1.8e-7 of the true one, and the sums with the bias
+// round to 2^-24 of reach each.  Two values, and the quanta round too.
 __device__ __forceinline__ KeyRules score_rules(float reach)
 {
     KeyRules r;
@@ -181,7 +182,7 @@ __device__ __forceinline__ KeyRules score_rules(float reach)
     r.scale = (kQuanta - 64.f) / (2.f * reach - 1.f);
     r.zero = 8u + static_cast<uint32_t>((reach - 1.f) * r.scale);
     r.offset = kQuanta + static_cast<float>(r.zero);
-    r.apart = 3u + static_cast<uint32_t>(2.f * (2e-6f + 3e-7f * reach) * r.scale);
+    r.apart = 3u + static_cast<uint32_t>(2.f * (4.5e-7f + 1.3e-7f * reach) * r.scale);
     return r;
 }
 
@@ -371,6 +372,28 @@ __device__ __noinline__ int choose_exact(const RouteParams &p, const typename El
     return mine;
 }
 
+// The chosen experts of `row` in the order of their exact choice values: lane
+// `place` of each `seg` lanes has place `place`'s.  Not for softmax by score.
+template <int D>
+__device__ __noinline__ int in_exact_order(const RouteParams &p, const typename Elem<D>::type *row, int chosen, int seg)
+{
+    const int place = threadIdx.x & (seg - 1);
+    const uint32_t key =
+        chosen >= 0 ? exact_key(p, Elem<D>::get(row[chosen]), p.bias ? p.bias[chosen] : 0.f, 0.f, 1.f) : 0u;
+    int before = 0;
+    for (int j = 0; j < p.top_k; ++j) {
+        const uint32_t k = __shfl_sync(kFullWarp, key, j);
+        const int e = __shfl_sync(kFullWarp, chosen, j);
+        before += (k > key || (k == key && e < chosen)) ? 1 : 0;
+    }
+    int ordered = -1;
+    for (int j = 0; j < p.top_k; ++j) {
+        const int at = __shfl_sync(kFullWarp, before, j), e = __shfl_sync(kFullWarp, chosen, j);
+        ordered = at == place ? e : ordered;
+    }
+    return place < p.top_k ? ordered : -1;
+}
+
 // The sum, or the largest, over the calling lane's `seg` lanes.
 __device__ __forceinline__ float seg_sum(float v, int seg)
 {
@@ -558,7 +581,11 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
                 // nothing that ranks by less than it may be off, and nothing but experts
                 const uint32_t down = __shfl_down_sync(kFullWarp, got, 1);
                 const uint32_t next = place + 1 < p.top_k ? down : after;
-                sure = !__any_sync(kFullWarp, place < p.top_k && (chosen < 0 || !surely_above(got, next, rules.apart)));
+                const bool near = place < p.top_k && !surely_above(got, next, rules.apart);
+                sure = !__any_sync(kFullWarp, place < p.top_k && (chosen < 0 || (near && place == p.top_k - 1)));
+                // the right ones, but some too near to be sure of their order: by their exact values
+                if (sure && __any_sync(kFullWarp, near))
+                    chosen = in_exact_order<D>(p, row, chosen, seg);
             }
         }
         if (!sure) {
@@ -613,16 +640,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     const uint32_t cta = blockIdx.x, ctas = gridDim.x;
     uint32_t *s_count = smem;                                          // [warps][E]
     uint32_t *s_base = s_count + (p.plan ? warps * E : 0);             // [E]
-    uint32_t *s_sums = s_base + E;                                     // [2][rows at a time][E], up to 4096
-    float *s_bias = reinterpret_cast<float *>(s_sums + 4096);          // [32 V]
+    uint32_t *s_total = s_base + E;                                     // [E]
+    float *s_bias = reinterpret_cast<float *>(s_total + E);             // [32 V]
     uint32_t *s_keys = reinterpret_cast<uint32_t *>(s_bias) + 32 * V;  // [warps][E], groups of other sizes than 32
     __shared__ uint32_t s_chunk[16];
     __shared__ int s_stop, s_reach;
 
-    uint32_t tag = 0;
+    uint32_t tag = 0, turn = 0;
     bool stop = false;
-    if (p.plan && warp == 0) {
+    if (p.plan) {
         tag = ld_relaxed_gpu(p.header + kStepEpochWord) + 1u;
+        turn = ld_relaxed_gpu(p.header + kStepRouteWord) + 1u;
         stop = ld_relaxed_gpu(p.header + kStepStatusWord + 1) != 0u;   // an earlier call failed
     }
     // the warp's stretch of tokens; its first row and the biases are on their way while the CTA sets up
@@ -660,10 +688,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     if (!p.plan)
         return;
 
-    // counts of the CTA's warps become the counts before each warp; the CTA's own go to the other CTAs, in
-    // 16 bits where no CTA has more tokens than that
+    // Counts of the CTA's warps become the counts before each warp.  The CTA's own go to its row and are added
+    // to its block's (16 CTAs), so that nobody has to read the rows of all CTAs: 152 rows by 152 CTAs took 2.5 us.
+    // The blocks' sums are kept twice; a call uses one, and clears the other for the next call.
     __syncthreads();
-    const bool narrow = p.tokens <= static_cast<int64_t>(ctas) * 65535;
+    uint32_t *sums = p.header + kStepSumWord + (turn & 1u) * kStepSumWords;
+    uint32_t *stale = p.header + kStepSumWord + ((turn & 1u) ^ 1u) * kStepSumWords;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         uint32_t run = 0u;
         for (int w = 0; w < warps; w += 8) {
@@ -679,16 +709,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
             }
         }
         s_base[e] = run;
-        if (ctas > 1) {
-            if (narrow)
-                reinterpret_cast<uint16_t *>(p.counts)[cta * (E + (E & 1)) + e] = static_cast<uint16_t>(run);
-            else
-                p.counts[cta * E + e] = run;
+        if (ctas > 1 && !stop) {
+            p.counts[cta * E + e] = run;
+            if (run)
+                red_add_relaxed_gpu(sums + cta / kStepBlockCtas * CNS_ROUTE_MAX_EXPERTS + e, run);
         }
     }
-    const int cols = narrow ? (E + 1) / 2 : E, wide = (cols + 31) / 32 * 32;
-    const int rows = ctas > 1 ? max(static_cast<int>(blockDim.x) / wide, 1) : 1;   // summed at a time
-    uint32_t *s_before = s_sums, *s_total = s_sums + rows * E;
     if (ctas > 1) {
         __syncthreads();
         if (warp == 0) {
@@ -698,66 +724,47 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
                 uint32_t none[kStepMaxCtas / 32];
                 stop = receive_all(p.header, ctas, tag, p.timeout_ns, none);
                 fence_acquire_gpu();
-                if (!stop && cta == 0 && lane == 0)
+                if (!stop && cta == 0 && lane == 0) {
                     st_relaxed_gpu(p.header + kStepEpochWord, tag);
+                    st_relaxed_gpu(p.header + kStepRouteWord, turn);
+                }
             }
             if (lane == 0)
                 s_stop = stop;
         }
-        __syncthreads();
-        if (s_stop)
-            return;
-        // sum the rows of all CTAs, and of those before this one: some columns and rows a thread
-        const int col = threadIdx.x % wide, part = threadIdx.x / wide;
-        if (col < cols && part < rows) {
-            uint32_t before0 = 0, before1 = 0, total0 = 0, total1 = 0;
-            constexpr int kBatch = 20;   // rows in flight: 152 CTAs' in one for up to 256 experts
-            for (uint32_t r0 = part; r0 < ctas; r0 += kBatch * rows) {
-                uint32_t c[kBatch];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const uint32_t r = r0 + i * rows;
-                    c[i] = r < ctas ? __ldcg(p.counts + r * cols + col) : 0u;
-                }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const bool earlier = r0 + i * rows < cta;
-                    const uint32_t c0 = narrow ? c[i] & 0xffffu : c[i], c1 = narrow ? c[i] >> 16 : 0u;
-                    total0 += c0;
-                    total1 += c1;
-                    before0 += earlier ? c0 : 0u;
-                    before1 += earlier ? c1 : 0u;
-                }
-            }
-            const int e = narrow ? 2 * col : col;
-            s_before[part * E + e] = before0;
-            s_total[part * E + e] = total0;
-            if (narrow && e + 1 < E) {
-                s_before[part * E + e + 1] = before1;
-                s_total[part * E + e + 1] = total1;
-            }
-        }
-        __syncthreads();
-    } else {
-        if (warp == 0 && lane == 0)
-            s_stop = stop;
-        for (int e = threadIdx.x; e < E; e += blockDim.x) {
-            s_before[e] = 0u;
-            s_total[e] = s_base[e];
-        }
-        __syncthreads();
-        if (s_stop)
-            return;
+    } else if (threadIdx.x == 0) {
+        s_stop = stop;
     }
-    // where each expert's list starts: a scan over the experts, 32 to a warp
-    for (int c = warp; c * 32 < E; c += warps) {
-        const int e = c * 32 + lane;
+    __syncthreads();
+    if (s_stop)
+        return;
+    if (ctas > 1)
+        for (uint32_t i = cta * blockDim.x + threadIdx.x; i < kStepSumWords; i += ctas * blockDim.x)
+            stale[i] = 0u;
+    // One thread an expert: the entries of earlier CTAs and of all; where its list starts, by a scan over the
+    // experts, 32 to a warp.
+    for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+        const int e = e0 + threadIdx.x;
         uint32_t before = 0, total = 0;
-        if (e < E) {
-            for (int r = 0; r < rows; ++r) {
-                before += s_before[r * E + e];
-                total += s_total[r * E + e];
+        if (e < E && ctas > 1) {
+            const uint32_t block = cta / kStepBlockCtas;
+            uint32_t c[kStepMaxCtas / kStepBlockCtas], r[kStepBlockCtas];
+#pragma unroll
+            for (uint32_t i = 0; i < kStepMaxCtas / kStepBlockCtas; ++i)
+                c[i] = i * kStepBlockCtas < ctas ? __ldcg(sums + i * CNS_ROUTE_MAX_EXPERTS + e) : 0u;
+#pragma unroll
+            for (uint32_t i = 0; i < kStepBlockCtas; ++i)
+                r[i] = block * kStepBlockCtas + i < cta ? __ldcg(p.counts + (block * kStepBlockCtas + i) * E + e) : 0u;
+#pragma unroll
+            for (uint32_t i = 0; i < kStepMaxCtas / kStepBlockCtas; ++i) {
+                total += c[i];
+                before += i < block ? c[i] : 0u;
             }
+#pragma unroll
+            for (uint32_t i = 0; i < kStepBlockCtas; ++i)
+                before += r[i];
+        } else if (e < E) {
+            total = s_base[e];
         }
         uint32_t run = total;
 #pragma unroll
@@ -765,14 +772,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
             const uint32_t o = __shfl_up_sync(kFullWarp, run, d);
             run += lane >= d ? o : 0u;
         }
-        if (lane == 31)
-            s_chunk[c] = run;
+        if (lane == 31 && e - lane < E)
+            s_chunk[e / 32] = run;
         if (e < E) {
             s_base[e] = run - total + before;
-            s_total[e] = run;   // row 0: read only by this lane
+            s_total[e] = run;
         }
     }
     __syncthreads();
+    uint32_t listed = 0;
+    for (int c = 0; c * 32 < E; ++c)
+        listed += s_chunk[c];
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         uint32_t earlier = 0;
         for (int c = 0; c < e / 32; ++c)
@@ -784,9 +794,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
             p.offsets[e + 1] = static_cast<int32_t>(earlier + s_total[e]);
         }
     }
-    uint32_t listed = 0;
-    for (int c = 0; c * 32 < E; ++c)
-        listed += s_chunk[c];
     __syncthreads();
 
     // phase 2: the same tokens in the same order, a batch's entries of one expert ranked by their lanes
@@ -821,7 +828,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
 inline size_t route_smem(const RouteParams &p, int V, int warps)
 {
     const bool odd_groups = p.groups > 1 && p.experts / p.groups != 32;
-    return sizeof(uint32_t) * ((p.plan ? warps * p.experts : 0) + p.experts + 4096 + 32 * V +
+    return sizeof(uint32_t) * ((p.plan ? warps * p.experts : 0) + 2 * p.experts + 32 * V +
                                (odd_groups ? warps * p.experts : 0));
 }
 

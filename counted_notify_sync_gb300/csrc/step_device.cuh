@@ -14,10 +14,14 @@ namespace cns {
 
 // Workspace header (cns_step_workspace_init zeroes it), in 32-bit words.
 constexpr uint32_t kStepEpochWord = 0;                             // line 0: calls done on this workspace
+constexpr uint32_t kStepRouteWord = 1;                             // of them, routings
 constexpr uint32_t kStepStatusWord = CNS_SYNCALL_LINE_BYTES / 4;   // line 1: status, abort, round, CTA
 constexpr uint32_t kStepBoxWord = 2048;                            // byte 8192: the mailboxes
 constexpr uint32_t kStepMaxCtas = 160;
-static_assert(4 * kStepBoxWord + 8 * kStepMaxCtas * kStepMaxCtas == CNS_STEP_WORKSPACE_HEADER_BYTES, "header layout");
+constexpr uint32_t kStepBlockCtas = 16;                            // CTAs whose counts are summed together
+constexpr uint32_t kStepSumWord = kStepBoxWord + 2 * kStepMaxCtas * kStepMaxCtas;   // [2][blocks][experts] of route.cu
+constexpr uint32_t kStepSumWords = kStepMaxCtas / kStepBlockCtas * CNS_ROUTE_MAX_EXPERTS;
+static_assert(4 * (kStepSumWord + 2 * kStepSumWords) == CNS_STEP_WORKSPACE_HEADER_BYTES, "header layout");
 
 constexpr unsigned kFullWarp = 0xffffffffu;
 

@@ -714,7 +714,7 @@ typedef enum { CNS_DT_F32 = 0, CNS_DT_BF16 = 1, CNS_DT_F16 = 2 } cns_dtype_t;
  * one each.  A call that fails on the device (a bounded wait that ran out)
  * leaves its status and incomplete outputs, and so do later calls on the
  * workspace until it is initialised again. */
-#define CNS_STEP_WORKSPACE_HEADER_BYTES 212992
+#define CNS_STEP_WORKSPACE_HEADER_BYTES 253952
 #define CNS_STEP_WORKSPACE_ALIGN 128
 
 /*

@@ -257,6 +257,24 @@ def test_streams_graphs_and_shared_workspaces(cns):
         assert np.array_equal(r.order.cpu().numpy(), order) and np.array_equal(r.places.cpu().numpy(), places)
 
 
+def test_a_workspace_shared_with_clipping(cns):
+    """Routings and clippings in turn on one workspace: each leaves it as the other needs it."""
+    import torch
+    ws = cns.new_step_workspace(max(cns.cns_route_workspace_bytes(6000, 96, 4)[1], cns.cns_grad_workspace_bytes(2)[1]))
+    xs = [torch.randn(n, 96, device="cuda") for n in (6000, 700, 3000)]
+    routes = [cns.new_route(x.shape[0], 96, 4, workspace=ws) for x in xs]
+    g = torch.randn(1_000_000, device="cuda")
+    clip = cns.new_grad_clip([g], 1e30, outs=[torch.empty_like(g)], workspace=ws)
+    for turn in range(7):
+        for k, (r, x) in enumerate(zip(routes, xs)):
+            r.order.fill_(-7)
+            cns.run_route(r, x)
+            if (turn + k) % 3 == 0:
+                cns.run_grad_clip(clip)
+            want = steps.plan(np.argsort(-x.cpu().numpy(), -1, kind="stable")[:, :4], 96)
+            assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip((r.offsets, r.order, r.places), want))
+
+
 def test_a_failed_workspace_is_refused_until_it_is_initialised(cns):
     import torch
     x = torch.randn(9000, 64, device="cuda")
