@@ -27,7 +27,12 @@ struct RouteGradParams {
     float scale;
 };
 
+// What of a row has a gradient: the chosen experts alone; every expert through
+// the softmax (weights that are not renormalised); every expert through dscores.
+enum : int { kGradSparse = 0, kGradSoftmax = 1, kGradScores = 2 };
+
 constexpr int kGradWarps = 8;
+constexpr int kHeld = 32;   // elements of a row that a lane keeps in registers
 
 template <int SEG>
 __device__ __forceinline__ float lanes_sum(float v)
@@ -98,24 +103,39 @@ __device__ __forceinline__ void store_elems(typename Elem<D>::type *a, const flo
 // Bound by the bytes of dlogits, and of logits where the whole softmax takes
 // part.  SEG lanes take a token (8 for up to 8 places, so a warp has four
 // tokens and its reductions serve them together), W elements of 16 bytes a
-// lane; each lane also has one place.  The row is read from L1 a second and a
-// third time rather than held: any number of experts, few registers, and the
-// loads of many warps in flight.
-template <int D, int W, int SEG>
-__global__ void __launch_bounds__(kGradWarps * 32) route_backward_kernel(const RouteGradParams p)
+// lane; each lane also has one place.  For the softmax a row of up to HOLD
+// vectors a lane stays in registers, longer ones (and rows at odd addresses) are
+// read from L1 a second and a third time: 50021 x 160 f32 13.8 us (4.8 TB/s)
+// held, 16.7 us read again, and 19 us with a register budget that spills.  The
+// sparse forms write zeros and the chosen ones: 16384 x 256 f32 4.8 us (3.8 TB/s).
+template <int D, int W, int SEG, int HOLD, int MODE>
+__global__ void __launch_bounds__(kGradWarps * 32, MODE == kGradSparse ? 8 : 4) route_backward_kernel(const RouteGradParams p)
 {
     using T = typename Elem<D>::type;
     const int lane = threadIdx.x & 31, place = lane & (SEG - 1);
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kGradWarps * 32 / SEG);
     const int64_t begin = (static_cast<int64_t>(blockIdx.x) * kGradWarps + (threadIdx.x >> 5)) * (32 / SEG);
-    const bool softmax = p.score == CNS_SCORE_SOFTMAX;
-    const bool whole = p.dscores || (softmax && !p.renorm);
+    const bool softmax = MODE == kGradSoftmax || p.score == CNS_SCORE_SOFTMAX;
+    const bool renorm = MODE != kGradSoftmax && p.renorm;
+    constexpr bool whole = MODE != kGradSparse;
     for (int64_t t0 = begin; t0 < p.tokens; t0 += step) {
         const int64_t t = t0 + lane / SEG;
         const bool token = t < p.tokens;
         const T *row = static_cast<const T *>(p.logits) + t * p.stride;
-        const float *ds = p.dscores ? p.dscores + t * p.experts : nullptr;
+        const float *ds = MODE == kGradScores ? p.dscores + t * p.experts : nullptr;
         T *out = static_cast<T *>(p.dlogits) + t * p.dstride;
+        float held[HOLD ? HOLD : 1][W];   // the lane's logits, then e^(x - top)
+        if (HOLD && whole) {
+#pragma unroll
+            for (int j = 0; j < HOLD; ++j) {
+                const int e = (j * SEG + place) * W;
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    held[j][i] = -INFINITY;
+                if (token && e < p.experts)
+                    load_elems<D, W>(row + e, held[j]);
+            }
+        }
         // the lane's place
         int id = token && place < p.top_k ? p.ids[t * p.top_k + place] : -1;
         if (id >= p.experts)
@@ -123,13 +143,19 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_backward_kernel(const R
         const bool there = id >= 0;
         float g = there ? p.dweights[t * p.top_k + place] * p.scale : 0.f;
         const float x = there ? Elem<D>::get(row[id]) : -INFINITY;
-        const float h = there && ds ? ds[id] : 0.f;
+        const float h = MODE == kGradScores && there ? ds[id] : 0.f;
 
         // the row's softmax: top and the sum under it, and sum_i e^(x_i - top) h_i
         float top = 0.f, sum = 1.f, mean = 0.f;
         if (whole && softmax) {
             top = -INFINITY;
-            if (token) {
+            if constexpr (HOLD > 0) {
+#pragma unroll
+                for (int j = 0; j < HOLD; ++j)
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        top = fmaxf(top, held[j][i]);
+            } else if (token) {
 #pragma unroll 4
                 for (int e = place * W; e < p.experts; e += SEG * W) {
                     float v[W];
@@ -143,19 +169,34 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_backward_kernel(const R
             if (top == -INFINITY)
                 top = 0.f;   // every expert masked
             sum = 0.f;
-            if (token) {
-                // __expf: off by a relative 2^-22 + 2^-23 |x - top|, most where e^(x - top) is least
+            if constexpr (HOLD > 0) {
+#pragma unroll
+                for (int j = 0; j < HOLD; ++j) {
+                    const int e = (j * SEG + place) * W;
+                    float w[W];
+                    if (MODE == kGradScores && token && e < p.experts)
+                        load_elems<CNS_DT_F32, W>(ds + e, w);
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        held[j][i] = exp_near(held[j][i] - top);
+                        sum += held[j][i];
+                        if (MODE == kGradScores && token && e < p.experts)
+                            mean = fmaf(held[j][i], w[i], mean);
+                    }
+                }
+            } else if (token) {
 #pragma unroll 4
                 for (int e = place * W; e < p.experts; e += SEG * W) {
                     float v[W], w[W];
                     load_elems<D, W>(row + e, v);
-                    if (ds)
+                    if (MODE == kGradScores)
                         load_elems<CNS_DT_F32, W>(ds + e, w);
 #pragma unroll
                     for (int i = 0; i < W; ++i) {
-                        const float ex = __expf(v[i] - top);
+                        const float ex = exp_near(v[i] - top);   // off the most where it is the least
                         sum += ex;
-                        mean = ds ? fmaf(ex, w[i], mean) : mean;
+                        if (MODE == kGradScores)
+                            mean = fmaf(ex, w[i], mean);
                     }
                 }
             }
@@ -169,7 +210,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_backward_kernel(const R
         float d;
         if (softmax) {
             const float pj = whole && there ? expf(x - top) / sum : 0.f;
-            if (p.renorm) {
+            if (renorm) {
                 const float best = lanes_max<SEG>(x);
                 float q = there ? expf(x - best) : 0.f;
                 q = q / lanes_sum<SEG>(q);
@@ -182,7 +223,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_backward_kernel(const R
         } else {
             const float ex = expf(-fabsf(x)), r = 1.f / (1.f + ex);   // s and 1 - s without cancellation
             const float s = there ? (x >= 0.f ? r : ex * r) : 0.f, rest = x >= 0.f ? ex * r : r;
-            if (p.renorm) {
+            if (renorm) {
                 const float total = lanes_sum<SEG>(s) + 1e-20f;
                 g = (g - lanes_sum<SEG>(g * s) / total) / total;
             }
@@ -192,26 +233,39 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_backward_kernel(const R
         // the row, then the chosen ones over it
         if (token) {
             const float scale = 1.f / sum;
-#pragma unroll 4
-            for (int e = place * W; e < p.experts; e += SEG * W) {
-                float v[W], w[W];
-                if (whole) {
-                    load_elems<D, W>(row + e, v);
-                    if (ds)
-                        load_elems<CNS_DT_F32, W>(ds + e, w);
-                }
+            // one vector: its logits, or e^(x - top) of them, become its gradient
+            auto finish = [&](int e, float *v, bool exps) {
+                float w[W];
+                if (MODE == kGradScores)
+                    load_elems<CNS_DT_F32, W>(ds + e, w);
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
                     if (!whole) {
                         v[i] = 0.f;
                     } else if (softmax) {
-                        v[i] = __expf(v[i] - top) * scale * ((ds ? w[i] : 0.f) - mean);
+                        v[i] = (exps ? v[i] : exp_near(v[i] - top)) * scale * ((MODE == kGradScores ? w[i] : 0.f) - mean);
                     } else {
-                        const float ex = __expf(-fabsf(v[i])), r = 1.f / (1.f + ex);
+                        const float ex = exp_near(-fabsf(v[i])), r = 1.f / (1.f + ex);
                         v[i] = r * (ex * r) * w[i];
                     }
                 }
                 store_elems<D, W>(out + e, v);
+            };
+            if constexpr (HOLD > 0) {
+#pragma unroll
+                for (int j = 0; j < HOLD; ++j) {
+                    const int e = (j * SEG + place) * W;
+                    if (e < p.experts)
+                        finish(e, held[j], true);
+                }
+            } else {
+#pragma unroll 4
+                for (int e = place * W; e < p.experts; e += SEG * W) {
+                    float v[W];
+                    if (whole)
+                        load_elems<D, W>(row + e, v);
+                    finish(e, v, false);
+                }
             }
         }
         __syncwarp();   // orders the lanes' stores to one place
@@ -225,20 +279,40 @@ void launch_backward(const RouteGradParams &p, int sms, cudaStream_t s)
 {
     using T = typename Elem<D>::type;
     constexpr int W = 16 / static_cast<int>(sizeof(T));
-    const int per = p.top_k <= 8 ? 4 : 1;   // tokens of a warp
-    const int64_t ctas = (p.tokens + kGradWarps * per - 1) / (kGradWarps * per);
-    const int grid = static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(sms) * 8 * 16));
     const auto whole16 = [](const void *a) { return reinterpret_cast<uintptr_t>(a) % 16 == 0; };
+    // whole vectors in every row
     const bool wide = p.experts % W == 0 && whole16(p.logits) && whole16(p.dlogits) && whole16(p.dscores) &&
                       p.stride % W == 0 && p.dstride % W == 0;
-    if (wide && per == 4)
-        route_backward_kernel<D, W, 8><<<grid, kGradWarps * 32, 0, s>>>(p);
-    else if (wide)
-        route_backward_kernel<D, W, 32><<<grid, kGradWarps * 32, 0, s>>>(p);
-    else if (per == 4)
-        route_backward_kernel<D, 1, 8><<<grid, kGradWarps * 32, 0, s>>>(p);
-    else
-        route_backward_kernel<D, 1, 32><<<grid, kGradWarps * 32, 0, s>>>(p);
+    const auto launch = [&](auto kernel, int seg) {
+        const int64_t per = kGradWarps * (32 / seg), ctas = (p.tokens + per - 1) / per;
+        kernel<<<static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(sms) * 128)), kGradWarps * 32, 0, s>>>(p);
+    };
+    const bool eight = p.top_k <= 8;
+    if (p.dscores) {
+        if (wide && eight)
+            launch(route_backward_kernel<D, W, 8, 0, kGradScores>, 8);
+        else if (wide)
+            launch(route_backward_kernel<D, W, 32, 0, kGradScores>, 32);
+        else
+            launch(route_backward_kernel<D, 1, 32, 0, kGradScores>, 32);
+    } else if (p.score == CNS_SCORE_SOFTMAX && !p.renorm) {
+        if (wide && eight && p.experts <= kHeld * 8)
+            launch(route_backward_kernel<D, W, 8, kHeld / W, kGradSoftmax>, 8);
+        else if (wide && eight)
+            launch(route_backward_kernel<D, W, 8, 0, kGradSoftmax>, 8);
+        else if (wide)
+            launch(route_backward_kernel<D, W, 32, 16 / W, kGradSoftmax>, 32);
+        else
+            launch(route_backward_kernel<D, 1, 32, 0, kGradSoftmax>, 32);
+    } else if (wide && eight) {
+        launch(route_backward_kernel<D, W, 8, 0, kGradSparse>, 8);
+    } else if (wide) {
+        launch(route_backward_kernel<D, W, 32, 0, kGradSparse>, 32);
+    } else if (eight) {
+        launch(route_backward_kernel<D, 1, 8, 0, kGradSparse>, 8);
+    } else {
+        launch(route_backward_kernel<D, 1, 32, 0, kGradSparse>, 32);
+    }
 }
 
 size_t workspace_bytes(int64_t, int32_t experts, int32_t)

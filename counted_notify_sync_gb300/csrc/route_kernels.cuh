@@ -76,14 +76,6 @@ __device__ __forceinline__ uint32_t choice_key(float v)
 }
 constexpr uint32_t kMaskedKey = 0x007fffffu;   // of -inf; what was taken has key 0
 
-// e^x for the near path and for sums: off by a relative 2^-22 + 2^-23 |x|; tiny results are 0.
-__device__ __forceinline__ float exp_near(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
-    return r;
-}
-
 __device__ __forceinline__ float sigmoid_of(float x) { return 1.f / (1.f + expf(-x)); }
 
 // The choice value of a key (not NaN's payload, not 0's sign).

@@ -137,6 +137,14 @@ __device__ __forceinline__ bool receive_all(uint32_t *header, uint32_t ctas, uin
     return false;
 }
 
+// e^x where 2^-22 is enough (sums, and what an exact value replaces): off by a relative 2^-22 + 2^-23 |x|; tiny results are 0.
+__device__ __forceinline__ float exp_near(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+
 // One element of type `dtype` (cns_dtype_t) as a float, and back.
 template <int D> struct Elem;
 template <> struct Elem<CNS_DT_F32> {
