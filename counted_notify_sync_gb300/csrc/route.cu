@@ -422,9 +422,11 @@ extern "C" int cns_route(cns_route_t *r)
                                                       std::min<int>(dev.sm_count, kStepMaxCtas)));
             warps = kRouteWarps;
         }
-        const cudaError_t e = r->dtype == CNS_DT_F32    ? launch_route_f32(p, ctas, warps, s)
-                              : r->dtype == CNS_DT_BF16 ? launch_route_bf16(p, ctas, warps, s)
-                                                        : launch_route_f16(p, ctas, warps, s);
+        const bool by_score = p.bias || p.group_top == 2;
+        const auto launch = r->dtype == CNS_DT_F32    ? (by_score ? launch_route_f32_score : launch_route_f32_logit)
+                            : r->dtype == CNS_DT_BF16 ? (by_score ? launch_route_bf16_score : launch_route_bf16_logit)
+                                                      : (by_score ? launch_route_f16_score : launch_route_f16_logit);
+        const cudaError_t e = launch(p, ctas, warps, s);
         if (e == cudaErrorCooperativeLaunchTooLarge) {
             (void)cudaGetLastError();
             return CNS_ERR_NOT_RESIDENT;

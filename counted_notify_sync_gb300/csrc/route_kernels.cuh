@@ -1,6 +1,5 @@
 // route_kernels.cuh -- the routing kernel: choose each token's experts, weigh
-// them, and place the entries by expert.  One translation unit per element
-// type of the logits (route_f32.cu, route_bf16.cu, route_f16.cu).
+// them, and place the entries by expert.
 //
 // One warp takes one token: element i of lane l is expert 32 i + l, so every
 // load of a row is coalesced whatever its alignment, and among equal choice
@@ -60,10 +59,15 @@ struct RouteParams {
     float scale;
 };
 
-// Defined in the translation unit of each element type.
-cudaError_t launch_route_f32(const RouteParams &p, int ctas, int warps, cudaStream_t s);
-cudaError_t launch_route_bf16(const RouteParams &p, int ctas, int warps, cudaStream_t s);
-cudaError_t launch_route_f16(const RouteParams &p, int ctas, int warps, cudaStream_t s);
+// Launch the kernel for p's choice: by logit or by score (a bias, or groups
+// worth two experts), all groups or some.  One translation unit for each type
+// and choice (route_*.cu).
+cudaError_t launch_route_f32_logit(const RouteParams &p, int ctas, int warps, cudaStream_t s);
+cudaError_t launch_route_f32_score(const RouteParams &p, int ctas, int warps, cudaStream_t s);
+cudaError_t launch_route_bf16_logit(const RouteParams &p, int ctas, int warps, cudaStream_t s);
+cudaError_t launch_route_bf16_score(const RouteParams &p, int ctas, int warps, cudaStream_t s);
+cudaError_t launch_route_f16_logit(const RouteParams &p, int ctas, int warps, cudaStream_t s);
+cudaError_t launch_route_f16_score(const RouteParams &p, int ctas, int warps, cudaStream_t s);
 
 #ifdef CNS_ROUTE_KERNELS
 
@@ -415,15 +419,15 @@ __device__ __forceinline__ int place_lanes(const RouteParams &p) { return p.top_
 // nothing that the fast path is made for.
 // Returns the last batch's expert of the lane's place: of all tokens, if they
 // are one batch.
-template <int D, int V>
+template <int D, int V, bool SCORES, bool GROUPS>
 __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first, int64_t last, const float *s_bias,
                                               float reach, uint32_t *s_key, uint32_t *s_count)
 {
     using T = typename Elem<D>::type;
     const int lane = threadIdx.x & 31;
-    const bool by_logit = !p.bias && p.group_top == 1;
+    constexpr bool by_logit = !SCORES;
     const bool whole = p.softmax && (p.scores || !p.renorm || !by_logit);   // needs the softmax over all experts
-    const bool packs = D != CNS_DT_F32 && by_logit;
+    constexpr bool packs = D != CNS_DT_F32 && by_logit;
     const KeyRules rules = packs ? packed_rules() : by_logit ? logit_rules() : score_rules(reach);
     // e / size by a product: exact for e < 512 and sizes up to 256
     const int size = p.experts / p.groups;
@@ -497,7 +501,7 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
                 none = __all_sync(kFullWarp, all <= 0.9f * V * kNever);   // every expert masked: a padded token
             }
         }
-        if (p.groups > p.top_groups && sure && !none) {
+        if (GROUPS && sure && !none) {
             const uint32_t kept = kept_groups_near<V>(p, key, s_key, row_groups, rules, &sure);
             if (row_groups) {
                 uint32_t bits = kept;
@@ -623,7 +627,7 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
     return done;
 }
 
-template <int D, int V>
+template <int D, int V, bool SCORES, bool GROUPS>
 __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid_constant__ RouteParams p)
 {
     extern __shared__ uint32_t smem[];
@@ -653,7 +657,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
         asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const typename Elem<D>::type *>(p.logits) +
                                                       first * p.stride + e));
     }
-    const bool scores = p.bias || p.group_top == 2;   // chosen by score
     float b = p.bias && static_cast<int>(threadIdx.x) < E ? p.bias[threadIdx.x] : 0.f;
     if (threadIdx.x == 0)
         s_reach = 0;
@@ -661,7 +664,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
         for (int i = threadIdx.x; i < warps * E; i += blockDim.x)
             s_count[i] = 0u;
     __syncthreads();
-    if (scores) {
+    if (SCORES) {
         for (int e = threadIdx.x; e < 32 * V; e += blockDim.x) {
             if (e >= static_cast<int>(blockDim.x))
                 b = p.bias && e < E ? p.bias[e] : 0.f;
@@ -676,7 +679,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     }
 
     const float reach = 1.f + __int_as_float(s_reach);
-    const int done = choose_tokens<D, V>(p, first, last, s_bias, reach <= kMostBias ? reach : NAN, s_keys + warp * E, s_count + warp * E);
+    const int done = choose_tokens<D, V, SCORES, GROUPS>(p, first, last, s_bias, reach <= kMostBias ? reach : NAN, s_keys + warp * E, s_count + warp * E);
     if (!p.plan)
         return;
 
@@ -824,13 +827,14 @@ inline size_t route_smem(const RouteParams &p, int V, int warps)
                                (odd_groups ? warps * p.experts : 0));
 }
 
-template <int D, int V>
+template <int D, int V, bool SCORES, bool GROUPS>
 cudaError_t launch_route_v(const RouteParams &p, int ctas, int warps, cudaStream_t s)
 {
+    const auto kernel = route_kernel<D, V, SCORES, GROUPS>;
     const size_t smem = route_smem(p, V, warps);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(route_kernel<D, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess)
             return e;
     }
@@ -846,21 +850,21 @@ cudaError_t launch_route_v(const RouteParams &p, int ctas, int warps, cudaStream
     cfg.numAttrs = p.plan && ctas > 1 ? 1 : 0;
     RouteParams arg = p;
     void *args[] = {&arg};
-    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(route_kernel<D, V>), args);
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), args);
 }
 
 // The narrowest kernel that has an element for each expert.
-template <int D>
+template <int D, bool SCORES, bool GROUPS>
 cudaError_t launch_route(const RouteParams &p, int ctas, int warps, cudaStream_t s)
 {
     const int v = (p.experts + 31) / 32;
-    return v <= 1    ? launch_route_v<D, 1>(p, ctas, warps, s)
-           : v <= 2  ? launch_route_v<D, 2>(p, ctas, warps, s)
-           : v <= 4  ? launch_route_v<D, 4>(p, ctas, warps, s)
-           : v <= 6  ? launch_route_v<D, 6>(p, ctas, warps, s)
-           : v <= 8  ? launch_route_v<D, 8>(p, ctas, warps, s)
-           : v <= 12 ? launch_route_v<D, 12>(p, ctas, warps, s)
-                     : launch_route_v<D, 16>(p, ctas, warps, s);
+    return v <= 1    ? launch_route_v<D, 1, SCORES, GROUPS>(p, ctas, warps, s)
+           : v <= 2  ? launch_route_v<D, 2, SCORES, GROUPS>(p, ctas, warps, s)
+           : v <= 4  ? launch_route_v<D, 4, SCORES, GROUPS>(p, ctas, warps, s)
+           : v <= 6  ? launch_route_v<D, 6, SCORES, GROUPS>(p, ctas, warps, s)
+           : v <= 8  ? launch_route_v<D, 8, SCORES, GROUPS>(p, ctas, warps, s)
+           : v <= 12 ? launch_route_v<D, 12, SCORES, GROUPS>(p, ctas, warps, s)
+                     : launch_route_v<D, 16, SCORES, GROUPS>(p, ctas, warps, s);
 }
 
 #endif
