@@ -368,26 +368,45 @@ __device__ __noinline__ int choose_exact(const RouteParams &p, const typename El
     return mine;
 }
 
-// The chosen experts of `row` in the order of their exact choice values: lane
-// `place` of each `seg` lanes has place `place`'s.  Not for softmax by score.
-template <int D>
-__device__ __noinline__ int in_exact_order(const RouteParams &p, const typename Elem<D>::type *row, int chosen, int seg)
+// Settles a token whose near keys leave its choice open: the experts whose keys
+// are not surely below the last place's, at most 32 (false if there are more),
+// in the order of their exact choice values, the lower first among equals.
+// Lane `place` of each `seg` lanes gets place `place`'s.  Not for softmax by score.
+template <int D, int V>
+__device__ __noinline__ bool settle(const RouteParams &p, const typename Elem<D>::type *row, const uint32_t *key,
+                                    uint32_t last, uint32_t apart, uint16_t *s_near, int seg, int *chosen)
 {
-    const int place = threadIdx.x & (seg - 1);
-    const uint32_t key =
-        chosen >= 0 ? exact_key(p, Elem<D>::get(row[chosen]), p.bias ? p.bias[chosen] : 0.f, 0.f, 1.f) : 0u;
-    int before = 0;
-    for (int j = 0; j < p.top_k; ++j) {
-        const uint32_t k = __shfl_sync(kFullWarp, key, j);
-        const int e = __shfl_sync(kFullWarp, chosen, j);
-        before += (k > key || (k == key && e < chosen)) ? 1 : 0;
+    const uint32_t lane = threadIdx.x & 31u, earlier = (1u << lane) - 1u;
+    const uint32_t quanta = last >> 9;
+    const uint32_t least = max((quanta > apart ? quanta - apart : 0u) << 9, 511u);   // 511: nothing that is no expert
+    uint32_t count = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const bool in = key[i] > least;
+        const uint32_t at = __ballot_sync(kFullWarp, in), to = count + __popc(at & earlier);
+        if (in && to < 32u)
+            s_near[to] = static_cast<uint16_t>(511u - (key[i] & 511u));
+        count += __popc(at);
     }
-    int ordered = -1;
-    for (int j = 0; j < p.top_k; ++j) {
-        const int at = __shfl_sync(kFullWarp, before, j), e = __shfl_sync(kFullWarp, chosen, j);
-        ordered = at == place ? e : ordered;
+    if (count > 32u)
+        return false;
+    __syncwarp();
+    const int e = lane < count ? s_near[lane] : -1;
+    const uint32_t exact = e >= 0 ? exact_key(p, Elem<D>::get(row[e]), p.bias ? p.bias[e] : 0.f, 0.f, 1.f) : 0u;
+    uint32_t before = 0u;
+    for (uint32_t j = 0; j < count; ++j) {
+        const uint32_t k = __shfl_sync(kFullWarp, exact, j);
+        const int o = __shfl_sync(kFullWarp, e, j);
+        before += (k > exact || (k == exact && o < e)) ? 1u : 0u;
     }
-    return place < p.top_k ? ordered : -1;
+    __syncwarp();
+    if (e >= 0)
+        s_near[before] = static_cast<uint16_t>(e);
+    __syncwarp();
+    const int place = lane & (seg - 1);
+    *chosen = place < p.top_k ? s_near[place] : -1;
+    __syncwarp();
+    return true;
 }
 
 // The sum, or the largest, over the calling lane's `seg` lanes.
@@ -421,7 +440,7 @@ __device__ __forceinline__ int place_lanes(const RouteParams &p) { return p.top_
 // are one batch.
 template <int D, int V, bool SCORES, bool GROUPS>
 __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first, int64_t last, const float *s_bias,
-                                              float reach, uint32_t *s_key, uint32_t *s_count)
+                                              float reach, uint32_t *s_key, uint16_t *s_near, uint32_t *s_count)
 {
     using T = typename Elem<D>::type;
     const int lane = threadIdx.x & 31;
@@ -574,14 +593,13 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
             }
             chosen = place < p.top_k && got > rules.never ? static_cast<int>(511u - (got & 511u)) : -1;
             if (rules.apart) {
-                // nothing that ranks by less than it may be off, and nothing but experts
+                // nothing but experts, and nothing that ranks by less than it may be off
                 const uint32_t down = __shfl_down_sync(kFullWarp, got, 1);
                 const uint32_t next = place + 1 < p.top_k ? down : after;
-                const bool near = place < p.top_k && !surely_above(got, next, rules.apart);
-                sure = !__any_sync(kFullWarp, place < p.top_k && (chosen < 0 || (near && place == p.top_k - 1)));
-                // the right ones, but some too near to be sure of their order: by their exact values
-                if (sure && __any_sync(kFullWarp, near))
-                    chosen = in_exact_order<D>(p, row, chosen, seg);
+                sure = !__any_sync(kFullWarp, place < p.top_k && chosen < 0);
+                if (sure && __any_sync(kFullWarp, place < p.top_k && !surely_above(got, next, rules.apart)))
+                    sure = settle<D, V>(p, row, key, __shfl_sync(kFullWarp, got, p.top_k - 1), rules.apart, s_near, seg,
+                                        &chosen);
             }
         }
         if (!sure) {
@@ -640,11 +658,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     float *s_bias = reinterpret_cast<float *>(s_total + E);             // [32 V]
     uint32_t *s_keys = reinterpret_cast<uint32_t *>(s_bias) + 32 * V;  // [warps][E], groups of other sizes than 32
     __shared__ uint32_t s_chunk[16];
+    __shared__ uint32_t s_tag, s_turn;
     __shared__ int s_stop, s_reach;
+    __shared__ uint16_t s_near[kRouteWarps][32];   // experts that a token's choice is between
 
+    // what the workspace says, read by one thread of a CTA: all threads' loads of one line took 2 us
     uint32_t tag = 0, turn = 0;
     bool stop = false;
-    if (p.plan) {
+    if (p.plan && threadIdx.x == 0) {
         tag = ld_relaxed_gpu(p.header + kStepEpochWord) + 1u;
         turn = ld_relaxed_gpu(p.header + kStepRouteWord) + 1u;
         stop = ld_relaxed_gpu(p.header + kStepStatusWord + 1) != 0u;   // an earlier call failed
@@ -679,14 +700,23 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     }
 
     const float reach = 1.f + __int_as_float(s_reach);
-    const int done = choose_tokens<D, V, SCORES, GROUPS>(p, first, last, s_bias, reach <= kMostBias ? reach : NAN, s_keys + warp * E, s_count + warp * E);
+    const int done = choose_tokens<D, V, SCORES, GROUPS>(p, first, last, s_bias, reach <= kMostBias ? reach : NAN, s_keys + warp * E, s_near[warp],
+                                                           s_count + warp * E);
     if (!p.plan)
         return;
 
     // Counts of the CTA's warps become the counts before each warp.  The CTA's own go to its row and are added
     // to its block's (16 CTAs), so that nobody has to read the rows of all CTAs: 152 rows by 152 CTAs took 2.5 us.
     // The blocks' sums are kept twice; a call uses one, and clears the other for the next call.
+    if (threadIdx.x == 0) {
+        s_tag = tag;
+        s_turn = turn;
+        s_stop = stop;
+    }
     __syncthreads();
+    tag = s_tag;
+    turn = s_turn;
+    stop = s_stop != 0;
     uint32_t *sums = p.header + kStepSumWord + (turn & 1u) * kStepSumWords;
     uint32_t *stale = p.header + kStepSumWord + ((turn & 1u) ^ 1u) * kStepSumWords;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
@@ -727,10 +757,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
             if (lane == 0)
                 s_stop = stop;
         }
-    } else if (threadIdx.x == 0) {
-        s_stop = stop;
+        __syncthreads();
     }
-    __syncthreads();
     if (s_stop)
         return;
     if (ctas > 1)

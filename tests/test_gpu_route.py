@@ -171,6 +171,63 @@ def test_strided_rows_and_spare_capacity(cns, dtype, experts):
         check(cns, x, b, dtype, top_k=3, score=SIG, stride=stride, capacity=200)
 
 
+@pytest.mark.parametrize("experts,top_k", [(40, 3), (256, 8), (384, 8), (500, 20)])
+@pytest.mark.parametrize("spread", [3, 12, 60, 500])
+def test_logits_a_rounding_apart(cns, experts, top_k, spread):
+    """Rows whose leading logits are neighbouring floats, `spread` of them: fewer and more than what a token's
+    choice is settled among, equals too."""
+    rng = np.random.RandomState(experts + spread)
+    x = rng.randn(64, experts).astype(np.float32)
+    for r in range(64):
+        at = rng.permutation(experts)[:spread]
+        x[r, at] = np.float32(5.0) + np.float32(2.0 ** -21) * rng.randint(0, max(2, spread // 2), size=at.size).astype(np.float32)
+    x[5] = x[5, 0]                                   # all equal
+    for groups in (1, 4) if experts % 4 == 0 else (1,):
+        check(cns, x.astype(np.float64), None, "f32", top_k=top_k, score=SOFT, groups=groups,
+              top_groups=3 if groups > 1 else 1)
+
+
+@pytest.mark.parametrize("experts,top_k", [(64, 8), (256, 8), (384, 6), (512, 16)])
+@pytest.mark.parametrize("spread", [3, 12, 60, 500])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (8, 2), (4, 1)])
+def test_scores_a_rounding_apart(cns, experts, top_k, spread, groups, group_top):
+    """The same for scores with a bias, against the definition in 32 bits on the device: 1 / (1 + exp(-l)), plus
+    the bias, sorted with equals in order."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(experts + spread)
+    x = torch.randn(200, experts, generator=gen, device="cuda")
+    pick = torch.rand(200, experts, generator=gen, device="cuda").argsort(-1)[:, :spread]
+    near = 1.5 + 1e-6 * torch.rand(200, pick.shape[1], generator=gen, device="cuda")
+    x.scatter_(1, pick, near)
+    b = 0.3 * torch.randn(experts, generator=gen, device="cuda")
+    b[torch.rand(experts, generator=gen, device="cuda") < 0.7] = 0.125
+    top_groups = max(1, groups // 2)
+    v = 1.0 / (1.0 + torch.exp(-x)) + b
+    if groups > 1:
+        worth = v.view(200, groups, -1).sort(dim=-1, descending=True).values[..., :group_top].sum(-1)
+        keep = worth.sort(dim=-1, descending=True, stable=True).indices[:, :top_groups]
+        stays = torch.zeros(200, groups, dtype=torch.bool, device="cuda").scatter_(1, keep, True)
+        v = torch.where(stays.repeat_interleave(experts // groups, 1), v, torch.full_like(v, -float("inf")))
+    want = v.sort(dim=-1, descending=True, stable=True).indices[:, :top_k]
+    r = cns.new_route(200, experts, top_k, score=SIG, groups=groups, top_groups=top_groups, group_top=group_top)
+    cns.run_route(r, x, bias=b, sync=True)
+    assert torch.equal(r.ids.long(), want)
+
+
+@pytest.mark.parametrize("bias", [3e30, -5e7, float("nan"), 0.0])
+def test_biases_beyond_the_fast_path(cns, bias):
+    import torch
+    x, _ = grid_inputs(90, 48, seed=2)
+    b = torch.zeros(48, device="cuda")
+    b[7] = bias
+    xs = torch.from_numpy(x).float().cuda()
+    r = cns.new_route(90, 48, 5, score=SIG)
+    cns.run_route(r, xs, bias=b, sync=True)
+    v = 1.0 / (1.0 + torch.exp(-xs)) + b
+    assert torch.equal(r.ids.long(), v.sort(dim=-1, descending=True, stable=True).indices[:, :5])
+
+
 def test_no_tokens(cns):
     import torch
     r = cns.new_route(16, 8, 2)
