@@ -131,6 +131,10 @@ def run_pipeline(done, ack, tiles: int, tile_words: int, rounds: int, producer_s
 
 
 # --- device-wide steps of a training step ------------------------------------------------------------------
+#
+# Like every call here these run on the stream that they are given (None: the default stream) and return before
+# the GPU is done.  A tensor that belongs to another stream needs what it needs for any kernel: the streams
+# ordered by an event, and record_stream before it is freed.
 
 _CODES = {}   # torch dtype -> cns_dtype_t, filled by the first new_route or new_grad_clip
 
@@ -268,12 +272,29 @@ def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogi
 
 def _dense(t):
     """Whether the tensor's elements fill one stretch of memory, in whatever order of the axes."""
+    if t.is_contiguous():
+        return True
     at = 1
     for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
         if stride != at:
             return False
         at *= size
     return True
+
+
+def _tensor_table(tensors, index, what):
+    """(cns_tensor_t array, [(first byte, last byte + 1)]) of dense tensors on device `index`."""
+    table = (_native.Tensor * max(len(tensors), 1))()
+    spans = []
+    for i, (t, e) in enumerate(zip(tensors, table)):
+        if t.get_device() != index:
+            raise ValueError(f"{what}[{i}]: on {t.device}, CUDA device {index} expected")
+        if not _dense(t):
+            raise ValueError(f"{what}[{i}]: not dense (strides {t.stride()})")
+        n, at, code = t.numel(), t.data_ptr(), _dtype_code(t)
+        e.data_dev, e.elems, e.dtype = at, n, code
+        spans.append((at, at + n * (4 if code == _native.CNS_DT_F32 else 2)))
+    return table, spans
 
 
 def new_grad_clip(grads, max_norm: float = float("inf"), *, outs=None, eps: float = 1e-6,
@@ -285,37 +306,28 @@ def new_grad_clip(grads, max_norm: float = float("inf"), *, outs=None, eps: floa
     torch = _torch()
     _dtype_codes()
     g = _native.GradClip()
-    n = len(grads)
+    grads, n = list(grads), len(grads)
     device = torch.device(device or (grads[0].device if n else "cuda"))
-    if outs is not None and len(outs) != n:
-        raise ValueError("outs: one for each gradient expected")
-    spans = []
-
-    def table(tensors):
-        a = (_native.Tensor * max(n, 1))()
-        for i, t in enumerate(tensors):
-            if t.device.type != "cuda" or (device.index is not None and t.device != device):
-                raise ValueError(f"tensor {i}: on {t.device}, {device} expected")
-            if t.numel() and not _dense(t):
-                raise ValueError(f"tensor {i}: not dense (strides {t.stride()})")
-            a[i].data_dev, a[i].elems, a[i].dtype = t.data_ptr(), t.numel(), _dtype_code(t)
-        return a
-
-    g.grad_table = table(grads)
-    g.out_table = None if outs is None else table(outs)
-    for i, t in enumerate(grads):
-        span = (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-        if outs is not None and t.numel():
-            o = outs[i]
-            if t.shape != o.shape or t.stride() != o.stride():
+    if device.type != "cuda":
+        raise ValueError(f"gradients on {device}, a CUDA device expected")
+    g.norm = torch.empty((), dtype=torch.float32, device=device)
+    index = g.norm.get_device()
+    g.grad_table, spans = _tensor_table(grads, index, "grads")
+    g.out_table = None
+    if outs is None:
+        spans = [(a, b, True, i) for i, (a, b) in enumerate(spans) if b > a]
+    else:
+        outs = list(outs)
+        if len(outs) != n:
+            raise ValueError("outs: one for each gradient expected")
+        g.out_table, to = _tensor_table(outs, index, "outs")
+        for i, (t, o) in enumerate(zip(grads, outs)):
+            if t.shape != o.shape or (t.stride() != o.stride() and t.numel()):
                 raise ValueError(f"outs[{i}]: the gradient's shape and strides expected")
-            spans.append((o.data_ptr(), o.data_ptr() + o.numel() * o.element_size(), True, i))
-            if spans[-1][:2] == span and t.dtype == o.dtype:
-                continue   # in place
-        elif outs is not None and t.shape != outs[i].shape:
-            raise ValueError(f"outs[{i}]: the gradient's shape expected")
-        if t.numel():
-            spans.append((*span, outs is None, i))
+        # an output that is its gradient is one tensor
+        same = [a == b and t.dtype == o.dtype for a, b, t, o in zip(spans, to, grads, outs)]
+        spans = ([(a, b, False, i) for i, ((a, b), s) in enumerate(zip(spans, same)) if b > a and not s] +
+                 [(a, b, True, i) for i, (a, b) in enumerate(to) if b > a])
     spans.sort()
     end, written = (0, 0), (0, 0)   # how far the tensors so far reach, and those of them that are written
     for first, last, writes, i in spans:
@@ -324,12 +336,11 @@ def new_grad_clip(grads, max_norm: float = float("inf"), *, outs=None, eps: floa
         end = max(end, (last, i))
         if writes:
             written = max(written, (last, i))
-    g.tensors = (list(grads), None if outs is None else list(outs))   # alive as long as the table
+    g.tensors = (grads, outs)   # alive as long as the table
     g.grads = g.grad_table
     if g.out_table is not None:
         g.outs = g.out_table
     g.count, g.max_norm, g.eps, g.norm_type, g.timeout_ms = n, max_norm, eps, norm_type, timeout_ms
-    g.norm = torch.empty((), dtype=torch.float32, device=device)
     if workspace is None:
         rc, nbytes = _native.cns_grad_workspace_bytes(n)
         _native.check(rc, "new_grad_clip")

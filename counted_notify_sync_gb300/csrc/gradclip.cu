@@ -104,7 +104,7 @@ __device__ __forceinline__ uint32_t tile0_of(const GradArgs<N> &a, int i)
 // A table of more tensors than fit the arguments goes to the workspace as the
 // arguments of launches of this kernel: no staging buffer, and nothing that a
 // graph capture would lose.
-constexpr int kChunkEntries = 120;
+constexpr int kChunkEntries = 1000;   // 32 KB of arguments
 struct TableChunk {
     GradEntry e[kChunkEntries];
     GradEntry *to;
@@ -580,7 +580,7 @@ int launch(const cns_grad_clip_t &g, const GradParams &p, int ctas)
         }
         if (N == 0 && (c.n == kChunkEntries || (c.n > 0 && i + 1 == g.count))) {
             c.to = const_cast<GradEntry *>(a.p.table) + a.p.count;
-            grad_table_kernel<<<1, 128, 0, s>>>(c);
+            grad_table_kernel<<<1, 1024, 0, s>>>(c);
             CNS_CUDA(cudaGetLastError());
             a.p.count += c.n;
             c.n = 0;
