@@ -408,6 +408,7 @@ extern "C" int cns_route(cns_route_t *r)
     p.group_top = r->group_top ? r->group_top : 1;
     p.renorm = r->renorm;
     p.scale = r->scale;
+    p.key_step = 512u;
     p.timeout_ns = barrier_timeout_ns(r->timeout_ms);
     p.header = static_cast<uint32_t *>(r->workspace_dev);
     p.counts = p.header + CNS_STEP_WORKSPACE_HEADER_BYTES / 4;

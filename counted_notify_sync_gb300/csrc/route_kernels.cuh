@@ -57,6 +57,7 @@ struct RouteParams {
     int32_t experts, top_k, groups, top_groups, group_top;
     int32_t softmax, renorm, plan;
     float scale;
+    uint32_t key_step;   // 512, which the compiler must not know (see choose_tokens)
 };
 
 // Launch the kernel for p's choice: by logit or by score (a bias, or groups
@@ -154,7 +155,8 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteParams &p, const uint
     return __ballot_sync(kFullWarp, lane < p.groups && before < p.top_groups);
 }
 
-// What the fast path's keys are (see the top of the file).
+// What the fast path's keys are (see the top of the file): a value v becomes
+// kQuanta * clamp(v * scale + offset, 0, 1) quanta.
 struct KeyRules {
     uint32_t never;   // keys up to this one cannot be chosen
     uint32_t apart;   // quanta between values that are surely in order; 0: keys are exact
@@ -164,29 +166,28 @@ struct KeyRules {
 
 constexpr float kNever = -1e30f;   // the value of what cannot be chosen
 constexpr float kMostBias = 1e6f;
-constexpr float kQuanta = 8388608.f;   // 2^23: a float from there to 2^24 has its integer in its low 23 bits
+constexpr float kLeastQuanta = 8388608.f;        // 2^23: a float from there to 2^24 has its integer in its low bits
+constexpr float kQuanta = kLeastQuanta - 64.f;
 
 // Scores lie in [0, 1], biases in [1 - reach, reach - 1].  The approximate
 // score's error is s (1 - s) (2^-22 + 2^-23.4 |x|) from the exponential, and
-// (2^-24 + 2^-23) s from the sum and the reciprocal: below 2.7e-7.  The exact
-// score in 32 bits is within 1.8e-7 of the true one, and the sums with the bias
-// round to 2^-24 of reach each.  Two values, and the quanta round too.
+// (2^-24 + 2^-23) s from the sum and the reciprocal: below 2.7e-7; what keeps
+// masked experts out adds at most 4.8e-7.  The exact score in 32 bits is within
+// 1.8e-7 of the true one, and the sums with the bias round to 2^-24 of reach
+// each.  Two values, and the quanta round too.
 __device__ __forceinline__ KeyRules score_rules(float reach)
 {
     KeyRules r;
     r.never = 511u;
-    r.scale = (kQuanta - 64.f) / (2.f * reach - 1.f);
-    r.zero = 8u + static_cast<uint32_t>((reach - 1.f) * r.scale);
-    r.offset = kQuanta + static_cast<float>(r.zero);
-    r.apart = 3u + static_cast<uint32_t>(2.f * (4.5e-7f + 1.3e-7f * reach) * r.scale);
+    r.scale = (1.f - 1e-5f) / (2.f * reach - 1.f);
+    r.offset = 1e-6f + (reach - 1.f) * r.scale;
+    r.zero = static_cast<uint32_t>(r.offset * kQuanta);
+    r.apart = 4u + static_cast<uint32_t>(2.f * (9.3e-7f + 1.9e-7f * reach) * r.scale * kQuanta);
     return r;
 }
 
-__device__ __forceinline__ KeyRules logit_rules()
-{
-    // the row's largest is 0, what lies 16 below it is out of reach
-    return KeyRules{511u, 1u, 0u, (kQuanta - 64.f) / 16.f, 2.f * kQuanta - 32.f};
-}
+// The row's largest is 0, what lies 16 below it is out of reach.
+__device__ __forceinline__ KeyRules logit_rules() { return KeyRules{511u, 1u, 0u, 1.f / 16.f, 1.f}; }
 
 __device__ __forceinline__ KeyRules packed_rules() { return KeyRules{kMaskedKey | 511u, 0u, 0u, 0.f, 0.f}; }
 
@@ -431,6 +432,12 @@ __device__ __forceinline__ float seg_max(float v, int seg)
 // Lanes that a token's places take when tokens are handled several at a time.
 __device__ __forceinline__ int place_lanes(const RouteParams &p) { return p.top_k <= 8 ? 8 : 32; }
 
+// Rows of 32 experts that the next narrower kernel has (launch_route).
+__host__ __device__ constexpr int narrower(int v)
+{
+    return v > 12 ? 12 : v > 8 ? 8 : v > 6 ? 6 : v > 4 ? 4 : v > 2 ? 2 : v - 1;
+}
+
 // Choose and weigh the experts of the tokens first .. last - 1 by the calling
 // warp; counts each expert's in s_count if there is a plan.  s_bias: of expert
 // e, 0 if there is no bias, kNever where it is -inf and beyond the last expert;
@@ -469,8 +476,8 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
         {
             float x[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                x[i] = 32 * i + lane < p.experts ? Elem<D>::get(row[32 * i + lane]) : -INFINITY;
+            for (int i = 0; i < V; ++i)   // (rows that the next narrower kernel has are whole)
+                x[i] = i < narrower(V) || 32 * i + lane < p.experts ? Elem<D>::get(row[32 * i + lane]) : -INFINITY;
             if (whole || (by_logit && !packs)) {
                 top = x[0];
 #pragma unroll
@@ -502,22 +509,27 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
                 for (int i = 0; i < V; ++i)
                     key[i] = (choice_key(x[i]) & ~511u) | (511u - (32 * i + lane));
             } else {
-                float all = 0.f;   // NaN if any value is
+                // The arithmetic stays on the FMA pipe where it can: min, max, compare and select go at half its
+                // rate, and the keys' comparisons below are many of them.  So the clamp is a saturating product,
+                // and the shift a product by a number that the compiler cannot turn into one.
+                float all = 0.f, some = 0.f;   // NaN or inf if any value is; 0 if every expert is masked
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float v = x[i] - top;
                     if (!by_logit) {
                         float s;
                         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + exp_near(-x[i])));
-                        v = s + s_bias[32 * i + lane];
+                        // the least float times the logit: -inf for a masked expert, else below 4.8e-7
+                        v = fmaf(x[i], 1.4e-45f, s + s_bias[32 * i + lane]);
                     }
-                    v = x[i] == -INFINITY ? kNever : v;
                     all += v;
-                    key[i] = (__float_as_uint(fmaxf(fmaf(v, rules.scale, rules.offset), kQuanta)) << 9) |
-                             (511u - (32 * i + lane));
+                    float part;
+                    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(part) : "f"(v), "f"(rules.scale), "f"(rules.offset));
+                    some += part;
+                    key[i] = __float_as_uint(fmaf(part, kQuanta, kLeastQuanta)) * p.key_step + (511u - 32u * i - lane);
                 }
-                sure = sure && !__any_sync(kFullWarp, !(all == all));
-                none = __all_sync(kFullWarp, all <= 0.9f * V * kNever);   // every expert masked: a padded token
+                sure = sure && !__any_sync(kFullWarp, !(all < INFINITY));
+                none = __all_sync(kFullWarp, some == 0.f);   // a padded token
             }
         }
         if (GROUPS && sure && !none) {

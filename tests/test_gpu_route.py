@@ -228,6 +228,44 @@ def test_biases_beyond_the_fast_path(cns, bias):
     assert torch.equal(r.ids.long(), v.sort(dim=-1, descending=True, stable=True).indices[:, :5])
 
 
+@pytest.mark.parametrize("low", [-50.0, -87.5, -88.5, -100.0, -1e10, -3.4028234663852886e38])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_low_logits_with_high_biases(cns, low, groups):
+    """Scores of next to nothing that a bias lifts among the chosen: masked is only -inf."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(11)
+    x = torch.randn(150, 128, generator=gen, device="cuda")
+    x[torch.rand(150, 128, generator=gen, device="cuda") < 0.3] = low
+    x[torch.rand(150, 128, generator=gen, device="cuda") < 0.2] = -float("inf")
+    b = torch.rand(128, generator=gen, device="cuda") * 1.5
+    v = 1.0 / (1.0 + torch.exp(-x)) + b
+    v = torch.where(x == -float("inf"), torch.full_like(v, -float("inf")), v)
+    if groups > 1:
+        best = v.view(150, groups, -1).sort(dim=-1, descending=True).values[..., :2]
+        worth = torch.where(best == -float("inf"), torch.zeros_like(best), best).sum(-1)
+        keep = worth.sort(dim=-1, descending=True, stable=True).indices[:, :2]
+        stays = torch.zeros(150, groups, dtype=torch.bool, device="cuda").scatter_(1, keep, True)
+        v = torch.where(stays.repeat_interleave(128 // groups, 1), v, torch.full_like(v, -float("inf")))
+    r = cns.new_route(150, 128, 8, score=SIG, groups=groups, top_groups=2 if groups > 1 else 1,
+                      group_top=2 if groups > 1 else 1)
+    cns.run_route(r, x, bias=b, sync=True)
+    assert torch.equal(r.ids.long(), v.sort(dim=-1, descending=True, stable=True).indices[:, :8])
+
+
+def test_infinite_logits_with_biases(cns):
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(12)
+    x = torch.randn(60, 64, generator=gen, device="cuda")
+    x[torch.rand(60, 64, generator=gen, device="cuda") < 0.05] = float("inf")
+    b = torch.rand(64, generator=gen, device="cuda")
+    v = 1.0 / (1.0 + torch.exp(-x)) + b
+    r = cns.new_route(60, 64, 8, score=SIG)
+    cns.run_route(r, x, bias=b, sync=True)
+    assert torch.equal(r.ids.long(), v.sort(dim=-1, descending=True, stable=True).indices[:, :8])
+
+
 def test_no_tokens(cns):
     import torch
     r = cns.new_route(16, 8, 2)
