@@ -197,13 +197,63 @@ __device__ __forceinline__ bool surely_above(uint32_t a, uint32_t b, uint32_t ap
     return (a >> 9) - (b >> 9) >= apart;
 }
 
+// One element's exact choice value as a key.
+__device__ __forceinline__ uint32_t exact_key(const RouteParams &p, float x, float bias, float top, float sum)
+{
+    float v = x;
+    if (p.bias || p.group_top == 2) {
+        v = p.softmax ? expf(x - top) / sum : sigmoid_of(x);
+        if (p.bias)
+            v += bias;
+        v = x == -INFINITY ? -INFINITY : v;
+    }
+    return choice_key(v);
+}
+
+// Bit g: group g is among the top_groups worthiest, where the quanta of lane
+// g's group's worth leave it open: of those that are neither surely above `most`,
+// the best group that is not in, nor surely below `least`, the last that is, by
+// their exact worths.
+template <int D>
+__device__ __noinline__ uint32_t settle_groups(const RouteParams &p, const typename Elem<D>::type *row, uint32_t worth,
+                                               uint32_t least, uint32_t most, uint32_t apart)
+{
+    const uint32_t lane = threadIdx.x & 31u;
+    const int size = p.experts / p.groups;
+    const bool group = lane < static_cast<uint32_t>(p.groups), in = group && worth >= most + apart;
+    uint32_t kept = __ballot_sync(kFullWarp, in);
+    const uint32_t open = __ballot_sync(kFullWarp, group && !in && worth + apart > least);
+    uint32_t exact = 0u;   // of lane g's group
+    for (uint32_t rest = open; rest; rest &= rest - 1u) {
+        const int g = __ffs(rest) - 1;
+        uint32_t one = 0u, two = 0u;
+        for (int i = lane; i < size; i += 32) {
+            const int e = g * size + i;
+            const uint32_t k = exact_key(p, Elem<D>::get(row[e]), p.bias ? p.bias[e] : 0.f, 0.f, 1.f);
+            two = max(two, min(one, k));
+            one = max(one, k);
+        }
+        __syncwarp();
+        const uint32_t best = __reduce_max_sync(kFullWarp, one), at = __ballot_sync(kFullWarp, one == best);
+        const uint32_t second = (at & (at - 1u)) ? best : __reduce_max_sync(kFullWarp, one == best ? two : one);
+        exact = lane == static_cast<uint32_t>(g) ? worth_of(best, second, p.group_top, kMaskedKey) : exact;
+    }
+    const int places = p.top_groups - __popc(kept);
+    int before = 0;
+    for (uint32_t rest = open; rest; rest &= rest - 1u) {
+        const uint32_t g = __ffs(rest) - 1, o = __shfl_sync(kFullWarp, exact, g);
+        before += (o > exact || (o == exact && g < lane)) ? 1 : 0;
+    }
+    return kept | __ballot_sync(kFullWarp, ((open >> lane) & 1u) && before < places);
+}
+
 // Bit g: group g is among the top_groups worthiest, from the fast path's keys,
 // which are all different: one redux finds a group's best and a second one,
-// without it, the next.  *sure becomes false where the last group that is in
-// and the first that is not are too near.
-template <int V>
-__device__ __forceinline__ uint32_t kept_groups_near(const RouteParams &p, const uint32_t *key, uint32_t *s_key,
-                                                     int row_groups, const KeyRules &rules, bool *sure)
+// without it, the next.
+template <int D, int V>
+__device__ __forceinline__ uint32_t kept_groups_near(const RouteParams &p, const typename Elem<D>::type *row,
+                                                     const uint32_t *key, uint32_t *s_key, int row_groups,
+                                                     const KeyRules &rules)
 {
     const uint32_t lane = threadIdx.x & 31u;
     uint32_t best = 0u, second = 0u;   // of group `lane`
@@ -253,6 +303,7 @@ __device__ __forceinline__ uint32_t kept_groups_near(const RouteParams &p, const
     if (lane >= static_cast<uint32_t>(p.groups))
         worth = 0u;
     // the worthiest, one after the other, and the one after them
+    const uint32_t its = worth;
     uint32_t kept = 0u, least = 0u;
     for (int j = 0; j < p.top_groups; ++j) {
         least = __reduce_max_sync(kFullWarp, worth);
@@ -261,7 +312,10 @@ __device__ __forceinline__ uint32_t kept_groups_near(const RouteParams &p, const
     }
     if (rules.apart) {
         const uint32_t most = __reduce_max_sync(kFullWarp, worth);
-        *sure = p.group_top == 2 ? (least >> 5) - (most >> 5) >= 2u * rules.apart : surely_above(least, most, rules.apart);
+        const int shift = p.group_top == 2 ? 5 : 9;
+        const uint32_t apart = p.group_top == 2 ? 2u * rules.apart : rules.apart;
+        if ((least >> shift) - (most >> shift) < apart)
+            kept = settle_groups<D>(p, row, its >> shift, least >> shift, most >> shift, apart);
     }
     return kept;
 }
@@ -310,19 +364,6 @@ __device__ __forceinline__ uint32_t best_eight(uint32_t one, uint32_t two, uint3
     other = max(other, min(v, o));
     *rest = other;
     return merge_eights(max(v, o), true);
-}
-
-// One element's exact choice value as a key.
-__device__ __forceinline__ uint32_t exact_key(const RouteParams &p, float x, float bias, float top, float sum)
-{
-    float v = x;
-    if (p.bias || p.group_top == 2) {
-        v = p.softmax ? expf(x - top) / sum : sigmoid_of(x);
-        if (p.bias)
-            v += bias;
-        v = x == -INFINITY ? -INFINITY : v;
-    }
-    return choice_key(v);
 }
 
 // The exact path: lane j gets place j's expert (-1: none).
@@ -533,7 +574,7 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
             }
         }
         if (GROUPS && sure && !none) {
-            const uint32_t kept = kept_groups_near<V>(p, key, s_key, row_groups, rules, &sure);
+            const uint32_t kept = kept_groups_near<D, V>(p, row, key, s_key, row_groups, rules);
             if (row_groups) {
                 uint32_t bits = kept;
                 int in = 0;
