@@ -27,7 +27,8 @@
 // 25M f32 (100 MB in, 100 MB out): 54 us with neither, 47 us with all of this
 // (50 us with streaming stores alone; 48 us without shared memory).  Keeping
 // two rounds in shared memory instead (224 KB) took 54 us: loads in flight
-// need L1, and too little of it was left.  Filling shared memory by bulk
+// need L1, and too little of it was left.  Prefetching the lost rounds into L2
+// while the CTAs exchange took 47 us.  Filling shared memory by bulk
 // copies, which do not, was no faster at 3.5 KB a copy (46 us here, but the
 // norm fell to 6.5 TB/s) and slower below: a bulk copy costs its SM some 50 ns.
 // Small sets are a launch, a trip to memory and the exchange: 0.2M f32
@@ -468,10 +469,13 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const __grid_constant
             norm = __uint_as_float(__reduce_max_sync(kFullWarp, most));
             if (NORM == CNS_NORM_L2 && norm > 0.f && norm < INFINITY) {
                 // squares of the largest root's parts: nothing overflows
+                const float inverse = 1.f / norm;   // (of a norm below 2^-126 this is inf: then the parts as they are)
                 float sum = 0.f;
 #pragma unroll
-                for (float x : r)
-                    sum = fmaf(x / norm, x / norm, sum);
+                for (float x : r) {
+                    const float y = inverse < INFINITY ? x * inverse : x / norm;
+                    sum = fmaf(y, y, sum);
+                }
                 norm *= sqrtf(warp_sum(sum));
             }
             if (!stop && blockIdx.x == 0 && lane == 0)
