@@ -1,6 +1,7 @@
 /*
  * cns.h -- C ABI of libcns: a device-wide epoch barrier (SYNCALL) and a
- * counted notify (CntNotify) for one NVIDIA GB300 GPU (sm_103a).
+ * counted notify (CntNotify) for one NVIDIA GB300 GPU (sm_103a), and
+ * device-wide steps of a training step built like the barrier's kernels.
  *
  * The operations follow two public descriptions:
  *   [SYNCALL] "PTO-ISA 跨核同步屏障 SYNCALL 实战指南" (the PTO-ISA SYNCALL

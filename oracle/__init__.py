@@ -16,6 +16,8 @@ Parity status of each function (what pins it; see tests/test_oracle_*.py):
   cnt_record / cnt_wait_satisfied           hand-built truth table (golden)
   cnt_statemachine                          golden sequences + per-op table
   pipeline                                  closed-form checksum
+  steps.py (routing, its gradient, the      hand-worked rows, brute force,
+  gradient norm; 64 bits, numpy)            central differences
 """
 from __future__ import annotations
 
