@@ -96,20 +96,18 @@ __device__ __forceinline__ float value_of(uint32_t key)
     return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// What a group is worth, as a key, from the keys of its best and second best
-// (keys up to `masked` are of experts that cannot be chosen).
-__device__ __forceinline__ uint32_t worth_of(uint32_t best, uint32_t second, int group_top, uint32_t masked)
+// What a group is worth, as a key, from the exact keys of its best and second
+// best.
+__device__ __forceinline__ uint32_t worth_of(uint32_t best, uint32_t second, int group_top)
 {
-    return group_top == 2 && second > masked ? choice_key(value_of(best) + value_of(second)) : best;
+    return group_top == 2 && second > kMaskedKey ? choice_key(value_of(best) + value_of(second)) : best;
 }
 
-// Bit g: group g is among the top_groups worthiest; *worth_of_lane: of group
-// `lane`.  Groups of whole elements
-// of the warp (32, 64, ... experts) are valued by redux; of other sizes by one
-// lane each, from shared memory.
+// Bit g: group g is among the top_groups worthiest, from exact keys.  Groups of
+// whole elements of the warp (32, 64, ... experts) are valued by redux, of other
+// sizes by one lane each, from shared memory.
 template <int V>
-__device__ __forceinline__ uint32_t kept_groups(const RouteParams &p, const uint32_t *key, uint32_t *s_key,
-                                                uint32_t masked, uint32_t *worth_of_lane)
+__device__ __forceinline__ uint32_t kept_groups(const RouteParams &p, const uint32_t *key, uint32_t *s_key)
 {
     const int lane = threadIdx.x & 31, size = p.experts / p.groups;
     uint32_t worth = 0u;   // of group `lane`
@@ -130,7 +128,7 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteParams &p, const uint
                                               : __reduce_max_sync(kFullWarp, one == best ? two : one);
                 }
                 if (lane == g)
-                    worth = worth_of(best, second, p.group_top, masked);
+                    worth = worth_of(best, second, p.group_top);
                 one = two = 0u;
                 in = 0;
                 ++g;
@@ -149,11 +147,10 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteParams &p, const uint
                 two = max(two, min(one, k));
                 one = max(one, k);
             }
-            worth = worth_of(one, two, p.group_top, masked);
+            worth = worth_of(one, two, p.group_top);
         }
         __syncwarp();
     }
-    *worth_of_lane = worth;
     int before = 0;   // groups that go before this one
     for (int g = 0; g < p.groups; ++g) {
         const uint32_t o = __shfl_sync(kFullWarp, worth, g);
@@ -177,8 +174,9 @@ constexpr float kLeastQuanta = 8388608.f;        // 2^23: a float from there to 
 constexpr float kQuanta = kLeastQuanta - 64.f;
 
 // Scores lie in [0, 1], biases in [1 - reach, reach - 1].  The approximate
-// score's error is s (1 - s) (2^-22 + 2^-23.4 |x|) from the exponential, and
-// (2^-24 + 2^-23) s from the sum and the reciprocal: below 2.7e-7; what keeps
+// sigmoid's error is s (1 - s) (2^-22 + 2^-23.4 |x|) from the exponential, and
+// (2^-24 + 2^-23) s from the sum and the reciprocal: below 2.7e-7 (a softmax
+// score's: s (2^-22 + 2^-23 |x - top|) and two roundings, below 4e-7); what keeps
 // masked experts out adds at most 4.8e-7.  The exact score in 32 bits is within
 // 1.8e-7 of the true one, and the sums with the bias round to 2^-24 of reach
 // each.  Two values, and the quanta round too.
@@ -204,7 +202,7 @@ __device__ __forceinline__ bool surely_above(uint32_t a, uint32_t b, uint32_t ap
     return (a >> 9) - (b >> 9) >= apart;
 }
 
-// One element's exact choice value as a key.
+// One element's exact choice value as a key; top, sum: of the row's softmax.
 __device__ __forceinline__ uint32_t exact_key(const RouteParams &p, float x, float bias, float top, float sum)
 {
     float v = x;
@@ -223,7 +221,7 @@ __device__ __forceinline__ uint32_t exact_key(const RouteParams &p, float x, flo
 // their exact worths.
 template <int D>
 __device__ __noinline__ uint32_t settle_groups(const RouteParams &p, const typename Elem<D>::type *row, uint32_t worth,
-                                               uint32_t least, uint32_t most, uint32_t apart)
+                                               uint32_t least, uint32_t most, uint32_t apart, float top, float sum)
 {
     const uint32_t lane = threadIdx.x & 31u;
     const int size = p.experts / p.groups;
@@ -236,14 +234,14 @@ __device__ __noinline__ uint32_t settle_groups(const RouteParams &p, const typen
         uint32_t one = 0u, two = 0u;
         for (int i = lane; i < size; i += 32) {
             const int e = g * size + i;
-            const uint32_t k = exact_key(p, Elem<D>::get(row[e]), p.bias ? p.bias[e] : 0.f, 0.f, 1.f);
+            const uint32_t k = exact_key(p, Elem<D>::get(row[e]), p.bias ? p.bias[e] : 0.f, top, sum);
             two = max(two, min(one, k));
             one = max(one, k);
         }
         __syncwarp();
         const uint32_t best = __reduce_max_sync(kFullWarp, one), at = __ballot_sync(kFullWarp, one == best);
         const uint32_t second = (at & (at - 1u)) ? best : __reduce_max_sync(kFullWarp, one == best ? two : one);
-        exact = lane == static_cast<uint32_t>(g) ? worth_of(best, second, p.group_top, kMaskedKey) : exact;
+        exact = lane == static_cast<uint32_t>(g) ? worth_of(best, second, p.group_top) : exact;
     }
     const int places = p.top_groups - __popc(kept);
     int before = 0;
@@ -260,7 +258,7 @@ __device__ __noinline__ uint32_t settle_groups(const RouteParams &p, const typen
 template <int D, int V>
 __device__ __forceinline__ uint32_t kept_groups_near(const RouteParams &p, const typename Elem<D>::type *row,
                                                      const uint32_t *key, uint32_t *s_key, int row_groups,
-                                                     const KeyRules &rules)
+                                                     const KeyRules &rules, float top, float sum)
 {
     const uint32_t lane = threadIdx.x & 31u;
     uint32_t best = 0u, second = 0u;   // of group `lane`
@@ -322,7 +320,7 @@ __device__ __forceinline__ uint32_t kept_groups_near(const RouteParams &p, const
         const int shift = p.group_top == 2 ? 5 : 9;
         const uint32_t apart = p.group_top == 2 ? 2u * rules.apart : rules.apart;
         if ((least >> shift) - (most >> shift) < apart)
-            kept = settle_groups<D>(p, row, its >> shift, least >> shift, most >> shift, apart);
+            kept = settle_groups<D>(p, row, its >> shift, least >> shift, most >> shift, apart, top, sum);
     }
     return kept;
 }
@@ -387,8 +385,7 @@ __device__ __noinline__ int choose_exact(const RouteParams &p, const typename El
     }
     if (p.groups > p.top_groups) {
         const int size = p.experts / p.groups;
-        uint32_t worth;
-        const uint32_t kept = kept_groups<V>(p, key, s_key, kMaskedKey, &worth);
+        const uint32_t kept = kept_groups<V>(p, key, s_key);
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (32 * i + lane < p.experts && !((kept >> ((32 * i + lane) / size)) & 1u))
@@ -420,10 +417,11 @@ __device__ __noinline__ int choose_exact(const RouteParams &p, const typename El
 // Settles a token whose near keys leave its choice open: the experts whose keys
 // are not surely below the last place's, at most 32 (false if there are more),
 // in the order of their exact choice values, the lower first among equals.
-// Lane `place` of each `seg` lanes gets place `place`'s.  Not for softmax by score.
+// Lane `place` of each `seg` lanes gets place `place`'s.
 template <int D, int V>
 __device__ __noinline__ bool settle(const RouteParams &p, const typename Elem<D>::type *row, const uint32_t *key,
-                                    uint32_t last, uint32_t apart, uint16_t *s_near, int seg, int *chosen)
+                                    uint32_t last, uint32_t apart, uint16_t *s_near, int seg, float top, float sum,
+                                    int *chosen)
 {
     const uint32_t lane = threadIdx.x & 31u, earlier = (1u << lane) - 1u;
     const uint32_t quanta = last >> 9;
@@ -441,7 +439,7 @@ __device__ __noinline__ bool settle(const RouteParams &p, const typename Elem<D>
         return false;
     __syncwarp();
     const int e = lane < count ? s_near[lane] : -1;
-    const uint32_t exact = e >= 0 ? exact_key(p, Elem<D>::get(row[e]), p.bias ? p.bias[e] : 0.f, 0.f, 1.f) : 0u;
+    const uint32_t exact = e >= 0 ? exact_key(p, Elem<D>::get(row[e]), p.bias ? p.bias[e] : 0.f, top, sum) : 0u;
     uint32_t before = 0u;
     for (uint32_t j = 0; j < count; ++j) {
         const uint32_t k = __shfl_sync(kFullWarp, exact, j);
@@ -518,7 +516,7 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
         if (t + 1 < last && lane < V)
             asm volatile("prefetch.global.L1 [%0];" ::"l"(row + p.stride + min(32 * lane, p.experts - 1)));
         uint32_t key[V];
-        bool sure = by_logit || (!p.softmax && reach == reach);
+        bool sure = by_logit || reach == reach;
         bool none = false;
         float top = 0.f, sum = 1.f;
         {
@@ -561,27 +559,40 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
                 // rate, and the keys' comparisons below are many of them.  So the clamp is a saturating product,
                 // and the shift a product by a number that the compiler cannot turn into one.
                 float all = 0.f, some = 0.f;   // NaN or inf if any value is; 0 if every expert is masked
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float v = x[i] - top;
-                    if (!by_logit) {
-                        float s;
-                        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + exp_near(-x[i])));
-                        // the least float times the logit: -inf for a masked expert, else below 4.8e-7
-                        v = fmaf(x[i], 1.4e-45f, s + s_bias[32 * i + lane]);
-                    }
+                auto take = [&](int i, float v) {
                     all += v;
                     float part;
                     asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(part) : "f"(v), "f"(rules.scale), "f"(rules.offset));
                     some += part;
                     key[i] = __float_as_uint(fmaf(part, kQuanta, kLeastQuanta)) * p.key_step + (511u - 32u * i - lane);
+                };
+                // a score's value; the least float times the logit is -inf for a masked expert, else below 4.8e-7
+                auto take_score = [&](int i, float s) {
+                    take(i, fmaf(x[i], 1.4e-45f, s + s_bias[32 * i + lane]));
+                };
+                if (by_logit) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        take(i, x[i] - top);
+                } else if (p.softmax) {
+                    const float inverse = 1.f / sum;
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        take_score(i, exp_near(x[i] - top) * inverse);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        float s;
+                        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + exp_near(-x[i])));
+                        take_score(i, s);
+                    }
                 }
                 sure = sure && !__any_sync(kFullWarp, !(all < INFINITY));
                 none = __all_sync(kFullWarp, some == 0.f);   // a padded token
             }
         }
         if (GROUPS && sure && !none) {
-            const uint32_t kept = kept_groups_near<D, V>(p, row, key, s_key, row_groups, rules);
+            const uint32_t kept = kept_groups_near<D, V>(p, row, key, s_key, row_groups, rules, top, sum);
             if (row_groups) {
                 uint32_t bits = kept;
                 int in = 0;
@@ -659,7 +670,7 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
                 sure = !__any_sync(kFullWarp, place < p.top_k && chosen < 0);
                 if (sure && __any_sync(kFullWarp, place < p.top_k && !surely_above(got, next, rules.apart)))
                     sure = settle<D, V>(p, row, key, __shfl_sync(kFullWarp, got, p.top_k - 1), rules.apart, s_near, seg,
-                                        &chosen);
+                                        top, sum, &chosen);
             }
         }
         if (!sure) {
@@ -714,8 +725,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     const uint32_t cta = blockIdx.x, ctas = gridDim.x;
     uint32_t *s_count = smem;                                          // [warps][E]
     uint32_t *s_base = s_count + (p.plan ? warps * E : 0);             // [E]
-    uint32_t *s_total = s_base + E;                                     // [E]
-    float *s_bias = reinterpret_cast<float *>(s_total + E);             // [32 V]
+    uint32_t *s_total = s_base + E;                                    // [E]
+    float *s_bias = reinterpret_cast<float *>(s_total + E);            // [32 V]
     uint32_t *s_keys = reinterpret_cast<uint32_t *>(s_bias) + 32 * V;  // [warps][E], groups of other sizes than 32
     __shared__ uint32_t s_chunk[16];
     __shared__ uint32_t s_tag, s_turn;
@@ -760,8 +771,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     }
 
     const float reach = 1.f + __int_as_float(s_reach);
-    const int done = choose_tokens<D, V, SCORES, GROUPS>(p, first, last, s_bias, reach <= kMostBias ? reach : NAN, s_keys + warp * E, s_near[warp],
-                                                           s_count + warp * E);
+    const int done =
+        choose_tokens<D, V, SCORES, GROUPS>(p, first, last, s_bias, reach <= kMostBias ? reach : NAN, s_keys + warp * E,
+                                            s_near[warp], s_count + warp * E);
     if (!p.plan)
         return;
 

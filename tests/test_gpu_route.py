@@ -228,6 +228,52 @@ def test_biases_beyond_the_fast_path(cns, bias):
     assert torch.equal(r.ids.long(), v.sort(dim=-1, descending=True, stable=True).indices[:, :5])
 
 
+@pytest.mark.parametrize("experts,top_k,groups,group_top", [(64, 6, 1, 1), (256, 8, 8, 2), (160, 4, 8, 2), (512, 20, 1, 1)])
+@pytest.mark.parametrize("bias", [True, False])
+def test_softmax_by_score(cns, experts, top_k, groups, group_top, bias):
+    """Softmax scores chosen with a bias, or with groups worth two.  The softmax's sum rounds with its order, so
+    the choice is held to its definition in 64 bits within 1e-6 of the values: in order, and none left out that
+    is above."""
+    import torch
+    if not bias and group_top == 1:
+        pytest.skip("chosen by logit")
+    rng = np.random.RandomState(experts)
+    x = (2 * rng.randn(400, experts)).astype(np.float32)
+    x[rng.rand(400, experts) < 0.05] = -np.inf
+    x[3] = -np.inf
+    b = (0.02 * rng.randn(experts)).astype(np.float32) if bias else None
+    top_groups = max(1, groups // 2)
+    r = cns.new_route(400, experts, top_k, score=SOFT, groups=groups, top_groups=top_groups, group_top=group_top)
+    cns.run_route(r, torch.from_numpy(x).cuda(), bias=None if b is None else torch.from_numpy(b).cuda(), sync=True)
+    ids, w = r.ids.cpu().numpy(), r.weights.cpu().double().numpy()
+    assert (ids[3] == -1).all() and (w[3] == 0).all()
+    for t in range(400):
+        if t == 3:
+            continue
+        s = steps.scores(x[t].astype(np.float64), SOFT)
+        v = s + (0 if b is None else b.astype(np.float64))
+        v[x[t] == -np.inf] = -np.inf
+        assert len(set(ids[t])) == top_k and ids[t].min() >= 0
+        if groups > 1:
+            worth = np.array([np.sort(g[g > -np.inf])[-2:].sum() for g in v.reshape(groups, -1)])
+            used = np.unique(ids[t] // (experts // groups))
+            assert len(used) <= top_groups
+            # the groups used are worth as much as the best ones, and nothing better in them was left out
+            bound = np.sort(worth)[-top_groups]
+            assert (worth[used] >= bound - 2e-6).all()
+            open_ = [g for g in range(groups) if worth[g] > bound + 2e-6] + list(used)
+            inside = np.isin(np.arange(experts) // (experts // groups), open_)
+        else:
+            inside = np.ones(experts, dtype=bool)
+        chosen = v[ids[t]]
+        assert (np.diff(chosen) <= 1e-6).all()
+        rest = inside.copy()
+        rest[ids[t]] = False
+        assert not rest.any() or v[rest].max() <= chosen[-1] + 1e-6
+        q = steps.scores(x[t][ids[t]].astype(np.float64), SOFT)
+        np.testing.assert_allclose(w[t], q, rtol=3.9e-6)
+
+
 @pytest.mark.parametrize("low", [-50.0, -87.5, -88.5, -100.0, -1e10, -3.4028234663852886e38])
 @pytest.mark.parametrize("groups", [1, 4])
 def test_low_logits_with_high_biases(cns, low, groups):
