@@ -252,6 +252,46 @@ __device__ __noinline__ uint32_t settle_groups(const RouteParams &p, const typen
     return kept | __ballot_sync(kFullWarp, ((open >> lane) & 1u) && before < places);
 }
 
+// The best and the second best over the lanes of each element, to lane i for
+// element i < V (a power of two).  Halves of the elements change sides between
+// halves of the lanes, so all elements' reductions share the shuffles: 50
+// instructions for 8 elements where a redux or two for each took 70 and
+// more latency.
+template <int V>
+__device__ __forceinline__ void best_two_of_each(const uint32_t *key, uint32_t *best, uint32_t *second)
+{
+    const uint32_t lane = threadIdx.x & 31u;
+    uint32_t a[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        a[i] = key[i];
+        b[i] = 0u;
+    }
+    int d = 16;
+#pragma unroll
+    for (int n = V / 2; n > 0; n >>= 1, d >>= 1) {
+        const bool upper = lane & d;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const uint32_t x = upper ? a[i + n] : a[i], y = __shfl_xor_sync(kFullWarp, upper ? a[i] : a[i + n], d);
+            if (n == V / 2) {
+                b[i] = min(x, y);
+            } else {
+                const uint32_t u = upper ? b[i + n] : b[i], w = __shfl_xor_sync(kFullWarp, upper ? b[i] : b[i + n], d);
+                b[i] = max(min(x, y), max(u, w));
+            }
+            a[i] = max(x, y);
+        }
+    }
+    for (; d > 0; d >>= 1) {
+        const uint32_t y = __shfl_xor_sync(kFullWarp, a[0], d), w = __shfl_xor_sync(kFullWarp, b[0], d);
+        b[0] = max(min(a[0], y), max(b[0], w));
+        a[0] = max(a[0], y);
+    }
+    *best = __shfl_sync(kFullWarp, a[0], (lane * (32 / V)) & 31u);
+    *second = __shfl_sync(kFullWarp, b[0], (lane * (32 / V)) & 31u);
+}
+
 // Bit g: group g is among the top_groups worthiest, from the fast path's keys,
 // which are all different: one redux finds a group's best and a second one,
 // without it, the next.
@@ -262,7 +302,10 @@ __device__ __forceinline__ uint32_t kept_groups_near(const RouteParams &p, const
 {
     const uint32_t lane = threadIdx.x & 31u;
     uint32_t best = 0u, second = 0u;   // of group `lane`
-    if (row_groups == 1) {
+    if (V > 1 && (V & (V - 1)) == 0 && row_groups == 1) {
+        if constexpr (V > 1 && (V & (V - 1)) == 0)
+            best_two_of_each<V>(key, &best, &second);
+    } else if (row_groups == 1) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const uint32_t top = __reduce_max_sync(kFullWarp, key[i]);

@@ -398,6 +398,29 @@ def test_streams_graphs_and_shared_workspaces(cns):
         assert np.array_equal(r.order.cpu().numpy(), order) and np.array_equal(r.places.cpu().numpy(), places)
 
 
+def test_calls_on_several_streams_at_once(cns):
+    """Whole-GPU grids from three streams, each with its own workspace: none waits for another's."""
+    import torch
+    shapes = [(6000, 64, 4), (9000, 256, 8), (400, 128, 8)]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    runs = [(cns.new_route(t, e, k), torch.randn(t, e, device="cuda")) for t, e, k in shapes]
+    g = torch.randn(5_000_000, device="cuda")
+    clip = cns.new_grad_clip([g], 1.0, outs=[torch.empty_like(g)])
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for (r, x), s in zip(runs, streams):
+            cns.run_route(r, x, stream=s)
+        cns.run_grad_clip(clip, stream=streams[3])
+    torch.cuda.synchronize()
+    for (r, x), (t, e, k) in zip(runs, shapes):
+        assert cns.syncall_read_workspace(r.workspace)[3] == 0
+        want = np.argsort(-x.cpu().numpy(), -1, kind="stable")[:, :k]
+        assert np.array_equal(r.ids.cpu().numpy(), want)
+        assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip((r.offsets, r.order, r.places), steps.plan(want, e)))
+    assert cns.syncall_read_workspace(clip.workspace)[3] == 0
+    assert abs(clip.norm.item() / float(torch.linalg.vector_norm(g.double())) - 1) < 4.1e-6
+
+
 def test_a_workspace_shared_with_clipping(cns):
     """Routings and clippings in turn on one workspace: each leaves it as the other needs it."""
     import torch
