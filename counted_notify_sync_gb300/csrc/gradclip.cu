@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const __grid_constant
         const uint32_t begin = n * blockIdx.x / gridDim.x, end = n * (blockIdx.x + 1) / gridDim.x;
         return begin + warp < end ? round * full + begin + warp : ~0u;
     };
+    grid_dependency_wait();   // launched early: nothing of the tensors or the workspace before this
     uint32_t tag = 0;
     bool stop = false;
     if (warp == 0) {
@@ -590,7 +591,8 @@ int launch(const cns_grad_clip_t &g, const GradParams &p, int ctas)
             c.n = 0;
         }
     }
-    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = ctas > 1 ? together_launch(&attr) : early_launch(&attr);
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
@@ -599,12 +601,6 @@ int launch(const cns_grad_clip_t &g, const GradParams &p, int ctas)
         CNS_CUDA(cudaFuncSetAttribute(grad_kernel<NORM, CLIP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       kLaneVecs * kRowBytes * kWarps));
     }
-    cudaLaunchAttribute coop;
-    coop.id = cudaLaunchAttributeCooperative;
-    coop.val.cooperative = 1;
-    cfg.attrs = &coop;
-    
-    cfg.numAttrs = ctas > 1 ? 1 : 0;
     void *args[] = {&a};
     const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(grad_kernel<NORM, CLIP, N>), args);
     if (e == cudaErrorCooperativeLaunchTooLarge) {
@@ -675,7 +671,6 @@ int grad_run(cns_grad_clip_t *g)
     p.max_norm = g->max_norm;
     p.eps = g->eps;
     // one CTA an SM, fewer when there is not a tile for each
-    
     const int ctas = std::max(1, static_cast<int>(std::min<int64_t>(tiles, most)));
     if (int rc = g->norm_type == CNS_NORM_L2 ? launch_sized<CNS_NORM_L2, CLIP>(*g, p, ctas)
                                              : launch_sized<CNS_NORM_INF, CLIP>(*g, p, ctas))

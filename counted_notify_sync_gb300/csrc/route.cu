@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, MODE == kGradSparse ? 8 : 4) 
     const bool softmax = MODE == kGradSoftmax || p.score == CNS_SCORE_SOFTMAX;
     const bool renorm = MODE != kGradSoftmax && p.renorm;
     constexpr bool whole = MODE != kGradSparse;
+    grid_dependency_wait();   // launched early: nothing of the tensors before this
     for (int64_t t0 = begin; t0 < p.tokens; t0 += step) {
         const int64_t t = t0 + lane / SEG;
         const bool token = t < p.tokens;
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, MODE == kGradSparse ? 8 : 4) 
 }
 
 template <int D>
-void launch_backward(const RouteGradParams &p, int sms, cudaStream_t s)
+cudaError_t launch_backward(const RouteGradParams &p, int sms, cudaStream_t s)
 {
     using T = typename Elem<D>::type;
     constexpr int W = 16 / static_cast<int>(sizeof(T));
@@ -285,34 +286,29 @@ void launch_backward(const RouteGradParams &p, int sms, cudaStream_t s)
                       p.stride % W == 0 && p.dstride % W == 0;
     const auto launch = [&](auto kernel, int seg) {
         const int64_t per = kGradWarps * (32 / seg), ctas = (p.tokens + per - 1) / per;
-        kernel<<<static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(sms) * 128)), kGradWarps * 32, 0, s>>>(p);
+        cudaLaunchAttribute early;
+        cudaLaunchConfig_t cfg = early_launch(&early);
+        cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(ctas, static_cast<int64_t>(sms) * 128)));
+        cfg.blockDim = dim3(kGradWarps * 32);
+        cfg.stream = s;
+        RouteGradParams arg = p;
+        void *args[] = {&arg};
+        return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), args);
     };
     const bool eight = p.top_k <= 8;
-    if (p.dscores) {
-        if (wide && eight)
-            launch(route_backward_kernel<D, W, 8, 0, kGradScores>, 8);
-        else if (wide)
-            launch(route_backward_kernel<D, W, 32, 0, kGradScores>, 32);
-        else
-            launch(route_backward_kernel<D, 1, 32, 0, kGradScores>, 32);
-    } else if (p.score == CNS_SCORE_SOFTMAX && !p.renorm) {
-        if (wide && eight && p.experts <= kHeld * 8)
-            launch(route_backward_kernel<D, W, 8, kHeld / W, kGradSoftmax>, 8);
-        else if (wide && eight)
-            launch(route_backward_kernel<D, W, 8, 0, kGradSoftmax>, 8);
-        else if (wide)
-            launch(route_backward_kernel<D, W, 32, 16 / W, kGradSoftmax>, 32);
-        else
-            launch(route_backward_kernel<D, 1, 32, 0, kGradSoftmax>, 32);
-    } else if (wide && eight) {
-        launch(route_backward_kernel<D, W, 8, 0, kGradSparse>, 8);
-    } else if (wide) {
-        launch(route_backward_kernel<D, W, 32, 0, kGradSparse>, 32);
-    } else if (eight) {
-        launch(route_backward_kernel<D, 1, 8, 0, kGradSparse>, 8);
-    } else {
-        launch(route_backward_kernel<D, 1, 32, 0, kGradSparse>, 32);
-    }
+    if (p.dscores)
+        return wide && eight ? launch(route_backward_kernel<D, W, 8, 0, kGradScores>, 8)
+               : wide        ? launch(route_backward_kernel<D, W, 32, 0, kGradScores>, 32)
+                             : launch(route_backward_kernel<D, 1, 32, 0, kGradScores>, 32);
+    if (p.score == CNS_SCORE_SOFTMAX && !p.renorm)
+        return wide && eight && p.experts <= kHeld * 8 ? launch(route_backward_kernel<D, W, 8, kHeld / W, kGradSoftmax>, 8)
+               : wide && eight                         ? launch(route_backward_kernel<D, W, 8, 0, kGradSoftmax>, 8)
+               : wide ? launch(route_backward_kernel<D, W, 32, 16 / W, kGradSoftmax>, 32)
+                      : launch(route_backward_kernel<D, 1, 32, 0, kGradSoftmax>, 32);
+    return wide && eight ? launch(route_backward_kernel<D, W, 8, 0, kGradSparse>, 8)
+           : wide        ? launch(route_backward_kernel<D, W, 32, 0, kGradSparse>, 32)
+           : eight       ? launch(route_backward_kernel<D, 1, 8, 0, kGradSparse>, 8)
+                         : launch(route_backward_kernel<D, 1, 32, 0, kGradSparse>, 32);
 }
 
 size_t workspace_bytes(int64_t, int32_t experts, int32_t)
@@ -486,11 +482,8 @@ extern "C" int cns_route_backward(const cns_route_grad_t *g)
     p.renorm = g->renorm;
     p.scale = g->scale;
     cudaStream_t s = to_stream(g->stream);
-    switch (g->dtype) {
-    case CNS_DT_F32: launch_backward<CNS_DT_F32>(p, dev.sm_count, s); break;
-    case CNS_DT_BF16: launch_backward<CNS_DT_BF16>(p, dev.sm_count, s); break;
-    default: launch_backward<CNS_DT_F16>(p, dev.sm_count, s); break;
-    }
-    CNS_CUDA(cudaGetLastError());
+    CNS_CUDA(g->dtype == CNS_DT_F32    ? launch_backward<CNS_DT_F32>(p, dev.sm_count, s)
+             : g->dtype == CNS_DT_BF16 ? launch_backward<CNS_DT_BF16>(p, dev.sm_count, s)
+                                       : launch_backward<CNS_DT_F16>(p, dev.sm_count, s));
     return CNS_SUCCESS;
 }

@@ -776,6 +776,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     __shared__ int s_stop, s_reach;
     __shared__ uint16_t s_near[kRouteWarps][32];   // experts that a token's choice is between
 
+    grid_dependency_wait();   // launched early: nothing of the tensors or the workspace before this
     // what the workspace says, read by one thread of a CTA: all threads' loads of one line took 2 us
     uint32_t tag = 0, turn = 0;
     bool stop = false;
@@ -981,16 +982,12 @@ cudaError_t launch_route_v(const RouteParams &p, int ctas, int warps, cudaStream
         if (e != cudaSuccess)
             return e;
     }
-    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = p.plan && ctas > 1 ? together_launch(&attr) : early_launch(&attr);
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute coop;
-    coop.id = cudaLaunchAttributeCooperative;
-    coop.val.cooperative = 1;
-    cfg.attrs = &coop;
-    cfg.numAttrs = p.plan && ctas > 1 ? 1 : 0;
     RouteParams arg = p;
     void *args[] = {&arg};
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), args);

@@ -23,6 +23,31 @@ constexpr uint32_t kStepSumWord = kStepBoxWord + 2 * kStepMaxCtas * kStepMaxCtas
 constexpr uint32_t kStepSumWords = kStepMaxCtas / kStepBlockCtas * CNS_ROUTE_MAX_EXPERTS;
 static_assert(4 * (kStepSumWord + 2 * kStepSumWords) == CNS_STEP_WORKSPACE_HEADER_BYTES, "header layout");
 
+// Launches of CTAs that wait for one another: cooperative, so that all are on the GPU together.
+inline cudaLaunchConfig_t together_launch(cudaLaunchAttribute *a)
+{
+    a->id = cudaLaunchAttributeCooperative;
+    a->val.cooperative = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.attrs = a;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// All other launches: the grid is set up while the one before it in the stream finishes, and waits for that one's
+// results by grid_dependency_wait, which every thread calls before it touches memory.  In a stream of them a grid
+// is scheduled 0.3-0.6 us after the last one's CTAs have left, where ordinary launches follow one another in steps
+// of 2.05 us: a routing gradient of 509 x 64 1.8 us a call against 4.1 us, of 16384 x 256 4.4 against 6.2.
+inline cudaLaunchConfig_t early_launch(cudaLaunchAttribute *a)
+{
+    a->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a->val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.attrs = a;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
 constexpr unsigned kFullWarp = 0xffffffffu;
 
 __device__ __forceinline__ float warp_sum(float v)
