@@ -4,8 +4,9 @@
 //   norm = sqrt(sum over all tensors of x^2)   (or the largest |x|)
 //   out  = x * min(1, max_norm / (norm + eps))
 //
-// One cooperative launch, one CTA an SM: read everything once and sum; exchange
-// the CTAs' parts (step_device.cuh); scale.
+// One launch, one CTA an SM: read everything once and sum; then, for the norm
+// alone, the last CTA joins the parts; to clip, the CTAs exchange them
+// (step_device.cuh; a cooperative launch) and scale.
 //
 // Layout.  A tile is `vecs` 16-byte vectors a lane of one warp (512 B to 4 KB,
 // all tiles of a call alike), cut at 16-byte boundaries of the address space:
@@ -14,8 +15,8 @@
 // the GPU, neighbours to a CTA, so that the rounds sweep through memory; `vecs`
 // is chosen so that the last round is as full as the others.
 //
-// Bound.  The norm reads its bytes once: HBM (400M bf16 elements: 117 us, 6.85
-// TB/s, 103 % of the measured copy rate).  Clipping has to read everything
+// Bound.  The norm reads its bytes once: HBM (400M bf16 elements: 112.9 us, 7.1
+// TB/s, 106 % of the measured copy rate).  Clipping has to read everything
 // before it can write anything, so a set larger than the chip is read twice
 // and written once: 400M bf16 to bf16 367 us, 6.5 TB/s over 2.4 GB.  What the
 // chip holds it reads once:
@@ -31,8 +32,9 @@
 // while the CTAs exchange took 47 us.  Filling shared memory by bulk
 // copies, which do not, was no faster at 3.5 KB a copy (46 us here, but the
 // norm fell to 6.5 TB/s) and slower below: a bulk copy costs its SM some 50 ns.
-// Small sets are a launch, a trip to memory and the exchange: 0.2M f32
-// elements 4.7 us in a CUDA graph.
+// Small sets are a launch, a trip to memory and the join: the norm of 0.2M f32
+// elements 3.9 us, in a loop as in a CUDA graph (by the exchange, which needs
+// the cooperative launch, 6.2 and 4.5 us); clipping 1M elements 8.2 and 6.2 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -279,6 +281,29 @@ __device__ __forceinline__ float warp_part(float v)
         return __uint_as_float(__reduce_max_sync(kFullWarp, __float_as_uint(v)));
 }
 
+// The norm from the CTAs' norms, r[i] that of CTA 32 i + lane (0 beyond the last).
+template <int NORM>
+__device__ __forceinline__ float joined(const float *r)
+{
+    uint32_t most = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kStepMaxCtas / 32; ++i)
+        most = max(most, __float_as_uint(r[i]));
+    float norm = __uint_as_float(__reduce_max_sync(kFullWarp, most));
+    if (NORM == CNS_NORM_L2 && norm > 0.f && norm < INFINITY) {
+        // squares of the largest one's parts: nothing overflows
+        const float inverse = 1.f / norm;   // (of a norm below 2^-126 this is inf: then the parts as they are)
+        float sum = 0.f;
+#pragma unroll
+        for (uint32_t i = 0; i < kStepMaxCtas / 32; ++i) {
+            const float y = inverse < INFINITY ? r[i] * inverse : r[i] / norm;
+            sum = fmaf(y, y, sum);
+        }
+        norm *= sqrtf(warp_sum(sum));
+    }
+    return norm;
+}
+
 template <int D>
 __device__ __forceinline__ uint32_t pack2(float a, float b)
 {
@@ -456,38 +481,32 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const __grid_constant
         s_part[warp] = part;
     __syncthreads();
     if (warp == 0) {
+        // CTAs exchange roots: a sum of squares that is out of range for 32 bits may have a norm that is not
         part = warp_part<NORM>(s_part[lane]);
         float norm = NORM == CNS_NORM_L2 ? sqrtf(part) : part;
-        if (gridDim.x > 1 && !stop) {
-            // CTAs exchange roots: a sum of squares that is out of range for 32 bits may have a norm that is not
-            send_all(p.header, gridDim.x, tag, __float_as_uint(norm));
-            float r[kStepMaxCtas / 32] = {};
-            stop = receive_all(p.header, gridDim.x, tag, p.timeout_ns, r);
-            uint32_t most = 0;
-#pragma unroll
-            for (float x : r)
-                most = max(most, __float_as_uint(x));
-            norm = __uint_as_float(__reduce_max_sync(kFullWarp, most));
-            if (NORM == CNS_NORM_L2 && norm > 0.f && norm < INFINITY) {
-                // squares of the largest root's parts: nothing overflows
-                const float inverse = 1.f / norm;   // (of a norm below 2^-126 this is inf: then the parts as they are)
-                float sum = 0.f;
-#pragma unroll
-                for (float x : r) {
-                    const float y = inverse < INFINITY ? x * inverse : x / norm;
-                    sum = fmaf(y, y, sum);
-                }
-                norm *= sqrtf(warp_sum(sum));
+        float r[kStepMaxCtas / 32] = {};
+        bool mine = blockIdx.x == 0;   // to write the norm
+        if constexpr (CLIP) {
+            if (gridDim.x > 1 && !stop) {
+                send_all(p.header, gridDim.x, tag, __float_as_uint(norm));
+                stop = receive_all(p.header, gridDim.x, tag, p.timeout_ns, r);
+                norm = joined<NORM>(r);
+                if (!stop && blockIdx.x == 0 && lane == 0)
+                    st_relaxed_gpu(p.header + kStepEpochWord, tag);
             }
-            if (!stop && blockIdx.x == 0 && lane == 0)
-                st_relaxed_gpu(p.header + kStepEpochWord, tag);
+        } else if (gridDim.x > 1) {
+            mine = gather_last(p.header, gridDim.x, __float_as_uint(norm), r);
+            if (mine)
+                norm = joined<NORM>(r);
         }
         if (lane == 0) {
-            if (blockIdx.x == 0 && !stop)
+            if (mine && !stop)
                 *p.norm = norm;
-            const float f = p.max_norm / (norm + p.eps);
-            s_factor = f < 1.f || f != f ? f : 1.f;
-            s_stop = stop;
+            if constexpr (CLIP) {
+                const float f = p.max_norm / (norm + p.eps);
+                s_factor = f < 1.f || f != f ? f : 1.f;
+                s_stop = stop;
+            }
         }
     }
     if constexpr (!CLIP)
@@ -592,7 +611,7 @@ int launch(const cns_grad_clip_t &g, const GradParams &p, int ctas)
         }
     }
     cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = ctas > 1 ? together_launch(&attr) : early_launch(&attr);
+    cudaLaunchConfig_t cfg = CLIP && ctas > 1 ? together_launch(&attr) : early_launch(&attr);
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;

@@ -15,6 +15,7 @@ namespace cns {
 // Workspace header (cns_step_workspace_init zeroes it), in 32-bit words.
 constexpr uint32_t kStepEpochWord = 0;                             // line 0: calls done on this workspace
 constexpr uint32_t kStepRouteWord = 1;                             // of them, routings
+constexpr uint32_t kStepTicketWord = 2;                            // CTAs that gather_last has seen
 constexpr uint32_t kStepStatusWord = CNS_SYNCALL_LINE_BYTES / 4;   // line 1: status, abort, round, CTA
 constexpr uint32_t kStepBoxWord = 2048;                            // byte 8192: the mailboxes
 constexpr uint32_t kStepMaxCtas = 160;
@@ -160,6 +161,36 @@ __device__ __forceinline__ bool receive_all(uint32_t *header, uint32_t ctas, uin
         value[i] = *reinterpret_cast<const T *>(&v);
     }
     return false;
+}
+
+// Where only the result leaves the GPU, nobody has to wait: every CTA leaves
+// its value in the first row of mailboxes (under tag 0, which no call polls
+// for) and the last one to do so gets them all.  The calling warp gets true in
+// that CTA, with value[i] as receive_all fills it.
+template <class T>
+__device__ __forceinline__ bool gather_last(uint32_t *header, uint32_t ctas, uint32_t value, T *values)
+{
+    static_assert(sizeof(T) == 4, "values are 32-bit words");
+    const uint32_t lane = threadIdx.x & 31u;
+    uint32_t before = 0;
+    if (lane == 0) {
+        st_relaxed_gpu_u64(mailbox(header, 0, blockIdx.x), value);
+        fence_release_gpu();
+        before = atom_add_relaxed_gpu(header + kStepTicketWord, 1u);
+        fence_acquire_gpu();
+    }
+    if (__shfl_sync(kFullWarp, before, 0) != ctas - 1u)
+        return false;
+    __syncwarp();
+#pragma unroll
+    for (uint32_t i = 0; i < kStepMaxCtas / 32; ++i) {
+        const uint32_t v =
+            32 * i + lane < ctas ? static_cast<uint32_t>(ld_relaxed_gpu_u64(mailbox(header, 0, 32 * i + lane))) : 0u;
+        values[i] = *reinterpret_cast<const T *>(&v);
+    }
+    if (lane == 0)
+        st_relaxed_gpu(header + kStepTicketWord, 0u);   // for the next call
+    return true;
 }
 
 // e^x where 2^-22 is enough (sums, and what an exact value replaces): off by a relative 2^-22 + 2^-23 |x|; tiny results are 0.

@@ -239,6 +239,36 @@ def test_a_failed_workspace_is_refused_until_it_is_initialised(cns):
     assert abs(cns.run_grad_clip(plan, sync=True).item() - np.sqrt(3e6)) < 0.01
 
 
+def test_a_failed_workspace_refuses_the_norm_too(cns):
+    import torch
+    plan = cns.new_grad_clip([torch.ones(3_000_000, device="cuda")], 1.0)
+    plan.norm.fill_(-1.0)
+    plan.workspace[32] = cns.CNS_ERR_TIMEOUT
+    plan.workspace[33] = 1
+    with pytest.raises(cns.CnsError):
+        cns.run_grad_norm(plan, sync=True)
+    assert plan.norm.item() == -1.0
+    cns.check(cns.cns_step_workspace_init(plan.workspace, plan.workspace.numel() * 4))
+    assert abs(cns.run_grad_norm(plan, sync=True).item() - np.sqrt(3e6)) < 0.01
+
+
+def test_norms_and_clippings_of_all_sizes_share_a_workspace(cns):
+    """One after the other without a wait between them: the same bits as each alone."""
+    import torch
+    sizes = [7, 40_000, 3_000_000, 900_000, 1]
+    grads = [torch.randn(n, device="cuda") for n in sizes]
+    ws = cns.new_step_workspace(cns.cns_grad_workspace_bytes(1)[1])
+    plans = [cns.new_grad_clip([g], 1.0, outs=[torch.empty_like(g)], workspace=ws) for g in grads]
+    alone = [cns.run_grad_norm(cns.new_grad_clip([g]), sync=True).item() for g in grads]
+    got = []
+    for i in range(40):
+        plan = plans[i % 5]
+        got.append((cns.run_grad_clip if i % 3 == 0 else cns.run_grad_norm)(plan).clone())
+    torch.cuda.synchronize()
+    assert [g.item() for g in got] == [alone[i % 5] for i in range(40)]
+    assert cns.syncall_read_workspace(ws)[3] == 0
+
+
 def test_python_refusals(cns):
     import torch
     a = torch.zeros(64, device="cuda")
