@@ -85,7 +85,7 @@ CNS_SCORE_SIGMOID = 0
 CNS_SCORE_SOFTMAX = 1
 CNS_NORM_L2 = 0
 CNS_NORM_INF = 1
-CNS_STEP_WORKSPACE_HEADER_BYTES = 253952
+CNS_STEP_WORKSPACE_HEADER_BYTES = 233472
 CNS_STEP_WORKSPACE_ALIGN = 128
 CNS_ROUTE_MAX_EXPERTS = 512
 CNS_ROUTE_MAX_TOP_K = 32

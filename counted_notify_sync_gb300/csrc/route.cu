@@ -1,8 +1,8 @@
 // route.cu -- routing tokens to experts (cns_route) and its gradient
 // (cns_route_backward).
 //
-// The entry points, and the gradient's kernel.  The routing kernel is in
-// route_kernels.cuh.
+// The entry points, the kernels of the plan and of the gradient.  The routing
+// kernel is in route_kernels.cuh.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -15,6 +15,101 @@
 
 namespace cns {
 namespace {
+
+constexpr int kPlanHeld = 4;   // batches of a warp's tokens whose ids stay in registers
+
+// The plan of a routing by several CTAs: a grid of its own, as large as the one that chose.  Its CTAs set up while
+// that one's last are still choosing.
+__global__ void __launch_bounds__(kRouteWarps * 32, 1) route_plan_kernel(const __grid_constant__ RouteParams p)
+{
+    extern __shared__ uint32_t smem[];
+    __shared__ int s_stop;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int E = p.experts, e = threadIdx.x;
+    const uint32_t cta = blockIdx.x, ctas = gridDim.x;
+    const Stretch mine(p.tokens, warp, warps);
+    const int seg = place_lanes(p), per = 32 / seg, place = lane & (seg - 1);
+    uint32_t *s_count = smem;
+    for (int i = threadIdx.x; i < warps * E; i += blockDim.x)
+        s_count[i] = 0u;
+    __syncthreads();
+    grid_dependency_wait();   // all choices, and all CTAs' counts
+    // all loads before the first use of any: the workspace's status, the ids of the warp's first batches of tokens,
+    // the sums of the blocks and the counts of the CTA's block for expert e
+    const bool stop = threadIdx.x == 0 && ld_relaxed_gpu(p.header + kStepStatusWord + 1) != 0u;   // an earlier call failed
+    auto id_of = [&](int64_t t) { return t < mine.last && place < p.top_k ? p.ids[t * p.top_k + place] : -1; };
+    int held[kPlanHeld];
+    int64_t t = mine.first + lane / seg;
+#pragma unroll
+    for (int i = 0; i < kPlanHeld; ++i, t += per)
+        held[i] = id_of(t);
+    uint32_t before = 0, total = 0;
+    if (e < E) {
+        constexpr uint32_t kBlocks = kStepMaxCtas / kStepBlockCtas;
+        const uint32_t block = cta / kStepBlockCtas, *counts = p.counts + e;
+        uint32_t c[kBlocks], r[kStepBlockCtas];
+#pragma unroll
+        for (uint32_t i = 0; i < kBlocks; ++i)
+            c[i] = i * kStepBlockCtas < ctas ? __ldcg(block_sums(p, i) + e) : 0u;
+#pragma unroll
+        for (uint32_t i = 0; i < kStepBlockCtas; ++i)
+            r[i] = block * kStepBlockCtas + i < cta ? __ldcg(counts + (block * kStepBlockCtas + i) * E) : 0u;
+#pragma unroll
+        for (uint32_t i = 0; i < kBlocks; ++i) {
+            total += c[i];
+            before += i < block ? c[i] : 0u;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kStepBlockCtas; ++i)
+            before += r[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kPlanHeld; ++i)
+        if (held[i] >= 0)
+            atomicAdd(&s_count[warp * E + held[i]], 1u);
+    for (; t - lane / seg < mine.last; t += per) {
+        const int id = id_of(t);
+        if (id >= 0)
+            atomicAdd(&s_count[warp * E + id], 1u);
+    }
+    if (threadIdx.x == 0)
+        s_stop = stop;
+    __syncthreads();
+    if (s_stop)
+        return;
+    // every CTA has the sums when the last one says so; it clears them (and the count of those that said so)
+    uint32_t earlier = 0;
+    if (threadIdx.x == 0) {
+        fence_release_gpu();
+        earlier = atom_add_relaxed_gpu(p.header + kStepPlanWord, 1u);
+    }
+    place_entries(p, mine, held, before, total, s_count, s_count + warps * E, s_count + (warps + 1) * E);
+    if (warp == 0 && __shfl_sync(kFullWarp, earlier, 0) == ctas - 1u) {
+        fence_acquire_gpu();
+        for (uint32_t i = lane; i < kStepSumWords / 4; i += 32)
+            reinterpret_cast<uint4 *>(block_sums(p, 0u))[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (lane == 0)
+            st_relaxed_gpu(p.header + kStepPlanWord, 0u);
+    }
+}
+
+cudaError_t launch_plan(const RouteParams &p, int ctas, int warps, cudaStream_t s)
+{
+    const size_t smem = plan_smem(p, warps);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(route_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess)
+            return e;
+    }
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = early_launch(&attr);
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, route_plan_kernel, p);
+}
 
 struct RouteGradParams {
     const void *logits;
@@ -316,11 +411,11 @@ size_t workspace_bytes(int64_t, int32_t experts, int32_t)
     return CNS_STEP_WORKSPACE_HEADER_BYTES + sizeof(uint32_t) * kStepMaxCtas * static_cast<size_t>(experts);
 }
 
-// Up to this many tokens one CTA routes them all and needs no exchange (32 x 64 7.4 us against 8.3 us by eight
-// CTAs; 64 x 256 15.9 us against 11.7 us by sixteen).  Up to kSpreadTokens a CTA gets four tokens, since a warp
-// alone is latency and more warps to an SM slow one another (64 x 256: 11.7 us, with 32 a CTA 13.3); beyond them a
-// warp a token, with fewer CTAs to exchange with (1024 x 64: 9.8 us, with 4 a CTA 11.1), to one CTA an SM.
-constexpr int64_t kOneCtaTokens = 32, kSpreadTokens = 256;
+// Up to kOneCtaTokens one CTA routes them all, in one launch (32 x 64 5.4 us against 6.9 us by eight CTAs; 32 x 256
+// 10.2 against 9.8, 64 x 256 15.9 against 10.1).  More tokens go to as many CTAs as there are SMs, if each has
+// kLeastTokens: a warp alone is latency, and more warps to an SM slow one another (512 x 256 10.6 us, with eight
+// tokens a CTA 12.0, with 32 13.0; 3001 x 160 11.3 us on 152 CTAs, 11.5 on 94).
+constexpr int64_t kOneCtaTokens = 32, kLeastTokens = 4;
 
 bool sizes_ok(int64_t tokens, int32_t experts, int32_t top_k)
 {
@@ -405,7 +500,6 @@ extern "C" int cns_route(cns_route_t *r)
     p.renorm = r->renorm;
     p.scale = r->scale;
     p.key_step = 512u;
-    p.timeout_ns = barrier_timeout_ns(r->timeout_ms);
     p.header = static_cast<uint32_t *>(r->workspace_dev);
     p.counts = p.header + CNS_STEP_WORKSPACE_HEADER_BYTES / 4;
     if (r->tokens > 0 || plan) {
@@ -414,8 +508,7 @@ extern "C" int cns_route(cns_route_t *r)
             ctas = 1;
             warps = static_cast<int>(std::min<int64_t>(kRouteWarps, std::max<int64_t>(r->tokens, 4)));
         } else {
-            const int per = r->tokens <= kSpreadTokens ? 4 : kRouteWarps;
-            ctas = static_cast<int>(std::min<int64_t>((r->tokens + per - 1) / per,
+            ctas = static_cast<int>(std::min<int64_t>((r->tokens + kLeastTokens - 1) / kLeastTokens,
                                                       std::min<int>(dev.sm_count, kStepMaxCtas)));
             warps = kRouteWarps;
         }
@@ -423,13 +516,9 @@ extern "C" int cns_route(cns_route_t *r)
         const auto launch = r->dtype == CNS_DT_F32    ? (by_score ? launch_route_f32_score : launch_route_f32_logit)
                             : r->dtype == CNS_DT_BF16 ? (by_score ? launch_route_bf16_score : launch_route_bf16_logit)
                                                       : (by_score ? launch_route_f16_score : launch_route_f16_logit);
-        const cudaError_t e = launch(p, ctas, warps, s);
-        if (e == cudaErrorCooperativeLaunchTooLarge) {
-            (void)cudaGetLastError();
-            return CNS_ERR_NOT_RESIDENT;
-        }
-        if (e != cudaSuccess)
-            return cuda_fail(e, "route launch");
+        CNS_CUDA(launch(p, ctas, warps, s));
+        if (plan && ctas > 1)
+            CNS_CUDA(launch_plan(p, ctas, warps, s));
     }
     if (!r->sync)
         return CNS_SUCCESS;

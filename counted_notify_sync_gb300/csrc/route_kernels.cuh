@@ -26,18 +26,24 @@
 // are filled in rounds, one redux each.  Four tokens' weights (eight lanes
 // each) are computed together.  Now 640 instructions a token of 384 experts
 // with a bias, 68 % of the issue slots and 52 % of the half-rate pipe that
-// min, max and compare share: 65536 x 384 bf16 52.7 us, 16384 x 256 f32 with
-// groups 24.8 us (CUDA graph; 8.8 and 2.8 us of them are the bytes' time).
+// min, max and compare share: 65536 x 384 bf16 51 us, 16384 x 256 f32 with
+// groups 22.9 us (8.8 and 2.8 us of them are the bytes' time).
 //
 // Plan.  CTA b has a stretch of tokens and each of its warps a stretch of
-// those, so that entries in order are warps in order.  Phase 1 chooses and
-// counts per warp; the CTAs add their counts per expert to their block's (16
-// CTAs) and meet (step_device.cuh's exchange as a barrier); every CTA sums the
-// blocks and the rows of its block before its own, and phase 2 walks the tokens
-// again in order, each entry's place being its expert's running count.  Only
-// integer sums: the plan does not depend on timing.  The whole plan takes 6 us
-// of the 24.8: 1.3 to set up, 1.6 for the exchange after the last CTA has
-// chosen, 1.4 for the sums and their scan, 1.2 to place.
+// those, so that entries in order are warps in order.  The first grid chooses
+// and adds its counts per expert to those of its block of 16 CTAs; a second
+// grid over the same stretches (route_plan_kernel) counts each warp's ids
+// again, sums the blocks and the CTAs of its own block before it, and walks its
+// tokens in order, each entry's place being its expert's running count.  Only
+// integer sums: the plan does not depend on timing.  The second grid is
+// launched early: its CTAs take the places of the first one's as those end, and
+// set up while the last ones choose.  (As one cooperative grid with an exchange
+// between the phases the plan took as long in a CUDA graph, but 2 us more from
+// call to call in a stream, where such a launch cannot be early: 16384 x 256
+// 26.1 us against 22.9, 3001 x 160 14.4 against 11.9.)  Of 22.9 us the plan has
+// 5: 1.0 until the counts are there, 1.1 to load and count, 1.3 for the scans,
+// 1.3 to place.  What needs a 64-bit division is ready before the wait: two of
+// them a thread after it were 0.8 us.  A single CTA makes the plan itself.
 #pragma once
 
 #include "cns_host.h"
@@ -58,7 +64,6 @@ struct RouteParams {
     int32_t *places;
     uint32_t *header;    // of the workspace
     uint32_t *counts;    // [CTAs][experts], in the workspace
-    uint64_t timeout_ns;
     int64_t tokens;
     int64_t stride;
     int32_t experts, top_k, groups, top_groups, group_top;
@@ -76,6 +81,133 @@ cudaError_t launch_route_bf16_logit(const RouteParams &p, int ctas, int warps, c
 cudaError_t launch_route_bf16_score(const RouteParams &p, int ctas, int warps, cudaStream_t s);
 cudaError_t launch_route_f16_logit(const RouteParams &p, int ctas, int warps, cudaStream_t s);
 cudaError_t launch_route_f16_score(const RouteParams &p, int ctas, int warps, cudaStream_t s);
+
+// Lanes that a token's places take when tokens are handled several at a time.
+__device__ __forceinline__ int place_lanes(const RouteParams &p) { return p.top_k <= 8 ? 8 : 32; }
+
+// The tokens of a CTA, and of a warp of it: first .. last - 1.
+struct Stretch {
+    int64_t first, last;
+    __device__ __forceinline__ Stretch(int64_t tokens, int warp, int warps)
+    {
+        const int64_t begin = tokens * blockIdx.x / gridDim.x, end = tokens * (blockIdx.x + 1) / gridDim.x;
+        first = begin + (end - begin) * warp / warps;
+        last = begin + (end - begin) * (warp + 1) / warps;
+    }
+};
+
+// What the CTAs of a plan know of one another: for each expert the count of
+// each CTA, in p.counts, and of each block of 16 CTAs, so that nobody has to
+// read the counts of all CTAs (152 rows by 152 CTAs took 2.5 us).  The plan
+// leaves the blocks' sums cleared.
+__device__ __forceinline__ uint32_t *block_sums(const RouteParams &p, uint32_t block)
+{
+    return p.header + kStepSumWord + block * CNS_ROUTE_MAX_EXPERTS;
+}
+
+// The plan, by all threads of a CTA: places the entries of its tokens by
+// expert.  s_count: each warp's count of each expert; s_base, s_total: [E].
+// held: the ids of the lane's places in the warp's first HELD batches of
+// tokens.  before, total: with several CTAs, the entries of earlier ones and
+// of all, of expert threadIdx.x.
+template <int HELD>
+__device__ __forceinline__ void place_entries(const RouteParams &p, const Stretch &mine, const int (&held)[HELD],
+                                              uint32_t before, uint32_t total, uint32_t *s_count, uint32_t *s_base,
+                                              uint32_t *s_total)
+{
+    __shared__ uint32_t s_chunk[16];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int E = p.experts;
+    const uint32_t cta = blockIdx.x, ctas = gridDim.x;
+    // One thread an expert: counts of the CTA's warps become the counts before each warp; where the expert's list
+    // starts, by a scan over the experts, 32 to a warp.
+    for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+        const int e = e0 + threadIdx.x;
+        if (e < E) {
+            uint32_t run = 0u;
+            for (int w = 0; w < warps; w += 8) {
+                uint32_t n[8];   // loaded together, before any is stored
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    n[i] = w + i < warps ? s_count[(w + i) * E + e] : 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (w + i < warps)
+                        s_count[(w + i) * E + e] = run;
+                    run += n[i];
+                }
+            }
+            if (ctas == 1)
+                total = run;
+        } else {
+            total = 0u;
+        }
+        uint32_t run = total;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(kFullWarp, run, d);
+            run += lane >= d ? o : 0u;
+        }
+        if (lane == 31 && e - lane < E)
+            s_chunk[e / 32] = run;
+        if (e < E) {
+            s_base[e] = run - total + before;
+            s_total[e] = run;
+        }
+    }
+    __syncthreads();
+    uint32_t listed = 0;
+    for (int c = 0; c * 32 < E; ++c)
+        listed += s_chunk[c];
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        uint32_t earlier = 0;
+        for (int c = 0; c < e / 32; ++c)
+            earlier += s_chunk[c];
+        s_base[e] += earlier;
+        if (cta == 0) {
+            if (e == 0)
+                p.offsets[0] = 0;
+            p.offsets[e + 1] = static_cast<int32_t>(earlier + s_total[e]);
+        }
+    }
+    __syncthreads();
+
+    // the warp's tokens in order, a batch's entries of one expert ranked by their lanes
+    uint32_t *count = s_count + warp * E;
+    const int seg = place_lanes(p), per = 32 / seg, place = lane & (seg - 1);
+    auto put = [&](int64_t t, int id) {
+        const bool token = t < mine.last && place < p.top_k;
+        const uint32_t same = __match_any_sync(kFullWarp, id);
+        int at = -1;
+        if (id >= 0)
+            at = static_cast<int>(s_base[id] + count[id] + __popc(same & ((1u << lane) - 1u)));
+        __syncwarp();
+        if (id >= 0 && (same >> lane) == 1u)   // the last of them
+            count[id] += __popc(same);
+        __syncwarp();
+        if (token) {
+            const int64_t entry = t * p.top_k + place;
+            if (id >= 0)
+                p.order[at] = static_cast<int32_t>(entry);
+            if (p.places)
+                p.places[entry] = at;
+        }
+    };
+    int64_t t = mine.first + lane / seg;
+#pragma unroll
+    for (int i = 0; i < HELD; ++i, t += per)
+        if (t - lane / seg < mine.last)
+            put(t, held[i]);
+    for (; t - lane / seg < mine.last; t += per)
+        put(t, t < mine.last && place < p.top_k ? p.ids[t * p.top_k + place] : -1);
+    // places that no entry takes
+    const uint32_t n = static_cast<uint32_t>(p.tokens) * p.top_k;
+    for (uint32_t i = listed + cta * blockDim.x + threadIdx.x; i < n; i += ctas * blockDim.x)
+        p.order[i] = -1;
+}
+
+// Shared memory of place_entries.
+inline size_t plan_smem(const RouteParams &p, int warps) { return sizeof(uint32_t) * (warps + 2) * p.experts; }
 
 #ifdef CNS_ROUTE_KERNELS
 
@@ -518,8 +650,11 @@ __device__ __forceinline__ float seg_max(float v, int seg)
     return v;
 }
 
-// Lanes that a token's places take when tokens are handled several at a time.
-__device__ __forceinline__ int place_lanes(const RouteParams &p) { return p.top_k <= 8 ? 8 : 32; }
+// Whether a token's keys go through shared memory, for groups that are not one row of 32 experts.
+__host__ __device__ __forceinline__ bool odd_groups(const RouteParams &p)
+{
+    return p.groups > 1 && p.experts / p.groups != 32;
+}
 
 // Rows of 32 experts that the next narrower kernel has (launch_route).
 __host__ __device__ constexpr int narrower(int v)
@@ -759,6 +894,7 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
     return done;
 }
 
+// Chooses, and counts if there is a plan; a single CTA makes the plan too.
 template <int D, int V, bool SCORES, bool GROUPS>
 __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid_constant__ RouteParams p)
 {
@@ -766,39 +902,29 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int E = p.experts;
     const uint32_t cta = blockIdx.x, ctas = gridDim.x;
-    uint32_t *s_count = smem;                                          // [warps][E]
-    uint32_t *s_base = s_count + (p.plan ? warps * E : 0);             // [E]
-    uint32_t *s_total = s_base + E;                                    // [E]
-    float *s_bias = reinterpret_cast<float *>(s_total + E);            // [32 V]
-    uint32_t *s_keys = reinterpret_cast<uint32_t *>(s_bias) + 32 * V;  // [warps][E], groups of other sizes than 32
-    __shared__ uint32_t s_chunk[16];
-    __shared__ uint32_t s_tag, s_turn;
+    const bool alone = ctas == 1;
+    float *s_bias = reinterpret_cast<float *>(smem);                       // [32 V]
+    uint32_t *s_keys = smem + 32 * V;                                      // [warps][E], groups of other sizes than 32
+    uint32_t *s_count = s_keys + (odd_groups(p) ? warps * E : 0);          // [E], or for a single CTA [warps][E]
     __shared__ int s_stop, s_reach;
     __shared__ uint16_t s_near[kRouteWarps][32];   // experts that a token's choice is between
 
-    grid_dependency_wait();   // launched early: nothing of the tensors or the workspace before this
-    // what the workspace says, read by one thread of a CTA: all threads' loads of one line took 2 us
-    uint32_t tag = 0, turn = 0;
-    bool stop = false;
-    if (p.plan && threadIdx.x == 0) {
-        tag = ld_relaxed_gpu(p.header + kStepEpochWord) + 1u;
-        turn = ld_relaxed_gpu(p.header + kStepRouteWord) + 1u;
-        stop = ld_relaxed_gpu(p.header + kStepStatusWord + 1) != 0u;   // an earlier call failed
-    }
-    // the warp's stretch of tokens; its first row and the biases are on their way while the CTA sets up
-    const int64_t begin = p.tokens * cta / ctas, end = p.tokens * (cta + 1) / ctas;
-    const int64_t first = begin + (end - begin) * warp / warps, last = begin + (end - begin) * (warp + 1) / warps;
-    if (first < last && lane < V) {
-        const int e = min(lane * 32, E - 1);
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const typename Elem<D>::type *>(p.logits) +
-                                                      first * p.stride + e));
-    }
-    float b = p.bias && static_cast<int>(threadIdx.x) < E ? p.bias[threadIdx.x] : 0.f;
+    const Stretch mine(p.tokens, warp, warps);
     if (threadIdx.x == 0)
         s_reach = 0;
     if (p.plan)
-        for (int i = threadIdx.x; i < warps * E; i += blockDim.x)
+        for (int i = threadIdx.x; i < (alone ? warps * E : E); i += blockDim.x)
             s_count[i] = 0u;
+    grid_dependency_wait();   // launched early: nothing of the tensors or the workspace before this
+    if (p.plan && !alone)
+        grid_launch_dependents();   // the plan's CTAs take the places of this grid's as those end
+    // the warp's first row and the biases are on their way while the CTA sets up
+    if (mine.first < mine.last && lane < V) {
+        const int e = min(lane * 32, E - 1);
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const typename Elem<D>::type *>(p.logits) +
+                                                      mine.first * p.stride + e));
+    }
+    float b = p.bias && static_cast<int>(threadIdx.x) < E ? p.bias[threadIdx.x] : 0.f;
     __syncthreads();
     if (SCORES) {
         for (int e = threadIdx.x; e < 32 * V; e += blockDim.x) {
@@ -815,167 +941,39 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     }
 
     const float reach = 1.f + __int_as_float(s_reach);
-    const int done =
-        choose_tokens<D, V, SCORES, GROUPS>(p, first, last, s_bias, reach <= kMostBias ? reach : NAN, s_keys + warp * E,
-                                            s_near[warp], s_count + warp * E);
+    const int done = choose_tokens<D, V, SCORES, GROUPS>(p, mine.first, mine.last, s_bias,
+                                                         reach <= kMostBias ? reach : NAN, s_keys + warp * E,
+                                                         s_near[warp], s_count + (alone ? warp * E : 0));
     if (!p.plan)
         return;
-
-    // Counts of the CTA's warps become the counts before each warp.  The CTA's own go to its row and are added
-    // to its block's (16 CTAs), so that nobody has to read the rows of all CTAs: 152 rows by 152 CTAs took 2.5 us.
-    // The blocks' sums are kept twice; a call uses one, and clears the other for the next call.
-    if (threadIdx.x == 0) {
-        s_tag = tag;
-        s_turn = turn;
-        s_stop = stop;
-    }
+    if (threadIdx.x == 0)   // read by one thread of a CTA: all threads' loads of one line took 2 us
+        s_stop = alone && ld_relaxed_gpu(p.header + kStepStatusWord + 1) != 0u;   // an earlier call failed
     __syncthreads();
-    tag = s_tag;
-    turn = s_turn;
-    stop = s_stop != 0;
-    uint32_t *sums = p.header + kStepSumWord + (turn & 1u) * kStepSumWords;
-    uint32_t *stale = p.header + kStepSumWord + ((turn & 1u) ^ 1u) * kStepSumWords;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        uint32_t run = 0u;
-        for (int w = 0; w < warps; w += 8) {
-            uint32_t c[8];   // loaded together, before any is stored
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                c[i] = w + i < warps ? s_count[(w + i) * E + e] : 0u;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (w + i < warps)
-                    s_count[(w + i) * E + e] = run;
-                run += c[i];
-            }
-        }
-        s_base[e] = run;
-        if (ctas > 1 && !stop) {
-            p.counts[cta * E + e] = run;
-            if (run)
-                red_add_relaxed_gpu(sums + cta / kStepBlockCtas * CNS_ROUTE_MAX_EXPERTS + e, run);
-        }
-    }
-    if (ctas > 1) {
-        __syncthreads();
-        if (warp == 0) {
-            if (!stop) {
-                fence_release_gpu();
-                send_all(p.header, ctas, tag, 0u);
-                uint32_t none[kStepMaxCtas / 32];
-                stop = receive_all(p.header, ctas, tag, p.timeout_ns, none);
-                fence_acquire_gpu();
-                if (!stop && cta == 0 && lane == 0) {
-                    st_relaxed_gpu(p.header + kStepEpochWord, tag);
-                    st_relaxed_gpu(p.header + kStepRouteWord, turn);
-                }
-            }
-            if (lane == 0)
-                s_stop = stop;
-        }
-        __syncthreads();
-    }
-    if (s_stop)
+    if (alone) {
+        const int held[1] = {done};   // a warp of a single CTA has a token at most, or a batch of them
+        if (!s_stop)
+            place_entries(p, mine, held, 0u, 0u, s_count, s_count + warps * E, s_count + (warps + 1) * E);
         return;
-    if (ctas > 1)
-        for (uint32_t i = cta * blockDim.x + threadIdx.x; i < kStepSumWords; i += ctas * blockDim.x)
-            stale[i] = 0u;
-    // One thread an expert: the entries of earlier CTAs and of all; where its list starts, by a scan over the
-    // experts, 32 to a warp.
-    for (int e0 = 0; e0 < E; e0 += blockDim.x) {
-        const int e = e0 + threadIdx.x;
-        uint32_t before = 0, total = 0;
-        if (e < E && ctas > 1) {
-            const uint32_t block = cta / kStepBlockCtas;
-            uint32_t c[kStepMaxCtas / kStepBlockCtas], r[kStepBlockCtas];
-#pragma unroll
-            for (uint32_t i = 0; i < kStepMaxCtas / kStepBlockCtas; ++i)
-                c[i] = i * kStepBlockCtas < ctas ? __ldcg(sums + i * CNS_ROUTE_MAX_EXPERTS + e) : 0u;
-#pragma unroll
-            for (uint32_t i = 0; i < kStepBlockCtas; ++i)
-                r[i] = block * kStepBlockCtas + i < cta ? __ldcg(p.counts + (block * kStepBlockCtas + i) * E + e) : 0u;
-#pragma unroll
-            for (uint32_t i = 0; i < kStepMaxCtas / kStepBlockCtas; ++i) {
-                total += c[i];
-                before += i < block ? c[i] : 0u;
-            }
-#pragma unroll
-            for (uint32_t i = 0; i < kStepBlockCtas; ++i)
-                before += r[i];
-        } else if (e < E) {
-            total = s_base[e];
-        }
-        uint32_t run = total;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t o = __shfl_up_sync(kFullWarp, run, d);
-            run += lane >= d ? o : 0u;
-        }
-        if (lane == 31 && e - lane < E)
-            s_chunk[e / 32] = run;
-        if (e < E) {
-            s_base[e] = run - total + before;
-            s_total[e] = run;
-        }
     }
-    __syncthreads();
-    uint32_t listed = 0;
-    for (int c = 0; c * 32 < E; ++c)
-        listed += s_chunk[c];
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        uint32_t earlier = 0;
-        for (int c = 0; c < e / 32; ++c)
-            earlier += s_chunk[c];
-        s_base[e] += earlier;
-        if (cta == 0) {
-            if (e == 0)
-                p.offsets[0] = 0;
-            p.offsets[e + 1] = static_cast<int32_t>(earlier + s_total[e]);
-        }
+        const uint32_t n = s_count[e];
+        p.counts[cta * E + e] = n;
+        if (n)
+            red_add_relaxed_gpu(block_sums(p, cta / kStepBlockCtas) + e, n);
     }
-    __syncthreads();
-
-    // phase 2: the same tokens in the same order, a batch's entries of one expert ranked by their lanes
-    uint32_t *count = s_count + warp * E;
-    const int seg = place_lanes(p), per = 32 / seg, place = lane & (seg - 1);
-    for (int64_t t = first + lane / seg; t - lane / seg < last; t += per) {
-        const bool token = t < last && place < p.top_k;
-        const int64_t entry = t * p.top_k + place;
-        const int id = last - first <= per ? done : token ? p.ids[entry] : -1;
-        const uint32_t same = __match_any_sync(kFullWarp, id);
-        int at = -1;
-        if (id >= 0)
-            at = static_cast<int>(s_base[id] + count[id] + __popc(same & ((1u << lane) - 1u)));
-        __syncwarp();
-        if (id >= 0 && (same >> lane) == 1u)   // the last of them
-            count[id] += __popc(same);
-        __syncwarp();
-        if (token) {
-            if (id >= 0)
-                p.order[at] = static_cast<int32_t>(entry);
-            if (p.places)
-                p.places[entry] = at;
-        }
-    }
-    // places that no entry takes
-    const int64_t n = p.tokens * p.top_k;
-    const int64_t from = max(n * cta / ctas, static_cast<int64_t>(listed));
-    for (int64_t i = from + threadIdx.x; i < n * (cta + 1) / ctas; i += blockDim.x)
-        p.order[i] = -1;
 }
 
-inline size_t route_smem(const RouteParams &p, int V, int warps)
+inline size_t route_smem(const RouteParams &p, int V, int ctas, int warps)
 {
-    const bool odd_groups = p.groups > 1 && p.experts / p.groups != 32;
-    return sizeof(uint32_t) * ((p.plan ? warps * p.experts : 0) + 2 * p.experts + 32 * V +
-                               (odd_groups ? warps * p.experts : 0));
+    return sizeof(uint32_t) * (32 * V + (odd_groups(p) ? warps * p.experts : 0) + (p.plan && ctas > 1 ? p.experts : 0)) +
+           (p.plan && ctas == 1 ? plan_smem(p, warps) : 0);
 }
 
 template <int D, int V, bool SCORES, bool GROUPS>
 cudaError_t launch_route_v(const RouteParams &p, int ctas, int warps, cudaStream_t s)
 {
     const auto kernel = route_kernel<D, V, SCORES, GROUPS>;
-    const size_t smem = route_smem(p, V, warps);
+    const size_t smem = route_smem(p, V, ctas, warps);
     if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -983,7 +981,7 @@ cudaError_t launch_route_v(const RouteParams &p, int ctas, int warps, cudaStream
             return e;
     }
     cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = p.plan && ctas > 1 ? together_launch(&attr) : early_launch(&attr);
+    cudaLaunchConfig_t cfg = early_launch(&attr);
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = smem;

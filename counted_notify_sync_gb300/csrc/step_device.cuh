@@ -13,16 +13,16 @@
 namespace cns {
 
 // Workspace header (cns_step_workspace_init zeroes it), in 32-bit words.
-constexpr uint32_t kStepEpochWord = 0;                             // line 0: calls done on this workspace
-constexpr uint32_t kStepRouteWord = 1;                             // of them, routings
+constexpr uint32_t kStepEpochWord = 0;                             // line 0: exchanges done on this workspace
+constexpr uint32_t kStepPlanWord = 1;                              // CTAs of a plan that have the blocks' sums
 constexpr uint32_t kStepTicketWord = 2;                            // CTAs that gather_last has seen
 constexpr uint32_t kStepStatusWord = CNS_SYNCALL_LINE_BYTES / 4;   // line 1: status, abort, round, CTA
 constexpr uint32_t kStepBoxWord = 2048;                            // byte 8192: the mailboxes
 constexpr uint32_t kStepMaxCtas = 160;
 constexpr uint32_t kStepBlockCtas = 16;                            // CTAs whose counts are summed together
-constexpr uint32_t kStepSumWord = kStepBoxWord + 2 * kStepMaxCtas * kStepMaxCtas;   // [2][blocks][experts] of route.cu
+constexpr uint32_t kStepSumWord = kStepBoxWord + 2 * kStepMaxCtas * kStepMaxCtas;   // [blocks][experts] of route.cu
 constexpr uint32_t kStepSumWords = kStepMaxCtas / kStepBlockCtas * CNS_ROUTE_MAX_EXPERTS;
-static_assert(4 * (kStepSumWord + 2 * kStepSumWords) == CNS_STEP_WORKSPACE_HEADER_BYTES, "header layout");
+static_assert(4 * (kStepSumWord + kStepSumWords) == CNS_STEP_WORKSPACE_HEADER_BYTES, "header layout");
 
 // Launches of CTAs that wait for one another: cooperative, so that all are on the GPU together.
 inline cudaLaunchConfig_t together_launch(cudaLaunchAttribute *a)

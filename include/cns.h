@@ -698,10 +698,11 @@ int cns_pipeline_run(cns_pipeline_t *cfg);
 /* ========================================================================= */
 
 /* Operators in which every CTA needs a part from every other CTA before any
- * can go on, run as the library's persistent kernels are: data phase; all
- * CTAs meet; data phase.  Routing tokens to experts (choose and count; meet;
- * place the entries by expert) with its gradient, and the global gradient
- * norm over many tensors with clipping (sum; meet; scale). */
+ * can go on.  Clipping by the global gradient norm over many tensors runs as
+ * the library's persistent kernels do: data phase (sum); all CTAs meet; data
+ * phase (scale).  Routing tokens to experts (choose and count; place the
+ * entries by expert) takes two grids, the second set up while the first ends;
+ * the norm alone and the routing's gradient take one. */
 
 /* Element types of the tensors below. */
 typedef enum { CNS_DT_F32 = 0, CNS_DT_BF16 = 1, CNS_DT_F16 = 2 } cns_dtype_t;
@@ -715,7 +716,7 @@ typedef enum { CNS_DT_F32 = 0, CNS_DT_BF16 = 1, CNS_DT_F16 = 2 } cns_dtype_t;
  * one each.  A call that fails on the device (a bounded wait that ran out)
  * leaves its status and incomplete outputs, and so do later calls on the
  * workspace until it is initialised again. */
-#define CNS_STEP_WORKSPACE_HEADER_BYTES 253952
+#define CNS_STEP_WORKSPACE_HEADER_BYTES 233472
 #define CNS_STEP_WORKSPACE_ALIGN 128
 
 /*
@@ -780,9 +781,9 @@ typedef struct {
     int32_t group_top;       /* (in) 1 or 2; 0 = 1 */
     int32_t renorm;          /* (in) 0 or 1 */
     float scale;             /* (in) finite */
-    uint32_t timeout_ms;     /* (in) bound on each wait; 0 = library default, as in syncall_run */
+    uint32_t timeout_ms;     /* (in) without effect: a routing's CTAs do not wait for one another */
     int32_t sync;            /* (in) 1: wait for the call and return its status; 0: enqueue and return */
-    int32_t device_status;   /* (out, sync=1) 0 or CNS_ERR_TIMEOUT */
+    int32_t device_status;   /* (out, sync=1) 0, or CNS_ERR_TIMEOUT if an earlier call on the workspace left it */
 } cns_route_t;
 
 /* Workspace bytes for a plan of up to `tokens` tokens.  Host only.
@@ -794,7 +795,7 @@ int cns_route_workspace_bytes(int64_t tokens, int32_t experts, int32_t top_k, si
  * entries by expert.  Asynchronous on `stream` unless sync; with sync = 0 the
  * call may be captured into a CUDA graph.
  * Errors: NULL_PTR, INVALID_VALUE (sizes, enums, alignment to the element,
- * workspace), ARCH, NOT_RESIDENT, CUDA; with sync=1 also TIMEOUT.
+ * workspace), ARCH, CUDA; with sync=1 also TIMEOUT.
  */
 int cns_route(cns_route_t *r);
 
@@ -860,9 +861,9 @@ typedef struct {
     int32_t norm_type;         /* (in) cns_norm_t */
     float max_norm;            /* (in) >= 0 (cns_grad_clip only) */
     float eps;                 /* (in) >= 0, finite (cns_grad_clip only) */
-    uint32_t timeout_ms;       /* (in) as cns_route_t */
+    uint32_t timeout_ms;       /* (in) bound on each wait of a clipping; 0 = library default, as in syncall_run */
     int32_t sync;              /* (in) as cns_route_t */
-    int32_t device_status;     /* (out, sync=1) as cns_route_t */
+    int32_t device_status;     /* (out, sync=1) 0 or CNS_ERR_TIMEOUT */
 } cns_grad_clip_t;
 
 #define CNS_GRAD_MAX_TENSORS 1048576
@@ -877,8 +878,8 @@ int cns_grad_workspace_bytes(int64_t count, size_t *bytes);
  * asynchronous on `stream` unless sync; with sync = 0 they may be captured
  * into a CUDA graph (the tensors' addresses are then the capture's).
  * Errors: NULL_PTR, INVALID_VALUE (count, sizes, enums, alignment, workspace,
- * max_norm or eps out of range), ARCH, NOT_RESIDENT, CUDA; with sync=1 also
- * TIMEOUT.
+ * max_norm or eps out of range), ARCH, NOT_RESIDENT (cns_grad_clip), CUDA;
+ * with sync=1 also TIMEOUT.
  */
 int cns_grad_norm(cns_grad_clip_t *g);
 int cns_grad_clip(cns_grad_clip_t *g);
