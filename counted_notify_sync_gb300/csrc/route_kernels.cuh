@@ -24,10 +24,13 @@
 // first and second ones go through a sorting network (23 exchanges), and if a
 // third one belongs in, or more than eight places are asked for, the places
 // are filled in rounds, one redux each.  Four tokens' weights (eight lanes
-// each) are computed together.  Now 640 instructions a token of 384 experts
-// with a bias, 68 % of the issue slots and 52 % of the half-rate pipe that
-// min, max and compare share: 65536 x 384 bf16 51 us, 16384 x 256 f32 with
-// groups 22.9 us (8.8 and 2.8 us of them are the bytes' time).
+// each) are computed together.  A bias is part of the offset that a score's
+// scaling adds anyway, and keys of one lane carry its number only once they meet
+// those of others (not where groups are compared).  Now 530 instructions a token
+// of 384 experts with a bias, 76 % of the issue slots and 61 % of the half-rate
+// pipe that min, max and compare share (the plan has 70 more): 65536 x 384 bf16
+// 49 us, 16384 x 256 f32 with groups 23 us (8.8 and 2.8 us of them are the
+// bytes' time).
 //
 // Plan.  CTA b has a stretch of tokens and each of its warps a stretch of
 // those, so that entries in order are warps in order.  The first grid chooses
@@ -311,7 +314,8 @@ constexpr float kQuanta = kLeastQuanta - 64.f;
 // score's: s (2^-22 + 2^-23 |x - top|) and two roundings, below 4e-7); what keeps
 // masked experts out adds at most 4.8e-7.  The exact score in 32 bits is within
 // 1.8e-7 of the true one, and the sums with the bias round to 2^-24 of reach
-// each.  Two values, and the quanta round too.
+// each, as the near one's offset with the bias in it does.  Two values, and the
+// quanta round too.
 __device__ __forceinline__ KeyRules score_rules(float reach)
 {
     KeyRules r;
@@ -607,7 +611,7 @@ __device__ __noinline__ bool settle(const RouteParams &p, const typename Elem<D>
         const bool in = key[i] > least;
         const uint32_t at = __ballot_sync(kFullWarp, in), to = count + __popc(at & earlier);
         if (in && to < 32u)
-            s_near[to] = static_cast<uint16_t>(511u - (key[i] & 511u));
+            s_near[to] = static_cast<uint16_t>(32 * i + lane);
         count += __popc(at);
     }
     if (count > 32u)
@@ -663,14 +667,14 @@ __host__ __device__ constexpr int narrower(int v)
 }
 
 // Choose and weigh the experts of the tokens first .. last - 1 by the calling
-// warp; counts each expert's in s_count if there is a plan.  s_bias: of expert
-// e, 0 if there is no bias, kNever where it is -inf and beyond the last expert;
-// reach: 1 plus the largest magnitude among the others, or NaN if they are
-// nothing that the fast path is made for.
+// warp; counts each expert's in s_count if there is a plan.  s_offset: what the
+// scaled score of expert e is added to, kNever where the bias is -inf and beyond
+// the last expert; reach: 1 plus the largest magnitude among the other biases,
+// or NaN if they are nothing that the fast path is made for.
 // Returns the last batch's expert of the lane's place: of all tokens, if they
 // are one batch.
 template <int D, int V, bool SCORES, bool GROUPS>
-__device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first, int64_t last, const float *s_bias,
+__device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first, int64_t last, const float *s_offset,
                                               float reach, uint32_t *s_key, uint16_t *s_near, uint32_t *s_count)
 {
     using T = typename Elem<D>::type;
@@ -678,6 +682,8 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
     constexpr bool by_logit = !SCORES;
     const bool whole = p.softmax && (p.scores || !p.renorm || !by_logit);   // needs the softmax over all experts
     constexpr bool packs = D != CNS_DT_F32 && by_logit;
+    // keys of a lane need not say which lane's they are until they meet other lanes'
+    constexpr bool lanes_later = !packs && !GROUPS;
     const KeyRules rules = packs ? packed_rules() : by_logit ? logit_rules() : score_rules(reach);
     // e / size by a product: exact for e < 512 and sizes up to 256
     const int size = p.experts / p.groups;
@@ -737,21 +743,21 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
                 // rate, and the keys' comparisons below are many of them.  So the clamp is a saturating product,
                 // and the shift a product by a number that the compiler cannot turn into one.
                 float all = 0.f, some = 0.f;   // NaN or inf if any value is; 0 if every expert is masked
-                auto take = [&](int i, float v) {
+                auto take = [&](int i, float v, float offset) {
                     all += v;
                     float part;
-                    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(part) : "f"(v), "f"(rules.scale), "f"(rules.offset));
-                    some += part;
-                    key[i] = __float_as_uint(fmaf(part, kQuanta, kLeastQuanta)) * p.key_step + (511u - 32u * i - lane);
+                    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(part) : "f"(v), "f"(rules.scale), "f"(offset));
+                    if (GROUPS)
+                        some += part;
+                    key[i] = __float_as_uint(fmaf(part, kQuanta, kLeastQuanta)) * p.key_step +
+                             (lanes_later ? 480u - 32u * i : 511u - 32u * i - lane);
                 };
-                // a score's value; the least float times the logit is -inf for a masked expert, else below 4.8e-7
-                auto take_score = [&](int i, float s) {
-                    take(i, fmaf(x[i], 1.4e-45f, s + s_bias[32 * i + lane]));
-                };
+                // a score; the least float times the logit is -inf for a masked expert, else below 4.8e-7
+                auto take_score = [&](int i, float s) { take(i, fmaf(x[i], 1.4e-45f, s), s_offset[32 * i + lane]); };
                 if (by_logit) {
 #pragma unroll
                     for (int i = 0; i < V; ++i)
-                        take(i, x[i] - top);
+                        take(i, x[i] - top, rules.offset);
                 } else if (p.softmax) {
                     const float inverse = 1.f / sum;
 #pragma unroll
@@ -766,7 +772,7 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
                     }
                 }
                 sure = sure && !__any_sync(kFullWarp, !(all < INFINITY));
-                none = __all_sync(kFullWarp, some == 0.f);   // a padded token
+                none = GROUPS && __all_sync(kFullWarp, some == 0.f);   // a padded token
             }
         }
         if (GROUPS && sure && !none) {
@@ -800,6 +806,12 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
                 two = max(two, a);
                 three = max(three, b);
             }
+            if (lanes_later) {
+                none = __all_sync(kFullWarp, one <= rules.never);
+                one += 31u - lane;
+                two += 31u - lane;
+                three += 31u - lane;
+            }
             // the best key that place `place` can have, and the best one after the last place
             uint32_t got, after = 0u;
             bool rounds = seg != 8;
@@ -830,7 +842,8 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
                         if (owner) {
 #pragma unroll
                             for (int i = 0; i < V; ++i) {
-                                const uint32_t k = key[i] < best ? key[i] : 0u;
+                                const uint32_t whole_key = key[i] + (lanes_later ? 31u - lane : 0u);
+                                const uint32_t k = whole_key < best ? whole_key : 0u;
                                 two = max(two, min(one, k));
                                 one = max(one, k);
                             }
@@ -845,8 +858,8 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
                 // nothing but experts, and nothing that ranks by less than it may be off
                 const uint32_t down = __shfl_down_sync(kFullWarp, got, 1);
                 const uint32_t next = place + 1 < p.top_k ? down : after;
-                sure = !__any_sync(kFullWarp, place < p.top_k && chosen < 0);
-                if (sure && __any_sync(kFullWarp, place < p.top_k && !surely_above(got, next, rules.apart)))
+                sure = none || !__any_sync(kFullWarp, place < p.top_k && chosen < 0);
+                if (sure && !none && __any_sync(kFullWarp, place < p.top_k && !surely_above(got, next, rules.apart)))
                     sure = settle<D, V>(p, row, key, __shfl_sync(kFullWarp, got, p.top_k - 1), rules.apart, s_near, seg,
                                         top, sum, &chosen);
             }
@@ -903,7 +916,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
     const int E = p.experts;
     const uint32_t cta = blockIdx.x, ctas = gridDim.x;
     const bool alone = ctas == 1;
-    float *s_bias = reinterpret_cast<float *>(smem);                       // [32 V]
+    float *s_offset = reinterpret_cast<float *>(smem);                     // [32 V]
     uint32_t *s_keys = smem + 32 * V;                                      // [warps][E], groups of other sizes than 32
     uint32_t *s_count = s_keys + (odd_groups(p) ? warps * E : 0);          // [E], or for a single CTA [warps][E]
     __shared__ int s_stop, s_reach;
@@ -931,7 +944,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
             if (e >= static_cast<int>(blockDim.x))
                 b = p.bias && e < E ? p.bias[e] : 0.f;
             const bool never = e >= E || b == -INFINITY;
-            s_bias[e] = never ? kNever : b;
+            s_offset[e] = never ? kNever : b;
             // magnitudes compare as integers, NaN above all
             const uint32_t most = __reduce_max_sync(kFullWarp, never ? 0u : __float_as_uint(fabsf(b)));
             if (lane == 0 && most)
@@ -939,10 +952,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
         }
         __syncthreads();
     }
+    float reach = 1.f + __int_as_float(s_reach);
+    reach = reach <= kMostBias ? reach : NAN;
+    if (SCORES) {
+        const KeyRules rules = score_rules(reach);
+        for (int e = threadIdx.x; e < 32 * V; e += blockDim.x)
+            s_offset[e] = s_offset[e] == kNever ? kNever : fmaf(s_offset[e], rules.scale, rules.offset);
+        __syncthreads();
+    }
 
-    const float reach = 1.f + __int_as_float(s_reach);
-    const int done = choose_tokens<D, V, SCORES, GROUPS>(p, mine.first, mine.last, s_bias,
-                                                         reach <= kMostBias ? reach : NAN, s_keys + warp * E,
+    const int done = choose_tokens<D, V, SCORES, GROUPS>(p, mine.first, mine.last, s_offset, reach, s_keys + warp * E,
                                                          s_near[warp], s_count + (alone ? warp * E : 0));
     if (!p.plan)
         return;
