@@ -250,9 +250,9 @@ def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogi
     ids = route.ids if ids is None else ids
     if dlogits is None:
         dlogits = logits.new_empty((t, route.experts))
-    elif dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+    rows, g.dlogits_stride = _check_logits(route, dlogits, "dlogits")
+    if rows != t or dlogits.dtype != logits.dtype:
         raise ValueError("dlogits: the logits' type and shape expected")
-    _, g.dlogits_stride = _check_logits(route, dlogits, "dlogits")
     i32, f32 = route.types
     _check_rows(route, ids, "ids", t, route.top_k, i32)
     _check_rows(route, dweights, "dweights", t, route.top_k, f32)

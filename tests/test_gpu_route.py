@@ -421,6 +421,36 @@ def test_calls_on_several_streams_at_once(cns):
     assert abs(clip.norm.item() / float(torch.linalg.vector_norm(g.double())) - 1) < 4.1e-6
 
 
+@pytest.mark.parametrize("tokens,experts,top_k", [(20, 64, 4), (700, 96, 6), (5000, 128, 8)])
+def test_calls_follow_what_is_before_them_in_the_stream(cns, tokens, experts, top_k):
+    """Grids are launched before the kernel ahead of them has ended: its results, and no older ones, are read."""
+    import torch
+    slow = torch.randn(2048, 2048, device="cuda")
+    xs = [torch.randn(tokens, experts, device="cuda") for _ in range(12)]
+    dws = [torch.randn(tokens, top_k, device="cuda") for _ in range(12)]
+    x, dw, dx = torch.zeros_like(xs[0]), torch.zeros_like(dws[0]), torch.zeros_like(xs[0])
+    r = cns.new_route(tokens, experts, top_k)
+    clip = cns.new_grad_clip([dx], 0.5, outs=[torch.empty_like(dx)])
+    def step(k):
+        x.copy_(xs[k])
+        dw.copy_(dws[k])
+        cns.run_route(r, x)
+        cns.run_route_backward(r, x, dw, dlogits=dx)
+        norm = cns.run_grad_norm(clip).clone()
+        cns.run_grad_clip(clip)
+        return [t.clone() for t in (r.ids, r.weights, r.offsets, r.order, r.places, dx, clip.tensors[1][0])] + [norm]
+    alone = []
+    for k in range(12):
+        alone.append(step(k))
+        torch.cuda.synchronize()
+    for _ in range(3):
+        for _ in range(6):
+            slow @ slow                                            # lets the host run ahead
+        together = [step(k) for k in range(12)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for one, two in zip(alone, together) for a, b in zip(one, two))
+
+
 def test_a_workspace_shared_with_clipping(cns):
     """Routings and clippings in turn on one workspace: each leaves it as the other needs it."""
     import torch
