@@ -156,11 +156,21 @@ def _dtype_code(t):
 
 def new_step_workspace(nbytes: int, device=None, stream=None):
     """An initialised workspace of `nbytes` for cns_route, cns_grad_norm and cns_grad_clip.  Calls that follow
-    one another on a stream may share one; calls that may overlap need one each."""
+    one another on a stream may share one; calls that may overlap need one each.
+    Its memory is torch's current stream's and is zeroed on that stream; `stream` and the default stream wait for
+    it.  Any other stream that uses the workspace has to wait for the current one first, as for every tensor."""
     torch = _torch()
     nbytes = max(nbytes, _native.CNS_STEP_WORKSPACE_HEADER_BYTES)
-    ws = torch.empty((nbytes + 15) // 16 * 4, dtype=torch.int32, device=device or "cuda")   # torch aligns to 512 bytes
-    _native.check(_native.cns_step_workspace_init(ws, ws.numel() * 4, stream), "cns_step_workspace_init")
+    with torch.cuda.device(torch.device(device or "cuda")):
+        ws = torch.empty((nbytes + 15) // 16 * 4, dtype=torch.int32, device="cuda")   # torch aligns to 512 bytes
+        here = torch.cuda.current_stream()
+        _native.check(_native.cns_step_workspace_init(ws, ws.numel() * 4, here), "cns_step_workspace_init")
+        handle = _native.stream_handle(stream)
+        if handle and handle != here.cuda_stream:
+            torch.cuda.ExternalStream(handle).wait_stream(here)
+        # (what a capture records reaches the default stream by the replay alone)
+        if here.cuda_stream and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.default_stream().wait_stream(here)
     return ws
 
 
@@ -171,7 +181,9 @@ def new_route(tokens: int, experts: int, top_k: int, *, score: int = _native.CNS
     run_route fills:
       ids [tokens, top_k] int32, weights [tokens, top_k] float32;
       with plan: offsets [experts + 1], order [tokens * top_k], places [tokens, top_k], all int32;
-      with scores: scores [tokens, experts] float32."""
+      with scores: scores [tokens, experts] float32.
+    They are torch's current stream's, and so is the zeroing of the workspace that this enqueues: see
+    new_step_workspace for the streams that are ordered behind it."""
     torch = _torch()
     _dtype_codes()
     r = _native.Route()
@@ -302,7 +314,8 @@ def new_grad_clip(grads, max_norm: float = float("inf"), *, outs=None, eps: floa
     """The gradients of a step (a list of dense tensors, float32, bfloat16 or float16 mixed as they come) and
     where their clipped values go: `outs`, tensors of the same shapes and strides, or in place.  Holds the
     tensors' addresses, so it stands for these tensors for as long as they live; make another one for others.
-    `norm` is the float32 scalar that run_grad_norm and run_grad_clip fill."""
+    `norm` is the float32 scalar that run_grad_norm and run_grad_clip fill.  Enqueues the zeroing of its workspace
+    on torch's current stream: see new_step_workspace for the streams that are ordered behind it."""
     torch = _torch()
     _dtype_codes()
     g = _native.GradClip()

@@ -1,0 +1,70 @@
+"""Handles of the training-step operators on the GPU: the streams that they are made and used on."""
+import numpy as np
+import pytest
+
+from oracle import steps
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def cns():
+    import torch
+    import counted_notify_sync_gb300 as c
+    c.build()
+    torch.cuda.set_device(0)
+    return c
+
+
+def busy(torch, n=12):
+    """Some milliseconds of work on the current stream."""
+    a = torch.randn(4096, 4096, device="cuda")
+    for _ in range(n):
+        a @ a
+
+
+def test_handles_made_and_used_on_a_side_stream(cns):
+    """From memory that held ones, with the default stream busy: the zeroing comes before the first call."""
+    import torch
+    side = torch.cuda.Stream()
+    x, g = torch.randn(3000, 64, device="cuda"), torch.randn(2_000_000, device="cuda")
+    need = max(cns.cns_route_workspace_bytes(3000, 64, 4)[1], cns.cns_grad_workspace_bytes(1)[1])
+    for given in (None, side):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            ones = [torch.full((need // 4 + 4,), -1, dtype=torch.int32, device="cuda") for _ in range(4)]
+            del ones
+        side.synchronize()
+        busy(torch)
+        with torch.cuda.stream(side):
+            r = cns.new_route(3000, 64, 4, stream=given)
+            cns.run_route(r, x, stream=side)
+            clip = cns.new_grad_clip([g], 1.0, outs=[torch.empty_like(g)], stream=given)
+            cns.run_grad_clip(clip, stream=side)
+        side.synchronize()
+        assert cns.syncall_read_workspace(r.workspace, side)[3] == 0
+        want = np.argsort(-x.cpu().numpy(), -1, kind="stable")[:, :4]
+        assert np.array_equal(r.ids.cpu().numpy(), want)
+        assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip((r.offsets, r.order, r.places), steps.plan(want, 64)))
+        assert abs(clip.norm.item() / float(torch.linalg.vector_norm(g.double())) - 1) < 4.1e-6
+        # and on the default stream, which comes after
+        cns.run_route(r, x, sync=True)
+        assert np.array_equal(r.ids.cpu().numpy(), want)
+        torch.cuda.synchronize()
+
+
+def test_a_handle_made_within_a_capture(cns):
+    """Its zeroing is part of the graph, on the capturing stream."""
+    import torch
+    s = torch.cuda.Stream()
+    x = torch.randn(500, 32, device="cuda")
+    cns.run_route(cns.new_route(500, 32, 4), x, sync=True)         # the kernels are loaded
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        r = cns.new_route(500, 32, 4)
+        cns.run_route(r, x, stream=s)
+    graph.replay()
+    torch.cuda.synchronize()
+    want = np.argsort(-x.cpu().numpy(), -1, kind="stable")[:, :4]
+    assert np.array_equal(r.ids.cpu().numpy(), want)
