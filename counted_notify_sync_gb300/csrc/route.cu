@@ -517,8 +517,15 @@ extern "C" int cns_route(cns_route_t *r)
                             : r->dtype == CNS_DT_BF16 ? (by_score ? launch_route_bf16_score : launch_route_bf16_logit)
                                                       : (by_score ? launch_route_f16_score : launch_route_f16_logit);
         CNS_CUDA(launch(p, ctas, warps, s));
-        if (plan && ctas > 1)
-            CNS_CUDA(launch_plan(p, ctas, warps, s));
+        if (plan && ctas > 1) {
+            const cudaError_t e = launch_plan(p, ctas, warps, s);
+            if (e != cudaSuccess) {
+                // nobody will take up what the first grid adds to the blocks' sums: later plans must not
+                (void)cudaGetLastError();
+                (void)cudaMemsetAsync(p.header + kStepSumWord, 0, kStepSumWords * sizeof(uint32_t), s);
+                return cuda_fail(e, "routing plan launch");
+            }
+        }
     }
     if (!r->sync)
         return CNS_SUCCESS;
