@@ -135,6 +135,10 @@ def run_pipeline(done, ack, tiles: int, tile_words: int, rounds: int, producer_s
 # Like every call here these run on the stream that they are given (None: the default stream) and return before
 # the GPU is done.  A tensor that belongs to another stream needs what it needs for any kernel: the streams
 # ordered by an event, and record_stream before it is freed.
+#
+# A handle (new_route, new_grad_clip) has one workspace and one set of results, so its calls belong to one thread at
+# a time, and those of run_route, run_grad_norm and run_grad_clip to streams that are ordered with one another.
+# run_route_backward only reads the handle: gradients may be taken from several threads at once.
 
 _CODES = {}   # torch dtype -> cns_dtype_t, filled by the first new_route or new_grad_clip
 
@@ -257,7 +261,7 @@ def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogi
     """dL/dlogits of run_route(route, logits): from dL/dweights [tokens, top_k] float32 and, if given,
     dL/dscores [tokens, experts] float32.  `ids` are the chosen experts (default: route.ids); the result goes to
     `dlogits` (default: a new tensor) in the logits' type."""
-    g = route.backward
+    g = _native.RouteGrad.from_buffer_copy(route.backward)   # this call's own: other threads may be filling in theirs
     t, g.logits_stride = _check_logits(route, logits, "logits")
     ids = route.ids if ids is None else ids
     if dlogits is None:

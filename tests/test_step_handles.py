@@ -60,3 +60,38 @@ def test_a_captured_workspace_leaves_the_default_stream_alone(enqueued):
     enqueued.current, enqueued.capturing = 0x70, True
     cns.new_step_workspace(1 << 20, stream=0x70)
     assert enqueued == [("zero", 0x70)]
+
+
+def route_handle(index=-1, tokens=8, experts=16, top_k=2):
+    """What new_route returns, on CPU tensors (whose device index is -1)."""
+    import torch
+    r = _native.Route()
+    r.ids = torch.zeros((tokens, top_k), dtype=torch.int32)
+    r.capacity, r.index, r.types = tokens, index, (torch.int32, torch.float32)
+    r.experts, r.top_k = experts, top_k
+    r.backward = _native.RouteGrad(experts=experts, top_k=top_k, score=1, renorm=1, scale=1.0)
+    cns._CODES[torch.float32] = _native.CNS_DT_F32
+    return r
+
+
+def test_threads_share_a_route_for_their_gradients(monkeypatch):
+    """Each call's arguments are its own: while one is in the library, another one fills in its."""
+    import torch
+    r = route_handle()
+    calls = [dict(logits=torch.zeros(8, 16), dweights=torch.zeros(8, 2), ids=torch.zeros((8, 2), dtype=torch.int32),
+                  dlogits=torch.zeros(8, 16)) for _ in range(2)]
+    seen = []
+
+    def entry(g):
+        if not seen:
+            seen.append(None)
+            cns.run_route_backward(r, calls[1]["logits"][:4], calls[1]["dweights"], ids=calls[1]["ids"],
+                                   dlogits=calls[1]["dlogits"][:4], stream=0x50)   # from another thread, say
+        seen.append((g.logits_dev, g.dweights_dev, g.ids_dev, g.dlogits_dev, g.tokens, g.stream))
+        return 0
+
+    monkeypatch.setattr(_native, "cns_route_backward", entry)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    cns.run_route_backward(r, calls[0]["logits"], calls[0]["dweights"], ids=calls[0]["ids"], dlogits=calls[0]["dlogits"])
+    want = [tuple(c[k].data_ptr() for k in ("logits", "dweights", "ids", "dlogits")) for c in calls]
+    assert seen[1:] == [want[1] + (4, 0x50), want[0] + (8, None)]
