@@ -138,7 +138,8 @@ def run_pipeline(done, ack, tiles: int, tile_words: int, rounds: int, producer_s
 #
 # A handle (new_route, new_grad_clip) has one workspace and one set of results, so its calls belong to one thread at
 # a time, and those of run_route, run_grad_norm and run_grad_clip to streams that are ordered with one another.
-# run_route_backward only reads the handle: gradients may be taken from several threads at once.
+# run_route_backward only reads the handle: gradients may be taken from several threads at once.  A handle's device
+# has to be the current one at each call.
 
 _CODES = {}   # torch dtype -> cns_dtype_t, filled by the first new_route or new_grad_clip
 
@@ -151,11 +152,20 @@ def _dtype_codes():
     return _CODES
 
 
-def _dtype_code(t):
-    code = _CODES.get(t.dtype)
+def _dtype_code(dtype):
+    code = _CODES.get(dtype)
     if code is None:
-        raise TypeError(f"float32, bfloat16 or float16 expected, got {t.dtype}")
+        raise TypeError(f"float32, bfloat16 or float16 expected, got {dtype}")
     return code
+
+
+def _check_current(index):
+    """The library launches on the current device, whatever device the tensors are on.  (Handles say whether there
+    is another one at all: asking torch takes half a microsecond.)"""
+    import torch
+    at = torch.cuda.current_device()
+    if at != index:
+        raise ValueError(f"made for CUDA device {index}, and device {at} is the current one")
 
 
 def new_step_workspace(nbytes: int, device=None, stream=None):
@@ -204,7 +214,7 @@ def new_route(tokens: int, experts: int, top_k: int, *, score: int = _native.CNS
     r.workspace = workspace
     if plan and workspace is None:
         r.workspace = new_step_workspace(nbytes, device, stream)
-    r.capacity, r.index = tokens, r.ids.get_device()
+    r.capacity, r.index, r.others = tokens, r.ids.get_device(), torch.cuda.device_count() > 1
     r.types = (torch.int32, torch.float32)
     b = r.backward = _native.RouteGrad()   # run_route_backward's, but for the call's own tensors
     b.experts, b.top_k, b.score, b.renorm, b.scale = experts, top_k, score, int(renorm), scale
@@ -221,16 +231,17 @@ def new_route(tokens: int, experts: int, top_k: int, *, score: int = _native.CNS
 def _check_logits(route, logits, what):
     """(rows, elements from row to row) of a [tokens, experts] tensor."""
     shape, stride, e = logits.shape, logits.stride(), route.experts
-    if not (len(shape) == 2 and shape[1] == e and shape[0] <= route.capacity and logits.get_device() == route.index and
-            (stride[1] == 1 or e == 1) and (shape[0] <= 1 or stride[0] >= e)):
-        raise ValueError(f"{what}: [tokens <= {route.capacity}, {e}] on {route.ids.device}, rows apart and of unit stride, "
-                         f"expected; got {tuple(shape)}, strides {stride}, on {logits.device}")
-    return shape[0], stride[0] if shape[0] > 1 else 0
+    if len(shape) == 2 and logits.get_device() == route.index:
+        (t, cols), (step, one) = shape, stride
+        if cols == e and t <= route.capacity and (one == 1 or e == 1) and (step >= e or t <= 1):
+            return t, step if t > 1 else 0
+    raise ValueError(f"{what}: [tokens <= {route.capacity}, {e}] on {route.ids.device}, rows apart and of unit stride, "
+                     f"expected; got {tuple(shape)}, strides {stride}, on {logits.device}")
 
 
 def _check_rows(route, x, name, rows, cols, dtype):
     shape = x.shape
-    if not (x.is_contiguous() and len(shape) == 2 and shape[0] >= rows and shape[1] == cols and x.dtype == dtype and
+    if not (len(shape) == 2 and shape[0] >= rows and shape[1] == cols and x.is_contiguous() and x.dtype == dtype and
             x.get_device() == route.index):
         raise ValueError(f"{name}: contiguous {dtype} [tokens, {cols}] on {route.ids.device} expected")
 
@@ -239,6 +250,8 @@ def run_route(route, logits, bias=None, stream=None, sync: bool = False):
     """Route the rows of `logits` ([tokens, experts], float32, bfloat16 or float16, rows at any stride) on
     `stream` (None: the default stream).  Returns `route`, whose tensors hold the results: the first
     logits.shape[0] rows, and of `order` the first logits.shape[0] * top_k."""
+    if route.others:
+        _check_current(route.index)
     t, route.logits_stride = _check_logits(route, logits, "logits")
     if bias is None:
         route.bias_dev = None
@@ -247,7 +260,7 @@ def run_route(route, logits, bias=None, stream=None, sync: bool = False):
                 bias.get_device() == route.index):
             raise ValueError("bias: contiguous float32 [experts] on the logits' device expected")
         route.bias_dev = bias.data_ptr()
-    route.dtype = _dtype_code(logits)
+    route.dtype = _dtype_code(logits.dtype)
     route.logits_dev, route.tokens = logits.data_ptr(), t
     route.stream = _native.stream_handle(stream)
     route.sync = 1 if sync else 0
@@ -261,25 +274,33 @@ def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogi
     """dL/dlogits of run_route(route, logits): from dL/dweights [tokens, top_k] float32 and, if given,
     dL/dscores [tokens, experts] float32.  `ids` are the chosen experts (default: route.ids); the result goes to
     `dlogits` (default: a new tensor) in the logits' type."""
+    if route.others:
+        _check_current(route.index)
     g = _native.RouteGrad.from_buffer_copy(route.backward)   # this call's own: other threads may be filling in theirs
-    t, g.logits_stride = _check_logits(route, logits, "logits")
-    ids = route.ids if ids is None else ids
+    t, step = _check_logits(route, logits, "logits")
+    dtype = logits.dtype
+    if step:
+        g.logits_stride = step
     if dlogits is None:
         dlogits = logits.new_empty((t, route.experts))
-    rows, g.dlogits_stride = _check_logits(route, dlogits, "dlogits")
-    if rows != t or dlogits.dtype != logits.dtype:
-        raise ValueError("dlogits: the logits' type and shape expected")
-    i32, f32 = route.types
-    _check_rows(route, ids, "ids", t, route.top_k, i32)
-    _check_rows(route, dweights, "dweights", t, route.top_k, f32)
-    if dscores is None:
-        g.dscores_dev = None
     else:
+        rows, step = _check_logits(route, dlogits, "dlogits")
+        if rows != t or dlogits.dtype != dtype:
+            raise ValueError("dlogits: the logits' type and shape expected")
+        if step:
+            g.dlogits_stride = step
+    if ids is None:
+        ids = route.ids
+    (i32, f32), top_k = route.types, g.top_k
+    _check_rows(route, ids, "ids", t, top_k, i32)
+    _check_rows(route, dweights, "dweights", t, top_k, f32)
+    if dscores is not None:
         _check_rows(route, dscores, "dscores", t, route.experts, f32)
         g.dscores_dev = dscores.data_ptr()
+    if stream is not None:
+        g.stream = _native.stream_handle(stream)
     g.logits_dev, g.ids_dev, g.dweights_dev = logits.data_ptr(), ids.data_ptr(), dweights.data_ptr()
-    g.dlogits_dev, g.stream = dlogits.data_ptr(), _native.stream_handle(stream)
-    g.tokens, g.dtype = t, _dtype_code(logits)
+    g.dlogits_dev, g.tokens, g.dtype = dlogits.data_ptr(), t, _dtype_code(dtype)
     rc = _native.cns_route_backward(g)
     if rc:
         raise _native.CnsError(rc, "cns_route_backward")
@@ -307,7 +328,7 @@ def _tensor_table(tensors, index, what):
             raise ValueError(f"{what}[{i}]: on {t.device}, CUDA device {index} expected")
         if not _dense(t):
             raise ValueError(f"{what}[{i}]: not dense (strides {t.stride()})")
-        n, at, code = t.numel(), t.data_ptr(), _dtype_code(t)
+        n, at, code = t.numel(), t.data_ptr(), _dtype_code(t.dtype)
         e.data_dev, e.elems, e.dtype = at, n, code
         spans.append((at, at + n * (4 if code == _native.CNS_DT_F32 else 2)))
     return table, spans
@@ -328,7 +349,8 @@ def new_grad_clip(grads, max_norm: float = float("inf"), *, outs=None, eps: floa
     if device.type != "cuda":
         raise ValueError(f"gradients on {device}, a CUDA device expected")
     g.norm = torch.empty((), dtype=torch.float32, device=device)
-    index = g.norm.get_device()
+    index, g.others = g.norm.get_device(), torch.cuda.device_count() > 1
+    g.index = index
     g.grad_table, spans = _tensor_table(grads, index, "grads")
     g.out_table = None
     if outs is None:
@@ -370,6 +392,8 @@ def new_grad_clip(grads, max_norm: float = float("inf"), *, outs=None, eps: floa
 
 def run_grad_norm(plan, stream=None, sync: bool = False):
     """The global norm of new_grad_clip's gradients on `stream` (None: the default stream); returns plan.norm."""
+    if plan.others:
+        _check_current(plan.index)
     plan.stream = _native.stream_handle(stream)
     plan.sync = 1 if sync else 0
     rc = _native.cns_grad_norm(plan)
@@ -381,6 +405,8 @@ def run_grad_norm(plan, stream=None, sync: bool = False):
 def run_grad_clip(plan, stream=None, sync: bool = False):
     """Clip new_grad_clip's gradients by their global norm on `stream`; returns plan.norm, the norm before
     clipping."""
+    if plan.others:
+        _check_current(plan.index)
     plan.stream = _native.stream_handle(stream)
     plan.sync = 1 if sync else 0
     rc = _native.cns_grad_clip(plan)

@@ -62,22 +62,23 @@ def test_a_captured_workspace_leaves_the_default_stream_alone(enqueued):
     assert enqueued == [("zero", 0x70)]
 
 
-def route_handle(index=-1, tokens=8, experts=16, top_k=2):
-    """What new_route returns, on CPU tensors (whose device index is -1)."""
+def route_handle(monkeypatch, tokens=8, experts=16, top_k=2):
+    """What new_route returns, on CPU tensors (whose device index is -1), with device -1 the current one of several."""
     import torch
+    monkeypatch.setitem(cns._CODES, torch.float32, _native.CNS_DT_F32)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     r = _native.Route()
     r.ids = torch.zeros((tokens, top_k), dtype=torch.int32)
-    r.capacity, r.index, r.types = tokens, index, (torch.int32, torch.float32)
+    r.capacity, r.index, r.others, r.types = tokens, -1, True, (torch.int32, torch.float32)
     r.experts, r.top_k = experts, top_k
     r.backward = _native.RouteGrad(experts=experts, top_k=top_k, score=1, renorm=1, scale=1.0)
-    cns._CODES[torch.float32] = _native.CNS_DT_F32
     return r
 
 
 def test_threads_share_a_route_for_their_gradients(monkeypatch):
     """Each call's arguments are its own: while one is in the library, another one fills in its."""
     import torch
-    r = route_handle()
+    r = route_handle(monkeypatch)
     calls = [dict(logits=torch.zeros(8, 16), dweights=torch.zeros(8, 2), ids=torch.zeros((8, 2), dtype=torch.int32),
                   dlogits=torch.zeros(8, 16)) for _ in range(2)]
     seen = []
@@ -91,7 +92,28 @@ def test_threads_share_a_route_for_their_gradients(monkeypatch):
         return 0
 
     monkeypatch.setattr(_native, "cns_route_backward", entry)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     cns.run_route_backward(r, calls[0]["logits"], calls[0]["dweights"], ids=calls[0]["ids"], dlogits=calls[0]["dlogits"])
     want = [tuple(c[k].data_ptr() for k in ("logits", "dweights", "ids", "dlogits")) for c in calls]
     assert seen[1:] == [want[1] + (4, 0x50), want[0] + (8, None)]
+
+
+def test_a_handle_of_another_device_is_refused_before_the_launch(monkeypatch):
+    """The library launches on the current device: a handle whose tensors are elsewhere must not get there."""
+    import torch
+    r = route_handle(monkeypatch)
+    g = _native.GradClip()
+    g.index, g.others, g.norm = -1, True, torch.zeros(())
+    reached = []
+    for entry in ("cns_route", "cns_route_backward", "cns_grad_norm", "cns_grad_clip"):
+        monkeypatch.setattr(_native, entry, lambda *_, entry=entry: reached.append(entry) or 0)
+    x = torch.zeros(8, 16)
+    calls = (lambda: cns.run_route(r, x), lambda: cns.run_route_backward(r, x, torch.zeros(8, 2)),
+             lambda: cns.run_grad_norm(g), lambda: cns.run_grad_clip(g))
+    for call in calls:
+        call()
+    assert len(reached) == 4
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for call in calls:
+        with pytest.raises(ValueError, match="current"):
+            call()
+    assert len(reached) == 4
