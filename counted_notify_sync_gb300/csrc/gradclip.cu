@@ -503,8 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const __grid_constant
             if (mine && !stop)
                 *p.norm = norm;
             if constexpr (CLIP) {
+                // inf / inf (no limit) and 0 / 0 clip nothing; NaN comes from a norm of NaN alone
                 const float f = p.max_norm / (norm + p.eps);
-                s_factor = f < 1.f || f != f ? f : 1.f;
+                s_factor = f < 1.f || norm != norm ? f : 1.f;
                 s_stop = stop;
             }
         }

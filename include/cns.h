@@ -844,8 +844,9 @@ typedef enum { CNS_NORM_L2 = 0, CNS_NORM_INF = 1 } cns_norm_t;
 /* The gradients of a step, and where the clipped ones go.  norm is taken over
  * all elements of all tensors together; every element is then multiplied by
  * min(1, max_norm / (norm + eps)) in 32 bits and rounded once to the output's
- * type.  A norm of NaN makes the factor NaN, one of inf makes it 0.  Squares
- * are summed in 32 bits, a CTA's part at a time (so the norm overflows where
+ * type.  A norm of NaN makes the factor NaN, one of inf makes it 0; a max_norm
+ * of inf (no limit) leaves it 1 whatever the norm but NaN, and so does 0 / 0.
+ * Squares are summed in 32 bits, a CTA's part at a time (so the norm overflows where
  * such a part does, when gradients near 1e19 come in numbers), and the parts
  * joined without overflow, in an order that depends on the sizes alone.
  * Tensors must not overlap, except an output with its own gradient when the
