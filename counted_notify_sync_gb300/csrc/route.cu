@@ -268,13 +268,15 @@ __global__ void __launch_bounds__(kGradWarps * 32, MODE == kGradSparse ? 8 : 4) 
             if constexpr (HOLD > 0) {
 #pragma unroll
                 for (int j = 0; j < HOLD; ++j) {
+                    if (j * SEG * W >= p.experts)
+                        break;   // no lane has any (an expf takes 8 instructions)
                     const int e = (j * SEG + place) * W;
                     float w[W];
                     if (MODE == kGradScores && token && e < p.experts)
                         load_elems<CNS_DT_F32, W>(ds + e, w);
 #pragma unroll
                     for (int i = 0; i < W; ++i) {
-                        held[j][i] = exp_near(held[j][i] - top);
+                        held[j][i] = expf(held[j][i] - top);
                         sum += held[j][i];
                         if (MODE == kGradScores && token && e < p.experts)
                             mean = fmaf(held[j][i], w[i], mean);
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, MODE == kGradSparse ? 8 : 4) 
                         load_elems<CNS_DT_F32, W>(ds + e, w);
 #pragma unroll
                     for (int i = 0; i < W; ++i) {
-                        const float ex = exp_near(v[i] - top);   // off the most where it is the least
+                        const float ex = expf(v[i] - top);
                         sum += ex;
                         if (MODE == kGradScores)
                             mean = fmaf(ex, w[i], mean);
@@ -339,9 +341,9 @@ __global__ void __launch_bounds__(kGradWarps * 32, MODE == kGradSparse ? 8 : 4) 
                     if (!whole) {
                         v[i] = 0.f;
                     } else if (softmax) {
-                        v[i] = (exps ? v[i] : exp_near(v[i] - top)) * scale * ((MODE == kGradScores ? w[i] : 0.f) - mean);
+                        v[i] = (exps ? v[i] : expf(v[i] - top)) * scale * ((MODE == kGradScores ? w[i] : 0.f) - mean);
                     } else {
-                        const float ex = exp_near(-fabsf(v[i])), r = 1.f / (1.f + ex);
+                        const float ex = expf(-fabsf(v[i])), r = 1.f / (1.f + ex);
                         v[i] = r * (ex * r) * w[i];
                     }
                 }

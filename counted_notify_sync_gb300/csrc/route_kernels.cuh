@@ -719,10 +719,9 @@ __device__ __forceinline__ int choose_tokens(const RouteParams &p, int64_t first
             }
             if (whole) {
                 sum = 0.f;
-                // off the most where e^(x - top) is the least
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    sum += exp_near(x[i] - top);
+                    sum += expf(x[i] - top);
                 sum = warp_sum(sum);
                 if (sum == 0.f)
                     sum = 1.f;

@@ -193,7 +193,8 @@ __device__ __forceinline__ bool gather_last(uint32_t *header, uint32_t ctas, uin
     return true;
 }
 
-// e^x where 2^-22 is enough (sums, and what an exact value replaces): off by a relative 2^-22 + 2^-23 |x|; tiny results are 0.
+// e^x for what only ranks experts, and what an exact value settles where it leaves that open (the routing's near
+// keys): off by a relative 2^-22 + 2^-23 |x|; tiny results are 0.
 __device__ __forceinline__ float exp_near(float x)
 {
     float r;
