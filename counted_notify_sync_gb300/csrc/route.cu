@@ -95,13 +95,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_plan_kernel(const _
 
 cudaError_t launch_plan(const RouteParams &p, int ctas, int warps, cudaStream_t s)
 {
-    const size_t smem = plan_smem(p, warps);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(route_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        if (e != cudaSuccess)
-            return e;
-    }
+    const size_t smem = plan_smem(p.experts, warps);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(route_plan_kernel), smem,
+                                     plan_smem(CNS_ROUTE_MAX_EXPERTS, kRouteWarps));
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = early_launch(&attr);
     cfg.gridDim = dim3(ctas);

@@ -210,7 +210,16 @@ __device__ __forceinline__ void place_entries(const RouteParams &p, const Stretc
 }
 
 // Shared memory of place_entries.
-inline size_t plan_smem(const RouteParams &p, int warps) { return sizeof(uint32_t) * (warps + 2) * p.experts; }
+inline size_t plan_smem(int experts, int warps) { return sizeof(uint32_t) * (warps + 2) * experts; }
+
+// Let a kernel have `smem` bytes of shared memory; `most` is what any launch of it may ask for, and what it is always
+// allowed: another thread's launch may come between this and the caller's, and must not find less.
+inline cudaError_t allow_smem(const void *kernel, size_t smem, size_t most)
+{
+    if (smem <= 48 * 1024)
+        return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+}
 
 #ifdef CNS_ROUTE_KERNELS
 
@@ -984,7 +993,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 1) route_kernel(const __grid
 inline size_t route_smem(const RouteParams &p, int V, int ctas, int warps)
 {
     return sizeof(uint32_t) * (32 * V + (odd_groups(p) ? warps * p.experts : 0) + (p.plan && ctas > 1 ? p.experts : 0)) +
-           (p.plan && ctas == 1 ? plan_smem(p, warps) : 0);
+           (p.plan && ctas == 1 ? plan_smem(p.experts, warps) : 0);
+}
+
+// The largest route_smem of a kernel: 32 V experts in odd groups, and a single CTA's plan.
+constexpr size_t most_route_smem(int V)
+{
+    return sizeof(uint32_t) * 32 * V * (1 + kRouteWarps + kRouteWarps + 2);
 }
 
 template <int D, int V, bool SCORES, bool GROUPS>
@@ -992,12 +1007,9 @@ cudaError_t launch_route_v(const RouteParams &p, int ctas, int warps, cudaStream
 {
     const auto kernel = route_kernel<D, V, SCORES, GROUPS>;
     const size_t smem = route_smem(p, V, ctas, warps);
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess)
-            return e;
-    }
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem, most_route_smem(V));
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = early_launch(&attr);
     cfg.gridDim = dim3(ctas);

@@ -1,4 +1,6 @@
 """Handles of the training-step operators on the GPU: the streams that they are made and used on."""
+import threading
+
 import numpy as np
 import pytest
 
@@ -68,3 +70,28 @@ def test_a_handle_made_within_a_capture(cns):
     torch.cuda.synchronize()
     want = np.argsort(-x.cpu().numpy(), -1, kind="stable")[:, :4]
     assert np.array_equal(r.ids.cpu().numpy(), want)
+
+
+def test_threads_with_routings_of_other_sizes(cns):
+    """The same kernel with other amounts of shared memory, from four threads: no call is refused."""
+    import torch
+    fails = []
+
+    def work(experts):
+        s = torch.cuda.Stream()
+        x = torch.randn(5000, experts, device="cuda")
+        s.wait_stream(torch.cuda.current_stream())
+        r = cns.new_route(5000, experts, 4, stream=s)
+        try:
+            for _ in range(3000):
+                cns.run_route(r, x, stream=s)
+        except cns.CnsError as e:
+            fails.append((experts, str(e)))
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(e,)) for e in (500, 400, 512, 420)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not fails

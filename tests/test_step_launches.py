@@ -66,3 +66,29 @@ def test_a_plan_that_is_refused_leaves_the_workspace_as_it_was(run):
     assert rc != 0 and [c[0] for c in calls] == [0]
     rc, calls = run("print(json.dumps(route(5000, 64, 4)))")
     assert rc == 0 and [c[0] for c in calls] == [0, 0]
+
+
+def test_a_kernel_is_allowed_the_same_shared_memory_by_every_call(run):
+    """The limit is the kernel's, and calls of other threads set it between this one's setting and its launch: a
+    smaller call must not lower it."""
+    limits = run("""
+limits = {}
+for score in (0, 1):
+    for groups, top_groups, group_top in ((1, 1, 1), (4, 2, 1), (4, 2, 2)):
+        for experts in (512, 480, 420, 384, 360, 320, 256, 128, 64, 8):
+            for tokens in (1, 4, 32, 33, 5000):
+                for plan in (True, False):
+                    kw = {} if plan else dict(offsets_dev=None, order_dev=None, places_dev=None)
+                    rc, calls = route(tokens, experts, 2, score=score, groups=groups, top_groups=top_groups,
+                                      group_top=group_top, **kw)
+                    assert rc == 0
+                    allowed = {}
+                    for kind, _, what, size, _ in calls:
+                        if kind == ATTRIBUTE:
+                            limits.setdefault(what, []).append(size)
+                            allowed[what] = size
+                        if kind == LAUNCH:
+                            assert size <= allowed.get(what, 48 << 10)
+print(json.dumps([sorted(set(v)) for v in limits.values()]))
+""")
+    assert limits and all(len(v) == 1 and v[0] <= 227 << 10 for v in limits), limits
