@@ -319,6 +319,11 @@ def _dense(t):
     return True
 
 
+def _same_layout(t, o):
+    """Whether equal indices of two tensors of one shape are at equal distances from the start."""
+    return t.numel() == 0 or all(a == b or n == 1 for a, b, n in zip(t.stride(), o.stride(), t.shape))
+
+
 def _tensor_table(tensors, index, what):
     """(cns_tensor_t array, [(first byte, last byte + 1)]) of dense tensors on device `index`."""
     table = (_native.Tensor * max(len(tensors), 1))()
@@ -361,7 +366,7 @@ def new_grad_clip(grads, max_norm: float = float("inf"), *, outs=None, eps: floa
             raise ValueError("outs: one for each gradient expected")
         g.out_table, to = _tensor_table(outs, index, "outs")
         for i, (t, o) in enumerate(zip(grads, outs)):
-            if t.shape != o.shape or (t.stride() != o.stride() and t.numel()):
+            if t.shape != o.shape or not _same_layout(t, o):
                 raise ValueError(f"outs[{i}]: the gradient's shape and strides expected")
         # an output that is its gradient is one tensor
         same = [a == b and t.dtype == o.dtype for a, b, t, o in zip(spans, to, grads, outs)]

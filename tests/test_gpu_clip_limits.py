@@ -1,5 +1,6 @@
-"""Clipping where the quotient max_norm / (norm + eps) has no value: an unlimited norm (max_norm = inf, the default),
-a norm that overflowed, and zero over zero.  Only a norm of NaN makes NaN of numbers."""
+"""Clipping at its limits.  Where the quotient max_norm / (norm + eps) has no value: an unlimited norm (max_norm = inf, the default),
+a norm that overflowed, and zero over zero: only a norm of NaN makes NaN of numbers.  And layouts that are alike
+though their strides are not."""
 import numpy as np
 import pytest
 
@@ -56,3 +57,15 @@ def test_a_finite_limit_makes_an_infinite_norm_zeros(cns):
         out = torch.ones_like(g)
         assert cns.run_grad_clip(cns.new_grad_clip([g], limit, outs=[out]), sync=True).item() == INF
         assert (out == 0).all()
+
+
+def test_strides_along_axes_of_one_do_not_matter(cns):
+    """A 1 x 1 convolution's weights, channels last and not, lie the same way."""
+    import torch
+    g = torch.as_strided(torch.randn(40 * 24, device="cuda"), (40, 24, 1, 1), (24, 1, 24, 24))
+    out = torch.empty((40, 24, 1, 1), device="cuda")
+    assert g.stride() != out.stride()
+    norm = cns.run_grad_clip(cns.new_grad_clip([g], 1.0, outs=[out]), sync=True).cpu()
+    assert torch.equal(out.cpu(), g.cpu() * (torch.tensor(1.0) / (norm + torch.tensor(1e-6))))
+    with pytest.raises(ValueError, match="strides"):
+        cns.new_grad_clip([torch.zeros(6, 4, device="cuda").t()], 1.0, outs=[torch.zeros(4, 6, device="cuda")])
