@@ -270,10 +270,21 @@ def run_route(route, logits, bias=None, stream=None, sync: bool = False):
     return route
 
 
+def _empty_on(stream, like, shape):
+    """A tensor whose memory is the stream's that the call runs on: torch hands out what calls of its own stream may
+    still be using, which comes before that stream's work alone."""
+    import torch
+    handle = _native.stream_handle(stream) or 0
+    if torch.cuda.current_stream().cuda_stream == handle:
+        return like.new_empty(shape)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()):
+        return like.new_empty(shape)
+
+
 def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogits=None, stream=None):
     """dL/dlogits of run_route(route, logits): from dL/dweights [tokens, top_k] float32 and, if given,
     dL/dscores [tokens, experts] float32.  `ids` are the chosen experts (default: route.ids); the result goes to
-    `dlogits` (default: a new tensor) in the logits' type."""
+    `dlogits` (default: a new tensor, of `stream`'s memory) in the logits' type."""
     if route.others:
         _check_current(route.index)
     g = _native.RouteGrad.from_buffer_copy(route.backward)   # this call's own: other threads may be filling in theirs
@@ -282,7 +293,7 @@ def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogi
     if step:
         g.logits_stride = step
     if dlogits is None:
-        dlogits = logits.new_empty((t, route.experts))
+        dlogits = _empty_on(stream, logits, (t, route.experts))
     else:
         rows, step = _check_logits(route, dlogits, "dlogits")
         if rows != t or dlogits.dtype != dtype:

@@ -95,3 +95,23 @@ def test_threads_with_routings_of_other_sizes(cns):
     for t in threads:
         t.join()
     assert not fails
+
+
+def test_a_new_gradient_tensor_is_of_the_calls_stream(cns):
+    """Not of memory that the current stream has still to write."""
+    import torch
+    x, dw = torch.randn(3000, 64, device="cuda"), torch.randn(3000, 4, device="cuda")
+    r = cns.new_route(3000, 64, 4)
+    cns.run_route(r, x, sync=True)
+    want = cns.run_route_backward(r, x, dw)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for current, given in ((torch.cuda.default_stream(), side), (side, None), (side, other), (side, side)):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(current):
+            late = torch.empty_like(x)
+            busy(torch)
+            late.fill_(7.0)
+            del late
+            got = cns.run_route_backward(r, x, dw, stream=given)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)

@@ -107,7 +107,7 @@ def test_a_handle_of_another_device_is_refused_before_the_launch(monkeypatch):
     for entry in ("cns_route", "cns_route_backward", "cns_grad_norm", "cns_grad_clip"):
         monkeypatch.setattr(_native, entry, lambda *_, entry=entry: reached.append(entry) or 0)
     x = torch.zeros(8, 16)
-    calls = (lambda: cns.run_route(r, x), lambda: cns.run_route_backward(r, x, torch.zeros(8, 2)),
+    calls = (lambda: cns.run_route(r, x), lambda: cns.run_route_backward(r, x, torch.zeros(8, 2), dlogits=torch.zeros(8, 16)),
              lambda: cns.run_grad_norm(g), lambda: cns.run_grad_clip(g))
     for call in calls:
         call()
