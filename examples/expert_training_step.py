@@ -20,6 +20,18 @@ import torch  # noqa: E402
 import counted_notify_sync_gb300 as cns  # noqa: E402
 
 
+class RoutedGradient(torch.autograd.Function):
+    """The logits' gradient from the weights'.  It has no derivative of its own, and says so."""
+
+    @staticmethod
+    def forward(ctx, logits, dweights, ids, route):
+        return cns.run_route_backward(route, logits, dweights.contiguous(), ids=ids, stream=torch.cuda.current_stream())
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the routing is differentiable once")
+
+
 class Routed(torch.autograd.Function):
     """Weights of the chosen experts; `route` holds the ids and the plan afterwards."""
 
@@ -36,8 +48,7 @@ class Routed(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dweights, _):
         logits, ids = ctx.saved_tensors
-        return cns.run_route_backward(ctx.route, logits, dweights.contiguous(), ids=ids,
-                                      stream=torch.cuda.current_stream()), None, None
+        return RoutedGradient.apply(logits, dweights, ids, ctx.route), None, None
 
 
 class Experts(torch.nn.Module):
