@@ -115,3 +115,45 @@ def test_a_new_gradient_tensor_is_of_the_calls_stream(cns):
             got = cns.run_route_backward(r, x, dw, stream=given)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+def test_gradients_and_norms_in_a_graph(cns):
+    """cns_route_backward and cns_grad_norm captured, with the routing and the clipping around them; replays compute
+    on what the tensors then hold."""
+    import torch
+    s = torch.cuda.Stream()
+    r = cns.new_route(3000, 96, 6, score=steps.SIGMOID, scale=2.5)
+    x, dw = torch.randn(3000, 96, device="cuda"), torch.randn(3000, 6, device="cuda")
+    dx, out = torch.empty_like(x), torch.empty_like(x)
+    small = torch.randn(40, device="cuda")
+    norm, clip = cns.new_grad_clip([dx, small]), cns.new_grad_clip([dx], 0.5, outs=[out])
+    cns.run_route_backward(cns.run_route(r, x), x, dw)              # the kernels are loaded
+    cns.run_grad_norm(norm)
+    cns.run_grad_clip(clip)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        cns.run_route(r, x, stream=s)
+        cns.run_route_backward(r, x, dw, dlogits=dx, stream=s)
+        cns.run_grad_norm(norm, stream=s)
+        cns.run_grad_clip(clip, stream=s)
+    results = lambda: [t.clone() for t in (r.ids, r.weights, r.order, dx, norm.norm, clip.norm, out)]  # noqa: E731
+    for _ in range(3):
+        x.copy_(torch.randn_like(x))
+        dw.copy_(torch.randn_like(dw))
+        small.copy_(torch.randn_like(small))
+        for t in (dx, out, norm.norm, clip.norm):
+            t.fill_(-7.0)
+        graph.replay()
+        replayed = results()
+        torch.cuda.synchronize()
+        for t in (dx, out, norm.norm, clip.norm):
+            t.fill_(-7.0)
+        cns.run_route(r, x)
+        cns.run_route_backward(r, x, dw, dlogits=dx)
+        cns.run_grad_norm(norm)
+        cns.run_grad_clip(clip)
+        assert all(torch.equal(a, b) for a, b in zip(replayed, results()))
+        both = torch.cat([dx.reshape(-1), small]).double()
+        assert abs(norm.norm.item() / float(torch.linalg.vector_norm(both)) - 1) < 4.1e-6
+        assert clip.norm.item() < norm.norm.item()
