@@ -291,12 +291,12 @@ __device__ __forceinline__ float joined(const float *r)
         most = max(most, __float_as_uint(r[i]));
     float norm = __uint_as_float(__reduce_max_sync(kFullWarp, most));
     if (NORM == CNS_NORM_L2 && norm > 0.f && norm < INFINITY) {
-        // squares of the largest one's parts: nothing overflows
-        const float inverse = 1.f / norm;   // (of a norm below 2^-126 this is inf: then the parts as they are)
+        // squares of the largest one's parts: nothing overflows (a part is the root of a float: 2^-75 to 2^64)
+        const float inverse = 1.f / norm;
         float sum = 0.f;
 #pragma unroll
         for (uint32_t i = 0; i < kStepMaxCtas / 32; ++i) {
-            const float y = inverse < INFINITY ? r[i] * inverse : r[i] / norm;
+            const float y = r[i] * inverse;
             sum = fmaf(y, y, sum);
         }
         norm *= sqrtf(warp_sum(sum));

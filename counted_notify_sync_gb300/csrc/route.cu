@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, MODE == kGradSparse ? 8 : 4) 
     const bool softmax = MODE == kGradSoftmax || p.score == CNS_SCORE_SOFTMAX;
     const bool renorm = MODE != kGradSoftmax && p.renorm;
     constexpr bool whole = MODE != kGradSparse;
+    static_assert(HOLD == 0 || MODE == kGradSoftmax, "only a row that is read again is held");
     grid_dependency_wait();   // launched early: nothing of the tensors before this
     for (int64_t t0 = begin; t0 < p.tokens; t0 += step) {
         const int64_t t = t0 + lane / SEG;
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, MODE == kGradSparse ? 8 : 4) 
         const float *ds = MODE == kGradScores ? p.dscores + t * p.experts : nullptr;
         T *out = static_cast<T *>(p.dlogits) + t * p.dstride;
         float held[HOLD ? HOLD : 1][W];   // the lane's logits, then e^(x - top)
-        if (HOLD && whole) {
+        if (HOLD) {
 #pragma unroll
             for (int j = 0; j < HOLD; ++j) {
                 const int e = (j * SEG + place) * W;
@@ -268,16 +269,10 @@ __global__ void __launch_bounds__(kGradWarps * 32, MODE == kGradSparse ? 8 : 4) 
                 for (int j = 0; j < HOLD; ++j) {
                     if (j * SEG * W >= p.experts)
                         break;   // no lane has any (an expf takes 8 instructions)
-                    const int e = (j * SEG + place) * W;
-                    float w[W];
-                    if (MODE == kGradScores && token && e < p.experts)
-                        load_elems<CNS_DT_F32, W>(ds + e, w);
 #pragma unroll
                     for (int i = 0; i < W; ++i) {
                         held[j][i] = expf(held[j][i] - top);
                         sum += held[j][i];
-                        if (MODE == kGradScores && token && e < p.experts)
-                            mean = fmaf(held[j][i], w[i], mean);
                     }
                 }
             } else if (token) {

@@ -59,14 +59,6 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ float warp_max(float v)
-{
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(kFullWarp, v, d));
-    return v;
-}
-
 // ---------------------------------------------------------------------------
 // The exchange: every CTA sends one 32-bit value, every CTA gets them all
 // ---------------------------------------------------------------------------
