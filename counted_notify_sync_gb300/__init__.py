@@ -1,5 +1,5 @@
 """counted_notify_sync_gb300: SYNCALL epoch barrier and CntNotify on GB300, and device-wide steps of a
-training step built like the barrier's persistent kernels (routing to experts, gradient norm and clipping).
+training step (routing to experts, gradient norm and clipping).
 
 The C ABI (include/cns.h, libcns.so) does all the work; this package is the
 thin Python side: ``_native`` mirrors the C entry points one to one, and the
@@ -249,7 +249,8 @@ def _check_rows(route, x, name, rows, cols, dtype):
 def run_route(route, logits, bias=None, stream=None, sync: bool = False):
     """Route the rows of `logits` ([tokens, experts], float32, bfloat16 or float16, rows at any stride) on
     `stream` (None: the default stream).  Returns `route`, whose tensors hold the results: the first
-    logits.shape[0] rows, and of `order` the first logits.shape[0] * top_k."""
+    logits.shape[0] rows, and of `order` the first logits.shape[0] * top_k.  They are no part of torch's graph:
+    run_route_backward has the gradient (examples/expert_training_step.py joins the two to autograd)."""
     if route.others:
         _check_current(route.index)
     t, route.logits_stride = _check_logits(route, logits, "logits")
@@ -353,8 +354,9 @@ def _tensor_table(tensors, index, what):
 def new_grad_clip(grads, max_norm: float = float("inf"), *, outs=None, eps: float = 1e-6,
                   norm_type: int = _native.CNS_NORM_L2, workspace=None, timeout_ms: int = 0, device=None, stream=None):
     """The gradients of a step (a list of dense tensors, float32, bfloat16 or float16 mixed as they come) and
-    where their clipped values go: `outs`, tensors of the same shapes and strides, or in place.  Holds the
-    tensors' addresses, so it stands for these tensors for as long as they live; make another one for others.
+    where their clipped values go: `outs`, tensors of the same shapes and strides, or in place.  Holds these
+    tensors and their addresses: for others make another one.  A program that drops its gradients and lets torch make
+    new ones (zero_grad() does, unless set_to_none=False) would go on clipping the old ones.
     `norm` is the float32 scalar that run_grad_norm and run_grad_clip fill.  Enqueues the zeroing of its workspace
     on torch's current stream: see new_step_workspace for the streams that are ordered behind it."""
     torch = _torch()

@@ -16,7 +16,7 @@
 // is chosen so that the last round is as full as the others.
 //
 // Bound.  The norm reads its bytes once: HBM (400M bf16 elements: 112.9 us, 7.1
-// TB/s, 106 % of the measured copy rate).  Clipping has to read everything
+// TB/s, 104 % of the measured copy rate).  Clipping has to read everything
 // before it can write anything, so a set larger than the chip is read twice
 // and written once: 400M bf16 to bf16 367 us, 6.5 TB/s over 2.4 GB.  What the
 // chip holds it reads once:

@@ -198,9 +198,12 @@ __device__ __forceinline__ void store_elems(typename Elem<D>::type *a, const flo
 // tokens and its reductions serve them together), W elements of 16 bytes a
 // lane; each lane also has one place.  For the softmax a row of up to HOLD
 // vectors a lane stays in registers, longer ones (and rows at odd addresses) are
-// read from L1 a second and a third time: 50021 x 160 f32 13.8 us (4.8 TB/s)
-// held, 16.7 us read again, and 19 us with a register budget that spills.  The
-// sparse forms write zeros and the chosen ones: 16384 x 256 f32 4.8 us (3.8 TB/s).
+// read from L1 a second and a third time, and their exponentials taken twice:
+// 50021 x 160 f32 13.8 us (4.8 TB/s) held, 18.1 us read again.  The sparse forms
+// write zeros and the chosen ones: 16384 x 256 f32 4.5 us of the GPU (4.1 TB/s).
+// Exponentials are expf: by ex2.approx of a rounded product the first took 13.4
+// us, and gradients far below the row's largest were off by up to 4e-6 of
+// themselves; now they are within 1.9e-6.
 template <int D, int W, int SEG, int HOLD, int MODE>
 __global__ void __launch_bounds__(kGradWarps * 32, MODE == kGradSparse ? 8 : 4) route_backward_kernel(const RouteGradParams p)
 {

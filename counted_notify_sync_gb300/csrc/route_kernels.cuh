@@ -29,8 +29,9 @@
 // those of others (not where groups are compared).  Now 530 instructions a token
 // of 384 experts with a bias, 76 % of the issue slots and 61 % of the half-rate
 // pipe that min, max and compare share (the plan has 70 more): 65536 x 384 bf16
-// 49 us, 16384 x 256 f32 with groups 23 us (8.8 and 2.8 us of them are the
-// bytes' time).
+// 48 us, 16384 x 256 f32 with groups 23 us (8.6 and 2.8 us of them are the
+// bytes' time).  A softmax's sum, where the weights, the scores or the choice
+// need it, is of expf: 3001 x 160 11.6 us, 11.35 by the approximate one.
 //
 // Plan.  CTA b has a stretch of tokens and each of its warps a stretch of
 // those, so that entries in order are warps in order.  The first grid chooses
@@ -319,12 +320,15 @@ constexpr float kQuanta = kLeastQuanta - 64.f;
 
 // Scores lie in [0, 1], biases in [1 - reach, reach - 1].  The approximate
 // sigmoid's error is s (1 - s) (2^-22 + 2^-23.4 |x|) from the exponential, and
-// (2^-24 + 2^-23) s from the sum and the reciprocal: below 2.7e-7 (a softmax
-// score's: s (2^-22 + 2^-23 |x - top|) and two roundings, below 4e-7); what keeps
-// masked experts out adds at most 4.8e-7.  The exact score in 32 bits is within
-// 1.8e-7 of the true one, and the sums with the bias round to 2^-24 of reach
-// each, as the near one's offset with the bias in it does.  Two values, and the
-// quanta round too.
+// (2^-24 + 2^-23) s from the sum and the reciprocal: below 2.7e-7.  A softmax
+// score's, its sum taken as it is for both ways, is s (2^-22 + 2^-23 |x - top|)
+// and two roundings: at the row's largest e^0 is exact and the roundings are
+// left, any other's s is at most 1/2 and falls faster than |x - top| grows, so
+// it is below 1.8e-7.  What keeps masked experts out adds at most 4.8e-7.  The
+// exact score in 32 bits is within 1.8e-7 of the true one: 2.7e-7 + 4.8e-7 +
+// 1.8e-7 = 9.3e-7.  The sums with the bias round to 2^-24 of reach each, as the
+// near one's offset with the bias in it does.  Two values, and the quanta round
+// too.
 __device__ __forceinline__ KeyRules score_rules(float reach)
 {
     KeyRules r;

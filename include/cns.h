@@ -1,7 +1,7 @@
 /*
  * cns.h -- C ABI of libcns: a device-wide epoch barrier (SYNCALL) and a
  * counted notify (CntNotify) for one NVIDIA GB300 GPU (sm_103a), and
- * device-wide steps of a training step built like the barrier's kernels.
+ * device-wide steps of a training step.
  *
  * The operations follow two public descriptions:
  *   [SYNCALL] "PTO-ISA 跨核同步屏障 SYNCALL 实战指南" (the PTO-ISA SYNCALL
@@ -697,12 +697,12 @@ int cns_pipeline_run(cns_pipeline_t *cfg);
 /* Device-wide steps of a training step                                       */
 /* ========================================================================= */
 
-/* Operators in which every CTA needs a part from every other CTA before any
- * can go on.  Clipping by the global gradient norm over many tensors runs as
- * the library's persistent kernels do: data phase (sum); all CTAs meet; data
- * phase (scale).  Routing tokens to experts (choose and count; place the
- * entries by expert) takes two grids, the second set up while the first ends;
- * the norm alone and the routing's gradient take one. */
+/* Operators of a step of training a model with experts.  Clipping by the global
+ * gradient norm over many tensors runs as the library's persistent kernels do:
+ * data phase (sum); all CTAs meet; data phase (scale).  In the others no CTA
+ * waits for another.  Routing tokens to experts takes two grids: one chooses
+ * and counts, the other, set up while the first ends, places the entries by
+ * expert.  The norm alone and the routing's gradient take one. */
 
 /* Element types of the tensors below. */
 typedef enum { CNS_DT_F32 = 0, CNS_DT_BF16 = 1, CNS_DT_F16 = 2 } cns_dtype_t;
@@ -846,9 +846,10 @@ typedef enum { CNS_NORM_L2 = 0, CNS_NORM_INF = 1 } cns_norm_t;
  * min(1, max_norm / (norm + eps)) in 32 bits and rounded once to the output's
  * type.  A norm of NaN makes the factor NaN, one of inf makes it 0; a max_norm
  * of inf (no limit) leaves it 1 whatever the norm but NaN, and so does 0 / 0.
- * Squares are summed in 32 bits, a CTA's part at a time (so the norm overflows where
- * such a part does, when gradients near 1e19 come in numbers), and the parts
- * joined without overflow, in an order that depends on the sizes alone.
+ * Squares are summed in 32 bits, a CTA's part at a time (so the norm overflows
+ * where such a part does, when gradients near 1e19 come in numbers, and what
+ * is below 1e-22 loses bits or vanishes), and the parts joined without overflow,
+ * in an order that depends on the sizes alone.
  * Tensors must not overlap, except an output with its own gradient when the
  * two are the same tensor. */
 typedef struct {
