@@ -10,12 +10,15 @@
 // a time bound, so the *stream* is blocked, not the host (§4.3).
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <unistd.h>
 
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <ctime>
 #include <mutex>
+#include <random>
 #include <unordered_map>
 #include <unordered_set>
 #include <vector>
@@ -260,21 +263,27 @@ static int enqueue_wait(cns_cnt_notify_s *n, cudaStream_t s, const cns_wait_info
 // instance, has none: it is one dependent chain).  Every CTA is resident
 // (cooperative launch) and takes its tiles in increasing order, so the tile a
 // CTA waits for is always held by a running CTA (or done).  The tag makes the
-// link words need no initial content: a word holds (tag << 32) | count, and a
-// word from an earlier call carries an earlier tag.  A replay of a CUDA graph
-// that captured the call repeats the call's tag, so the thread that takes a
-// word sets it to 0 (no call has tag 0): the only word a launch leaves behind
-// is its last tile's, which no tile of a launch of the same size reads.  The
-// wait is bounded; if it runs out (only a stalled GPU can make it), the tile's
-// leading entries get count 0 and outcome CNS_OUT_INVALID.
+// links need no initial content, and they get none: the scratch is memory that
+// anything may have been in.  So the tag is 64 bits that nothing else writes
+// down, a random start of the process plus a large odd step a call, and a link
+// is two words, (half of the tag << 32) | count each, which have to agree: what
+// some other data left passes for one with a probability of 2^-96.  (With a call
+// counter of 32 bits as the tag, words {1, a float} of another kernel's exchange
+// in memory that an allocator had handed on were taken for counts.)  A replay of
+// a CUDA graph that captured the call repeats the call's tag, so the thread that
+// takes a link sets it to 0 (no call has a half of 0): the only link a launch
+// leaves behind is its last tile's, which no tile of a launch of the same size
+// reads.  The wait is bounded; if it runs out (only a stalled GPU can make it),
+// the tile's leading entries get count 0 and outcome CNS_OUT_INVALID.
 // ---------------------------------------------------------------------------
 
-// The link words between tiles, one to a 128-byte line: a tile's word is
-// written once and polled by the next tile's CTA, and words that shared lines
-// (16 to a line) made every call ~1.4 us slower (1e6 ops, an A/B on one box).
+// The links between tiles, one to a 128-byte line: a tile's link is written
+// once and polled by the next tile's CTA, and links that shared lines (16 to a
+// line, when they were a word) made every call ~1.4 us slower (1e6 ops, an A/B on
+// one box).
 // A tile holds 16 to 4096 ops, and the kernel has at most kMaxSmCtas CTAs, so
 // a call has at most min(ceil(n / 16), max(ceil(n / 4096), kMaxSmCtas)) tiles.
-constexpr int kLinkStride = 16;   // uint64 words from one tile's link word to the next
+constexpr int kLinkStride = 16;   // uint64 words from one tile's link to the next
 constexpr int64_t kMaxSmCtas = 4096;
 constexpr int64_t sm_max_tiles(int64_t n)
 {
@@ -404,20 +413,23 @@ constexpr int kFixWords = 3;
 
 constexpr uint64_t kSmLinkTimeoutNs = 10ull * 1000000000ull;
 
-__device__ __forceinline__ void sm_publish(uint64_t *link, uint32_t tag, uint32_t c)
+// A link carries its count itself, so its two words need no order with anything.
+__device__ __forceinline__ void sm_publish(uint64_t *link, uint64_t tag, uint32_t c)
 {
-    st_release_gpu_u64(link, (static_cast<uint64_t>(tag) << 32) | c);
+    st_relaxed_gpu_u64(link, tag << 32 | c);
+    st_relaxed_gpu_u64(link + 1, (tag >> 32) << 32 | c);
 }
 
 // Returns false if the wait ran out.
-__device__ __forceinline__ bool sm_take(const uint64_t *link, uint32_t tag, uint32_t *c)
+__device__ __forceinline__ bool sm_take(const uint64_t *link, uint64_t tag, uint32_t *c)
 {
     uint32_t spins = 0;
     uint64_t deadline = 0;
     for (;;) {
-        const uint64_t v = ld_acquire_gpu_u64(link);
-        if (static_cast<uint32_t>(v >> 32) == tag) {
-            *c = static_cast<uint32_t>(v);
+        const uint64_t v = ld_relaxed_gpu_u64(link), w = ld_relaxed_gpu_u64(link + 1);
+        const uint32_t count = static_cast<uint32_t>(v);
+        if (v == (tag << 32 | count) && w == ((tag >> 32) << 32 | count)) {
+            *c = count;
             return true;
         }
         if ((++spins & 63u) == 0u) {
@@ -496,7 +508,7 @@ __device__ __forceinline__ uint32_t f_walk(const uint4 *s_ops, uint2 *s_tr, int 
 
 __global__ void __launch_bounds__(kFThreads, 2) sm_onepass_kernel(const uint4 *ops, int64_t n, int tile_ops,
                                                                   uint32_t init, uint2 *trace, uint64_t *link,
-                                                                  uint32_t tag, uint32_t *final_count)
+                                                                  uint64_t tag, uint32_t *final_count)
 {
     extern __shared__ uint4 f_smem[];
     uint4 *s_ops = f_smem;
@@ -610,8 +622,10 @@ __global__ void __launch_bounds__(kFThreads, 2) sm_onepass_kernel(const uint4 *o
             const int lead = f_next_set(s_setm, 0, cnt);
             uint32_t cp = init;
             if (t == 0 || sm_take(link + (t - 1) * kLinkStride, tag, &cp)) {
-                if (t > 0)   // taken: tag 0 is no call's, so no later launch can take this word again
-                    *reinterpret_cast<volatile uint64_t *>(link + (t - 1) * kLinkStride) = 0ull;
+                if (t > 0) {   // taken: 0 is no call's, so no later launch can take this link again
+                    volatile uint64_t *taken = link + (t - 1) * kLinkStride;
+                    taken[0] = taken[1] = 0ull;
+                }
                 cp = f_walk(s_ops, s_tr, 0, lead, cp);
             } else {
                 for (int i = 0; i < lead; ++i)
@@ -631,10 +645,30 @@ __global__ void __launch_bounds__(kFThreads, 2) sm_onepass_kernel(const uint4 *o
     }
 }
 
-// The kernel's co-resident CTAs per device (set by sm_prepare) and the call
-// tags of this process.
+// The kernel's co-resident CTAs per device (set by sm_prepare).
 static int64_t g_sm_max_ctas[64];
-static std::atomic<uint32_t> g_sm_tag{0};
+
+// A call's tag: no two of a process are alike, and no half of one is 0.
+static uint64_t sm_next_tag()
+{
+    static const uint64_t start = []() -> uint64_t {
+        try {
+            std::random_device rd;
+            return static_cast<uint64_t>(rd()) << 32 | rd();
+        } catch (...) {   // no source of random numbers
+            timespec t{};
+            clock_gettime(CLOCK_MONOTONIC, &t);
+            return (static_cast<uint64_t>(t.tv_sec) * 1000000000u + t.tv_nsec) * 0xd1342543de82ef95ull ^
+                   reinterpret_cast<uintptr_t>(&t) ^ static_cast<uint64_t>(getpid()) << 32;
+        }
+    }();
+    static std::atomic<uint64_t> calls{0};
+    for (;;) {
+        const uint64_t tag = start + ++calls * 0x9e3779b97f4a7c15ull;   // an odd step: 2^64 tags before one returns
+        if (static_cast<uint32_t>(tag) != 0u && tag >> 32 != 0u)
+            return tag;
+    }
+}
 
 // Shared-memory opt-in and the co-residency limit, once per device.
 static int sm_prepare(int device)
@@ -676,16 +710,13 @@ static int sm_launch(const uint4 *ops, int64_t n, uint32_t init, uint2 *trace, u
     tile_ops = std::min<int64_t>(std::max<int64_t>(tile_ops, 16), kTileOps);
     const int64_t tiles = (n + tile_ops - 1) / tile_ops;
     const int64_t grid = tiles < max_ctas ? tiles : max_ctas;
-    uint32_t tag = ++g_sm_tag;
-    if (tag == 0)
-        tag = ++g_sm_tag;
     const uint4 *a0 = ops;
     int64_t a1 = n;
     int a2 = static_cast<int>(tile_ops);
     uint32_t a3 = init;
     uint2 *a4 = trace;
     uint64_t *a5 = link;
-    uint32_t a6 = tag;
+    uint64_t a6 = sm_next_tag();
     uint32_t *a7 = final_dev;
     void *args[] = {&a0, &a1, &a2, &a3, &a4, &a5, &a6, &a7};
     CNS_CUDA(cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(sm_onepass_kernel),

@@ -78,18 +78,6 @@ __device__ __forceinline__ float warp_sum(float v)
 // with the values stored beside it, it saves the release fence, the atomic's
 // round trip and the loads of the values behind the barrier.
 
-__device__ __forceinline__ uint64_t ld_relaxed_gpu_u64(const uint64_t *p)
-{
-    uint64_t v;
-    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void st_relaxed_gpu_u64(uint64_t *p, uint64_t v)
-{
-    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
-}
-
 __device__ __forceinline__ uint64_t *mailbox(uint32_t *header, uint32_t to, uint32_t from)
 {
     return reinterpret_cast<uint64_t *>(header + kStepBoxWord) + to * kStepMaxCtas + from;
