@@ -1,5 +1,6 @@
 """counted_notify_sync_gb300: SYNCALL epoch barrier and CntNotify on GB300, and device-wide steps of a
-training step (routing to experts, gradient norm and clipping).
+training step (the norm before a layer of experts, routing to them, the tokens' rows to them and back, gradient
+norm and clipping).
 
 The C ABI (include/cns.h, libcns.so) does all the work; this package is the
 thin Python side: ``_native`` mirrors the C entry points one to one, and the
@@ -12,8 +13,9 @@ from ._native import *  # noqa: F401,F403  (C names and constants)
 
 __all__ = [n for n in dir(_native) if not n.startswith("_")] + [
     "build", "new_workspace", "run_syncall", "run_statemachine", "run_pipeline",
-    "new_step_workspace", "new_route", "run_route", "run_route_backward", "new_grad_clip", "run_grad_norm",
-    "run_grad_clip",
+    "new_step_workspace", "new_route", "run_route", "run_route_backward", "run_dispatch", "run_dispatch_backward",
+    "run_combine", "run_combine_backward", "new_rms_norm", "run_rms_norm", "run_rms_norm_backward", "new_grad_clip",
+    "run_grad_norm", "run_grad_clip",
 ]
 
 
@@ -138,10 +140,10 @@ def run_pipeline(done, ack, tiles: int, tile_words: int, rounds: int, producer_s
 #
 # A handle (new_route, new_grad_clip) has one workspace and one set of results, so its calls belong to one thread at
 # a time, and those of run_route, run_grad_norm and run_grad_clip to streams that are ordered with one another.
-# run_route_backward only reads the handle: gradients may be taken from several threads at once.  A handle's device
-# has to be the current one at each call.
+# run_route_backward, run_dispatch, run_combine, their gradients and the norm only read the handle: they may be called
+# from several threads at once.  A handle's device has to be the current one at each call.
 
-_CODES = {}   # torch dtype -> cns_dtype_t, filled by the first new_route or new_grad_clip
+_CODES = {}   # torch dtype -> cns_dtype_t, filled by the first new_route, new_rms_norm or new_grad_clip
 
 
 def _dtype_codes():
@@ -271,15 +273,15 @@ def run_route(route, logits, bias=None, stream=None, sync: bool = False):
     return route
 
 
-def _empty_on(stream, like, shape):
+def _empty_on(stream, like, shape, dtype=None):
     """A tensor whose memory is the stream's that the call runs on: torch hands out what calls of its own stream may
     still be using, which comes before that stream's work alone."""
     import torch
     handle = _native.stream_handle(stream) or 0
     if torch.cuda.current_stream().cuda_stream == handle:
-        return like.new_empty(shape)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()):
-        return like.new_empty(shape)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogits=None, stream=None):
@@ -317,6 +319,312 @@ def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogi
     if rc:
         raise _native.CnsError(rc, "cns_route_backward")
     return dlogits
+
+
+def _matrix(x, name, index, rows, cols, dtype):
+    """Elements from row to row (0: packed) of a [rows, cols] tensor."""
+    shape = x.shape
+    if len(shape) == 2 and shape[0] == rows and shape[1] == cols and x.dtype == dtype and x.get_device() == index:
+        step, one = x.stride()
+        if one == 1 or cols == 1:
+            if rows <= 1:
+                return 0
+            if step >= cols:
+                return step
+    raise ValueError(f"{name}: [{rows}, {cols}] {dtype} on CUDA device {index}, rows apart and of unit stride, expected; "
+                     f"got {tuple(shape)} {x.dtype}, strides {x.stride()}, on {x.device}")
+
+
+def _places(route, places, rows):
+    """Address of the places of `rows` tokens: given ones, or those of the route's last call."""
+    if places is not None:
+        _check_rows(route, places, "places", rows, route.top_k, route.types[0])
+        return places.data_ptr()
+    if route.places is None:
+        raise ValueError("a route without a plan has no places")
+    if rows > route.tokens:
+        raise ValueError(f"{rows} tokens, and the route's last call had {route.tokens}")
+    return route.places_dev
+
+
+def _tokens(route, places, *like):
+    """How many tokens a call is for: the rows of the first given tensor, or those of the places."""
+    for x in like:
+        if x is not None:
+            return x.shape[0]
+    return route.tokens if places is None else places.shape[0]
+
+
+def run_dispatch(route, x, *, places=None, rows=None, scales=None, row_scales=None, stream=None):
+    """Sort tokens' rows by expert: rows[places[t, j]] = x[t], for `x` [tokens, width] of any type, rows at any
+    stride.  `places` [tokens, top_k] int32 are the plan's (default: those of run_route's last call); expert e's rows
+    are then rows[offsets[e]:offsets[e + 1]].  `rows` [any number, width] (default: a new tensor of tokens * top_k, of
+    `stream`'s memory); places outside it are passed over (a limited capacity), and rows that no place names stay as they
+    were, in a new tensor whatever its memory held.  With `scales` [tokens, n], of any type, row_scales[places[t, j]] =
+    scales[t] too.  Returns rows, with scales (rows, row_scales).  run_dispatch_backward has the gradient."""
+    if route.others:
+        _check_current(route.index)
+    d, index = _native.Dispatch(), route.index
+    t, width = x.shape
+    dtype, size, top_k = x.dtype, x.element_size(), route.top_k
+    d.x_stride = _matrix(x, "x", index, t, width, dtype) * size
+    d.places_dev = _places(route, places, t)
+    if rows is None:
+        rows = _empty_on(stream, x, (t * top_k, width))
+    n = rows.shape[0]
+    d.rows_stride = _matrix(rows, "rows", index, n, width, dtype) * size
+    if scales is not None:
+        cols, kind, each = scales.shape[-1], scales.dtype, scales.element_size()
+        d.scales_stride = _matrix(scales, "scales", index, t, cols, kind) * each
+        if row_scales is None:
+            row_scales = _empty_on(stream, scales, (n, cols))
+        d.row_scales_stride = _matrix(row_scales, "row_scales", index, n, cols, kind) * each
+        d.scales_dev, d.row_scales_dev, d.scale_bytes = scales.data_ptr(), row_scales.data_ptr(), cols * each
+    elif row_scales is not None:
+        raise ValueError("row_scales without scales")
+    d.x_dev, d.rows_dev, d.row_bytes = x.data_ptr(), rows.data_ptr(), width * size
+    d.tokens, d.rows, d.top_k = t, n, top_k
+    if stream is not None:
+        d.stream = _native.stream_handle(stream)
+    rc = _native.cns_dispatch(d)
+    if rc:
+        raise _native.CnsError(rc, "cns_dispatch")
+    return rows if scales is None else (rows, row_scales)
+
+
+def _combine(route, rows, weights, places, base, y, stream, what):
+    """cns_combine; `what` names the rows and the result in errors."""
+    if route.others:
+        _check_current(route.index)
+    c, index = _native.Combine(), route.index
+    t = _tokens(route, places, y, base)
+    n, width = rows.shape
+    dtype, top_k = rows.dtype, route.top_k
+    c.dtype = _dtype_code(dtype)
+    c.rows_stride = _matrix(rows, what[0], index, n, width, dtype)
+    c.places_dev = _places(route, places, t)
+    if weights is not None:
+        _check_rows(route, weights, "weights", t, top_k, route.types[1])
+        c.weights_dev = weights.data_ptr()
+    if base is not None:
+        c.base_stride, c.base_dev = _matrix(base, "base", index, t, width, dtype), base.data_ptr()
+    if y is None:
+        y = _empty_on(stream, rows, (t, width))
+    else:
+        c.y_stride = _matrix(y, what[1], index, t, width, dtype)
+    c.rows_dev, c.y_dev = rows.data_ptr(), y.data_ptr()
+    c.tokens, c.rows, c.width, c.top_k = t, n, width, top_k
+    if stream is not None:
+        c.stream = _native.stream_handle(stream)
+    rc = _native.cns_combine(c)
+    if rc:
+        raise _native.CnsError(rc, "cns_combine")
+    return y
+
+
+def run_dispatch_backward(route, drows, *, places=None, dx=None, stream=None):
+    """dL/dx of run_dispatch from dL/drows (float32, bfloat16 or float16): dx[t] = the sum over j of
+    drows[places[t, j]], in 32 bits, rounded once.  For the tokens of `dx` (default: a new tensor for those of
+    `places`, or of run_route's last call)."""
+    return _combine(route, drows, None, places, None, dx, stream, ("drows", "dx"))
+
+
+def run_combine(route, rows, *, weights=None, places=None, base=None, y=None, stream=None):
+    """Experts' rows back to their tokens: y[t] = base[t] + the sum over j of weights[t, j] * rows[places[t, j]], in 32
+    bits, rounded once, for rows [any number, width] in float32, bfloat16 or float16.  `weights` [tokens, top_k] float32
+    and `places` default to those of run_route's last call; `base` [tokens, width] (the residual, say) is optional.  The
+    result goes to `y` [tokens, width] (default: a new tensor, of `stream`'s memory), which may be `base`."""
+    if weights is None:
+        if places is not None:
+            raise ValueError("places come with their weights")
+        weights = route.weights
+    return _combine(route, rows, weights, places, base, y, stream, ("rows", "y"))
+
+
+def run_combine_backward(route, rows, dy, *, weights=None, places=None, drows=None, dweights=None, stream=None):
+    """The gradient of run_combine from dL/dy [tokens, width]: (drows, dweights), drows[places[t, j]] = weights[t, j] *
+    dy[t], and dweights[t, j] = dy[t] . rows[places[t, j]], 0 for a place without a row.  `drows` (default: a new tensor
+    like rows): what no place names stays as it was.  `rows` None: no dweights (None is returned); `drows` False: no
+    drows.  The base's gradient is dy."""
+    if route.others:
+        _check_current(route.index)
+    g, index = _native.CombineGrad(), route.index
+    t, width = dy.shape
+    dtype, top_k, (i32, f32) = dy.dtype, route.top_k, route.types
+    g.dtype = _dtype_code(dtype)
+    g.dy_stride = _matrix(dy, "dy", index, t, width, dtype)
+    if weights is None:
+        if places is not None:
+            raise ValueError("places come with their weights")
+        weights = route.weights
+    _check_rows(route, weights, "weights", t, top_k, f32)
+    g.places_dev = _places(route, places, t)
+    n = t * top_k
+    if rows is not None:
+        n = rows.shape[0]
+        g.rows_stride, g.rows_dev = _matrix(rows, "rows", index, n, width, dtype), rows.data_ptr()
+        if dweights is None:
+            dweights = _empty_on(stream, weights, (t, top_k))
+        else:
+            _check_rows(route, dweights, "dweights", t, top_k, f32)
+        g.dweights_dev = dweights.data_ptr()
+    elif dweights is not None:
+        raise ValueError("dweights without rows")
+    elif drows is not None and drows is not False:
+        n = drows.shape[0]
+    if drows is False:
+        drows = None
+    else:
+        if drows is None:
+            drows = _empty_on(stream, dy, (n, width))
+        g.drows_stride, g.drows_dev = _matrix(drows, "drows", index, n, width, dtype), drows.data_ptr()
+    g.weights_dev, g.dy_dev = weights.data_ptr(), dy.data_ptr()
+    g.tokens, g.rows, g.width, g.top_k = t, n, width, top_k
+    if stream is not None:
+        g.stream = _native.stream_handle(stream)
+    rc = _native.cns_combine_backward(g)
+    if rc:
+        raise _native.CnsError(rc, "cns_combine_backward")
+    return drows, dweights
+
+
+def new_rms_norm(width: int, *, eps: float = 1e-6, y: bool = True, scale_block: int | None = None,
+                 scale_type: int = _native.CNS_SCALE_F32, device=None):
+    """A root-mean-square norm of rows of `width` columns (cns_rms_norm_t, see cns.h for the rules).  Its outputs: `y`
+    in the rows' type, and, with scale_block, e4m3 values with scales, one for each block of 32, 64 or 128 columns, or
+    one a row (0): float32 (CNS_SCALE_F32) or powers of two in 8 bits (CNS_SCALE_E8M0).  The handle holds no memory of
+    the GPU."""
+    torch = _torch()
+    _dtype_codes()
+    if not 1 <= width <= _native.CNS_NORM_MAX_WIDTH:
+        raise ValueError(f"width: 1 to {_native.CNS_NORM_MAX_WIDTH} expected, got {width}")
+    if scale_block not in (None, 0, 32, 64, 128):
+        raise ValueError(f"scale_block: None, 0, 32, 64 or 128 expected, got {scale_block}")
+    if not y and scale_block is None:
+        raise ValueError("a norm with neither y nor 8-bit values")
+    n = _native.RmsNorm()
+    device = torch.device(device or "cuda")
+    n.index = torch.cuda.current_device() if device.index is None else device.index
+    n.others = torch.cuda.device_count() > 1
+    n.has_y, n.has_q = y, scale_block is not None
+    n.blocks = -(-width // scale_block) if scale_block else 1
+    n.types = (torch.float8_e4m3fn, torch.float8_e8m0fnu if scale_type == _native.CNS_SCALE_E8M0 else torch.float32,
+               torch.float32)
+    n.width, n.scale_block, n.scale_type, n.eps = width, scale_block or 0, scale_type, eps
+    return n
+
+
+def _gain(norm, gain):
+    """(address, cns_dtype_t) of a norm's gain."""
+    if gain is None:
+        return None, 0
+    if not (gain.is_contiguous() and gain.numel() == norm.width and gain.get_device() == norm.index):
+        raise ValueError(f"gain: contiguous [{norm.width}] on CUDA device {norm.index} expected")
+    return gain.data_ptr(), _dtype_code(gain.dtype)
+
+
+def run_rms_norm(norm, x, gain=None, *, residual=None, h=None, y=None, q=None, scales=None, stream=None):
+    """Normalise the rows of `x` ([rows, width], float32, bfloat16 or float16, rows at any stride) on `stream` (None:
+    the default stream): h = x + residual, y = h / sqrt(mean(h^2) + eps) * gain, q and scales as new_rms_norm says.
+    Returns (h, y, q, scales): h is x without a residual, and what the norm does not have is None.  The results go to
+    the tensors given (h may be x or residual), or to new ones, of `stream`'s memory.  run_rms_norm_backward has the
+    gradient."""
+    index, width = norm.index, norm.width
+    if norm.others:
+        _check_current(index)
+    n = _native.RmsNorm.from_buffer_copy(norm)
+    t, dtype = x.shape[0], x.dtype
+    n.dtype = _dtype_code(dtype)
+    n.x_stride, n.x_dev = _matrix(x, "x", index, t, width, dtype), x.data_ptr()
+    if gain is not None:
+        n.gain_dev, n.gain_dtype = _gain(norm, gain)
+    if residual is not None:
+        n.residual_stride = _matrix(residual, "residual", index, t, width, dtype)
+        if h is None:
+            h = _empty_on(stream, x, (t, width))
+        else:
+            n.h_stride = _matrix(h, "h", index, t, width, dtype)
+        n.residual_dev, n.h_dev = residual.data_ptr(), h.data_ptr()
+    elif h is not None:
+        raise ValueError("h without a residual is x")
+    else:
+        h = x
+    if norm.has_y:
+        if y is None:
+            y = _empty_on(stream, x, (t, width))
+        else:
+            n.y_stride = _matrix(y, "y", index, t, width, dtype)
+        n.y_dev = y.data_ptr()
+    elif y is not None:
+        raise ValueError("y: this norm has none")
+    if norm.has_q:
+        e4m3, kind, _ = norm.types
+        if q is None:
+            q = _empty_on(stream, x, (t, width), e4m3)
+        else:
+            n.q_stride = _matrix(q, "q", index, t, width, e4m3)
+        if scales is None:
+            scales = _empty_on(stream, x, (t, norm.blocks), kind)
+        else:
+            n.scales_stride = _matrix(scales, "scales", index, t, norm.blocks, kind)
+        n.q_dev, n.scales_dev = q.data_ptr(), scales.data_ptr()
+    elif q is not None or scales is not None:
+        raise ValueError("q, scales: this norm has none")
+    n.rows = t
+    if stream is not None:
+        n.stream = _native.stream_handle(stream)
+    rc = _native.cns_rms_norm(n)
+    if rc:
+        raise _native.CnsError(rc, "cns_rms_norm")
+    return h, y, q, scales
+
+
+def run_rms_norm_backward(norm, h, gain, dy, *, dh=None, dx=None, dgain=None, workspace=None, stream=None):
+    """The gradient of run_rms_norm from dL/dy and, through the residual's addition, dL/dh (optional), of the h that it
+    returned: (dx, dgain).  dx is x's and the residual's, in h's type; dgain is float32 [width].  They go to `dx` (which
+    may be dy or dh) and `dgain`, or to new tensors; without a gain, or with dgain False, dgain is None.  `workspace`:
+    any tensor of cns_rms_norm_workspace_bytes that no other call uses meanwhile (default: a new one, of `stream`'s
+    memory)."""
+    index, width = norm.index, norm.width
+    if norm.others:
+        _check_current(index)
+    n = _native.RmsNormGrad()
+    t, dtype = h.shape[0], h.dtype
+    n.dtype = _dtype_code(dtype)
+    n.h_stride, n.h_dev = _matrix(h, "h", index, t, width, dtype), h.data_ptr()
+    n.dy_stride, n.dy_dev = _matrix(dy, "dy", index, t, width, dtype), dy.data_ptr()
+    if gain is not None:
+        n.gain_dev, n.gain_dtype = _gain(norm, gain)
+    if dh is not None:
+        n.dh_stride, n.dh_dev = _matrix(dh, "dh", index, t, width, dtype), dh.data_ptr()
+    if dx is None:
+        dx = _empty_on(stream, h, (t, width))
+    else:
+        n.dx_stride = _matrix(dx, "dx", index, t, width, dtype)
+    n.dx_dev = dx.data_ptr()
+    if dgain is False or (dgain is None and gain is None):
+        dgain = None
+    else:
+        f32 = norm.types[2]
+        if dgain is None:
+            dgain = _empty_on(stream, h, (width,), f32)
+        elif not (dgain.is_contiguous() and dgain.numel() == width and dgain.dtype == f32 and dgain.get_device() == index):
+            raise ValueError(f"dgain: contiguous float32 [{width}] on CUDA device {index} expected")
+        if workspace is None:
+            rc, nbytes = _native.cns_rms_norm_workspace_bytes(t, width)
+            _native.check(rc, "cns_rms_norm_workspace_bytes")
+            workspace = _empty_on(stream, h, (nbytes // 4,), f32)
+        elif not (workspace.is_contiguous() and workspace.get_device() == index):
+            raise ValueError(f"workspace: contiguous, on CUDA device {index} expected")
+        n.dgain_dev, n.workspace_dev = dgain.data_ptr(), workspace.data_ptr()
+        n.workspace_bytes = workspace.numel() * workspace.element_size()
+    n.rows, n.width, n.eps = t, width, norm.eps
+    if stream is not None:
+        n.stream = _native.stream_handle(stream)
+    rc = _native.cns_rms_norm_backward(n)
+    if rc:
+        raise _native.CnsError(rc, "cns_rms_norm_backward")
+    return dx, dgain
 
 
 def _dense(t):

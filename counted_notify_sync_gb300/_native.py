@@ -91,6 +91,10 @@ CNS_ROUTE_MAX_EXPERTS = 512
 CNS_ROUTE_MAX_TOP_K = 32
 CNS_ROUTE_MAX_GROUPS = 32
 CNS_GRAD_MAX_TENSORS = 1048576
+CNS_ROWS_MAX_BYTES = 16777216
+CNS_SCALE_F32 = 0
+CNS_SCALE_E8M0 = 1
+CNS_NORM_MAX_WIDTH = 32768
 
 
 class CnsError(RuntimeError):
@@ -150,6 +154,52 @@ class RouteGrad(Structure):
     ]
 
 
+class Dispatch(Structure):
+    _fields_ = [
+        ("x_dev", c_void_p), ("rows_dev", c_void_p), ("scales_dev", c_void_p), ("row_scales_dev", c_void_p),
+        ("places_dev", c_void_p), ("stream", c_void_p), ("tokens", c_int64), ("rows", c_int64), ("row_bytes", c_int64),
+        ("scale_bytes", c_int64), ("x_stride", c_int64), ("rows_stride", c_int64), ("scales_stride", c_int64),
+        ("row_scales_stride", c_int64), ("top_k", c_int32), ("reserved", c_int32),
+    ]
+
+
+class Combine(Structure):
+    _fields_ = [
+        ("rows_dev", c_void_p), ("places_dev", c_void_p), ("weights_dev", c_void_p), ("base_dev", c_void_p),
+        ("y_dev", c_void_p), ("stream", c_void_p), ("tokens", c_int64), ("rows", c_int64), ("rows_stride", c_int64),
+        ("base_stride", c_int64), ("y_stride", c_int64), ("width", c_int32), ("top_k", c_int32), ("dtype", c_int32),
+        ("reserved", c_int32),
+    ]
+
+
+class CombineGrad(Structure):
+    _fields_ = [
+        ("rows_dev", c_void_p), ("dy_dev", c_void_p), ("places_dev", c_void_p), ("weights_dev", c_void_p),
+        ("drows_dev", c_void_p), ("dweights_dev", c_void_p), ("stream", c_void_p), ("tokens", c_int64),
+        ("rows", c_int64), ("rows_stride", c_int64), ("dy_stride", c_int64), ("drows_stride", c_int64),
+        ("width", c_int32), ("top_k", c_int32), ("dtype", c_int32), ("reserved", c_int32),
+    ]
+
+
+class RmsNorm(Structure):
+    _fields_ = [
+        ("x_dev", c_void_p), ("residual_dev", c_void_p), ("gain_dev", c_void_p), ("h_dev", c_void_p),
+        ("y_dev", c_void_p), ("q_dev", c_void_p), ("scales_dev", c_void_p), ("stream", c_void_p), ("rows", c_int64),
+        ("x_stride", c_int64), ("residual_stride", c_int64), ("h_stride", c_int64), ("y_stride", c_int64),
+        ("q_stride", c_int64), ("scales_stride", c_int64), ("width", c_int32), ("dtype", c_int32),
+        ("gain_dtype", c_int32), ("scale_block", c_int32), ("scale_type", c_int32), ("eps", c_float),
+    ]
+
+
+class RmsNormGrad(Structure):
+    _fields_ = [
+        ("h_dev", c_void_p), ("gain_dev", c_void_p), ("dy_dev", c_void_p), ("dh_dev", c_void_p), ("dx_dev", c_void_p),
+        ("dgain_dev", c_void_p), ("workspace_dev", c_void_p), ("workspace_bytes", c_uint64), ("stream", c_void_p),
+        ("rows", c_int64), ("h_stride", c_int64), ("dy_stride", c_int64), ("dh_stride", c_int64),
+        ("dx_stride", c_int64), ("width", c_int32), ("dtype", c_int32), ("gain_dtype", c_int32), ("eps", c_float),
+    ]
+
+
 class Tensor(Structure):
     _fields_ = [("data_dev", c_void_p), ("elems", c_int64), ("dtype", c_int32), ("reserved", c_int32)]
 
@@ -194,6 +244,12 @@ _SIGS = {
     "cns_route_workspace_bytes": (c_int, [c_int64, c_int32, c_int32, POINTER(c_size_t)]),
     "cns_route": (c_int, [POINTER(Route)]),
     "cns_route_backward": (c_int, [POINTER(RouteGrad)]),
+    "cns_dispatch": (c_int, [POINTER(Dispatch)]),
+    "cns_combine": (c_int, [POINTER(Combine)]),
+    "cns_combine_backward": (c_int, [POINTER(CombineGrad)]),
+    "cns_rms_norm": (c_int, [POINTER(RmsNorm)]),
+    "cns_rms_norm_workspace_bytes": (c_int, [c_int64, c_int32, POINTER(c_size_t)]),
+    "cns_rms_norm_backward": (c_int, [POINTER(RmsNormGrad)]),
     "cns_grad_workspace_bytes": (c_int, [c_int64, POINTER(c_size_t)]),
     "cns_grad_norm": (c_int, [POINTER(GradClip)]),
     "cns_grad_clip": (c_int, [POINTER(GradClip)]),
@@ -417,6 +473,33 @@ def cns_route(r: Route) -> int:
 
 def cns_route_backward(g: RouteGrad) -> int:
     return lib().cns_route_backward(ctypes.byref(g))
+
+
+def cns_dispatch(d: Dispatch) -> int:
+    return lib().cns_dispatch(ctypes.byref(d))
+
+
+def cns_combine(c: Combine) -> int:
+    return lib().cns_combine(ctypes.byref(c))
+
+
+def cns_combine_backward(g: CombineGrad) -> int:
+    return lib().cns_combine_backward(ctypes.byref(g))
+
+
+def cns_rms_norm(n: RmsNorm) -> int:
+    return lib().cns_rms_norm(ctypes.byref(n))
+
+
+def cns_rms_norm_workspace_bytes(rows: int, width: int, out: bool = True):
+    """(code, bytes); out=False passes a NULL bytes pointer."""
+    v = c_size_t(0)
+    rc = lib().cns_rms_norm_workspace_bytes(rows, width, ctypes.byref(v) if out else None)
+    return rc, v.value
+
+
+def cns_rms_norm_backward(n: RmsNormGrad) -> int:
+    return lib().cns_rms_norm_backward(ctypes.byref(n))
 
 
 def cns_grad_workspace_bytes(count: int, out: bool = True):

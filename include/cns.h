@@ -702,7 +702,9 @@ int cns_pipeline_run(cns_pipeline_t *cfg);
  * data phase (sum); all CTAs meet; data phase (scale).  In the others no CTA
  * waits for another.  Routing tokens to experts takes two grids: one chooses
  * and counts, the other, set up while the first ends, places the entries by
- * expert.  The norm alone and the routing's gradient take one. */
+ * expert.  The norm alone and the routing's gradient take one.  Around the
+ * experts' products, which are the caller's: the rows' norm before the router,
+ * the rows to their experts and back, and the gradients of these. */
 
 /* Element types of the tensors below. */
 typedef enum { CNS_DT_F32 = 0, CNS_DT_BF16 = 1, CNS_DT_F16 = 2 } cns_dtype_t;
@@ -827,6 +829,190 @@ typedef struct {
  * Errors: NULL_PTR, INVALID_VALUE, ARCH, CUDA.
  */
 int cns_route_backward(const cns_route_grad_t *g);
+
+/* ---- Rows to their experts and back -------------------------------------- */
+
+/* places[t][j] is the row of token t's place j, as a routing's plan gives it.
+ * A place outside 0 .. rows - 1 (-1, or past the end of a buffer of limited
+ * capacity) has no row: nothing is read, written or added for it.  The others
+ * are all different.  Rows that no place names are neither read nor written.
+ * Outputs must not overlap inputs.  Strides are from row to row; 0 = packed. */
+
+/* Dispatch: rows[places[t][j]] = x[t], as bytes, whatever the elements are;
+ * and, with scales_dev, row_scales[places[t][j]] = scales[t] (the scales of
+ * 8-bit rows, say).  Its gradient is cns_combine without weights. */
+typedef struct {
+    const void *x_dev;          /* (in) [tokens][row_bytes] */
+    void *rows_dev;             /* (out) [rows][row_bytes] */
+    const void *scales_dev;     /* (in, optional) [tokens][scale_bytes] */
+    void *row_scales_dev;       /* (out) [rows][scale_bytes]; NULL if scales_dev is */
+    const int32_t *places_dev;  /* (in) [tokens][top_k] */
+    cns_stream_t stream;        /* (in) */
+    int64_t tokens;             /* (in) >= 0; tokens * top_k < 2^31 */
+    int64_t rows;               /* (in) >= 0 */
+    int64_t row_bytes;          /* (in) 1 .. CNS_ROWS_MAX_BYTES */
+    int64_t scale_bytes;        /* (in) 1 .. CNS_ROWS_MAX_BYTES with scales_dev, else 0 */
+    int64_t x_stride;           /* (in) bytes */
+    int64_t rows_stride;        /* (in) bytes */
+    int64_t scales_stride;      /* (in) bytes */
+    int64_t row_scales_stride;  /* (in) bytes */
+    int32_t top_k;              /* (in) 1 .. CNS_ROUTE_MAX_TOP_K */
+    int32_t reserved;           /* 0 */
+} cns_dispatch_t;
+
+#define CNS_ROWS_MAX_BYTES 16777216
+
+/*
+ * cns_dispatch -- asynchronous; may be captured into a CUDA graph.
+ * Errors: NULL_PTR, INVALID_VALUE (sizes, strides, alignment of places_dev,
+ * equal addresses), ARCH, CUDA.
+ */
+int cns_dispatch(const cns_dispatch_t *d);
+
+/* Combine: y[t] = base[t] + sum over j of weights[t][j] * rows[places[t][j]],
+ * products and sums in 32 bits in rising j, the base last, rounded once.
+ * Without weights_dev every weight is 1: that is a dispatch's gradient, rows
+ * the gradient of the dispatched rows and y that of x. */
+typedef struct {
+    const void *rows_dev;       /* (in) [rows][width] */
+    const int32_t *places_dev;  /* (in) [tokens][top_k] */
+    const float *weights_dev;   /* (in, optional) [tokens][top_k] */
+    const void *base_dev;       /* (in, optional) [tokens][width] */
+    void *y_dev;                /* (out) [tokens][width]; may be base_dev, at base's stride */
+    cns_stream_t stream;        /* (in) */
+    int64_t tokens;             /* (in) >= 0; tokens * top_k < 2^31 */
+    int64_t rows;               /* (in) >= 0 */
+    int64_t rows_stride;        /* (in) elements */
+    int64_t base_stride;        /* (in) elements */
+    int64_t y_stride;           /* (in) elements */
+    int32_t width;              /* (in) 1 .. CNS_ROWS_MAX_BYTES / 4 */
+    int32_t top_k;              /* (in) 1 .. CNS_ROUTE_MAX_TOP_K */
+    int32_t dtype;              /* (in) cns_dtype_t of rows, base and y */
+    int32_t reserved;           /* 0 */
+} cns_combine_t;
+
+/*
+ * cns_combine -- asynchronous; may be captured into a CUDA graph.
+ * Errors: NULL_PTR, INVALID_VALUE, ARCH, CUDA.
+ */
+int cns_combine(const cns_combine_t *c);
+
+/* Combine's gradient: drows[places[t][j]] = weights[t][j] * dy[t], the product
+ * in 32 bits, rounded once; dweights[t][j] = the sum over the columns of
+ * dy[t] * rows[places[t][j]] in 32 bits, in an order that depends on the width
+ * alone, 0 for a place without a row.  The base's gradient is dy itself. */
+typedef struct {
+    const void *rows_dev;       /* (in) [rows][width], the forward call's; NULL without dweights_dev */
+    const void *dy_dev;         /* (in) [tokens][width] */
+    const int32_t *places_dev;  /* (in) [tokens][top_k] */
+    const float *weights_dev;   /* (in, optional) [tokens][top_k]; NULL: all 1 */
+    void *drows_dev;            /* (out, optional) [rows][width] */
+    float *dweights_dev;        /* (out, optional) [tokens][top_k] */
+    cns_stream_t stream;        /* (in) */
+    int64_t tokens;             /* (in) >= 0; tokens * top_k < 2^31 */
+    int64_t rows;               /* (in) >= 0 */
+    int64_t rows_stride;        /* (in) elements */
+    int64_t dy_stride;          /* (in) elements */
+    int64_t drows_stride;       /* (in) elements */
+    int32_t width;              /* (in) 1 .. CNS_ROWS_MAX_BYTES / 4 */
+    int32_t top_k;              /* (in) 1 .. CNS_ROUTE_MAX_TOP_K */
+    int32_t dtype;              /* (in) cns_dtype_t of rows, dy and drows */
+    int32_t reserved;           /* 0 */
+} cns_combine_grad_t;
+
+/*
+ * cns_combine_backward -- asynchronous; may be captured into a CUDA graph.
+ * Errors: NULL_PTR (neither output among them), INVALID_VALUE, ARCH, CUDA.
+ */
+int cns_combine_backward(const cns_combine_grad_t *g);
+
+/* ---- Root-mean-square norm ------------------------------------------------ */
+
+/* The scales of an 8-bit output: 32-bit numbers, or powers of two in 8 bits,
+ * the exponent plus 127 (255: NaN). */
+typedef enum { CNS_SCALE_F32 = 0, CNS_SCALE_E8M0 = 1 } cns_scale_t;
+
+#define CNS_NORM_MAX_WIDTH 32768
+
+/* Norm of each row, with the residual's addition:
+ *   h = x + residual in 32 bits, rounded to dtype (x without a residual);
+ *   y = h * r * gain in 32 bits, r = 1 / sqrt(mean of h^2 + eps), rounded once
+ *       to dtype where y_dev takes it.
+ * The squares are summed in 32 bits: a row whose sum overflows gets r = 0.
+ *   In 8 bits (q_dev): each row's columns in blocks of scale_block (the last
+ * may be shorter), or the whole row as one.  m = the block's largest |y|, of
+ * the y in 32 bits:
+ *   CNS_SCALE_F32   s = max(m / 448, 2^-126);
+ *   CNS_SCALE_E8M0  s = the least power of two >= m / 448, from 2^-127 on;
+ *   q = y / s rounded to the nearest e4m3 (ties to even).
+ * A block with an infinity or a NaN has s = NaN and q = NaN throughout. */
+typedef struct {
+    const void *x_dev;         /* (in) [rows][width] */
+    const void *residual_dev;  /* (in, optional) [rows][width] */
+    const void *gain_dev;      /* (in, optional) [width]; NULL: all 1 */
+    void *h_dev;               /* (out) [rows][width]; NULL without residual_dev; may be x_dev or residual_dev, at
+                                  its stride */
+    void *y_dev;               /* (out, optional) [rows][width] */
+    uint8_t *q_dev;            /* (out, optional) [rows][width], e4m3 */
+    void *scales_dev;          /* (out) [rows][blocks] of scale_type; NULL if q_dev is */
+    cns_stream_t stream;       /* (in) */
+    int64_t rows;              /* (in) >= 0 */
+    int64_t x_stride;          /* (in) elements from row to row, >= width; 0 = width (scales_stride: blocks) */
+    int64_t residual_stride;   /* (in) */
+    int64_t h_stride;          /* (in) */
+    int64_t y_stride;          /* (in) */
+    int64_t q_stride;          /* (in) */
+    int64_t scales_stride;     /* (in) */
+    int32_t width;             /* (in) 1 .. CNS_NORM_MAX_WIDTH */
+    int32_t dtype;             /* (in) cns_dtype_t of x, residual, h and y */
+    int32_t gain_dtype;        /* (in) cns_dtype_t */
+    int32_t scale_block;       /* (in) 32, 64 or 128; 0: the row */
+    int32_t scale_type;        /* (in) cns_scale_t */
+    float eps;                 /* (in) >= 0, finite */
+} cns_rms_norm_t;
+
+/*
+ * cns_rms_norm -- asynchronous; may be captured into a CUDA graph.
+ * Errors: NULL_PTR (no output at all among them), INVALID_VALUE, ARCH, CUDA.
+ */
+int cns_rms_norm(const cns_rms_norm_t *n);
+
+/* The norm's gradient, from dL/dy and, through the residual's addition, dL/dh:
+ *   dx = dh + r * g - h * r^3 * mean of (g * h),  g = gain * dy,
+ * in 32 bits, rounded once; it is the residual's gradient too; and
+ *   dgain = sum over the rows of dy * h * r, in 32 bits, in an order that
+ * depends on the sizes alone. */
+typedef struct {
+    const void *h_dev;         /* (in) [rows][width], the forward call's h (its x without a residual) */
+    const void *gain_dev;      /* (in, optional) */
+    const void *dy_dev;        /* (in) [rows][width] */
+    const void *dh_dev;        /* (in, optional) [rows][width] */
+    void *dx_dev;              /* (out) [rows][width]; may be dy_dev or dh_dev, at its stride */
+    float *dgain_dev;          /* (out, optional) [width] */
+    void *workspace_dev;       /* (in) with dgain_dev: scratch, 16-byte aligned, no initial content; calls that may
+                                  overlap on the GPU need one each */
+    uint64_t workspace_bytes;  /* (in) >= cns_rms_norm_workspace_bytes */
+    cns_stream_t stream;       /* (in) */
+    int64_t rows;              /* (in) >= 0 */
+    int64_t h_stride;          /* (in) elements from row to row, >= width; 0 = width */
+    int64_t dy_stride;         /* (in) */
+    int64_t dh_stride;         /* (in) */
+    int64_t dx_stride;         /* (in) */
+    int32_t width;             /* (in) 1 .. CNS_NORM_MAX_WIDTH */
+    int32_t dtype;             /* (in) cns_dtype_t of h, dy, dh and dx */
+    int32_t gain_dtype;        /* (in) cns_dtype_t */
+    float eps;                 /* (in) >= 0, finite */
+} cns_rms_norm_grad_t;
+
+/* Workspace bytes of a gradient of up to `rows` rows.  Host only.
+ * Errors: NULL_PTR (bytes), INVALID_VALUE (rows < 0, width out of range). */
+int cns_rms_norm_workspace_bytes(int64_t rows, int32_t width, size_t *bytes);
+
+/*
+ * cns_rms_norm_backward -- asynchronous; may be captured into a CUDA graph.
+ * Errors: NULL_PTR, INVALID_VALUE, ARCH, CUDA.
+ */
+int cns_rms_norm_backward(const cns_rms_norm_grad_t *g);
 
 /* ---- Global gradient norm and clipping ------------------------------------ */
 

@@ -1,0 +1,302 @@
+"""cns_rms_norm and cns_rms_norm_backward on the GPU against the definitions in 64 bits.
+
+Tolerances.  h is one sum in 32 bits and one rounding: equal bit for bit.  The sum of squares has only positive terms,
+so it is off by at most its longest path of roundings: 32 squares in a thread, 5 exchanges, 32 warps, under 70, each 2^-24;
+the root halves that.  The division, the addition of eps, the root and its reciprocal (half of the first two count), and
+the two products make 41 * 2^-24 of y altogether, and one rounding to its type.
+  A block's scale is the largest |y| (41), divided once.  A value in 8 bits is off by half a step of e4m3 at y / s, and
+by 41 + 3 roundings of y; a power of two may only be the next one where y / 448 is that close to it.
+  dx is the sum of r g, off by its 41 + 2 roundings, and h r (mean of g h) r^2: the mean is off by a path under 70 of the
+sum of the magnitudes, the rest by 3 * 41 + 6; under 200 of the magnitudes.  dgain sums over the rows in whatever order:
+at most a rounding for each of them, and 41 + 3 of each product."""
+import numpy as np
+import pytest
+
+from oracle import steps
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+TINY = {"f32": 2.0 ** -149, "bf16": 2.0 ** -133, "f16": 2.0 ** -25}
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def cns():
+    import torch
+    import counted_notify_sync_gb300 as c
+    c.build()
+    torch.cuda.set_device(0)
+    return c
+
+
+def types():
+    import torch
+    return {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def matrix(rng, rows, cols, dtype, pad=0, shift=0, scale=1.0):
+    """[rows, cols] values of the type within a larger buffer: `pad` columns more from row to row, `shift` before."""
+    import torch
+    n = rows * (cols + pad) + shift + 1
+    buf = torch.from_numpy((rng.randn(n) * scale).astype(np.float32)).to(types()[dtype]).cuda()
+    return buf[shift:shift + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+def check_scales(s, y, block, power):
+    want = steps.scales(y, block, power)
+    assert (np.isnan(s) == np.isnan(want)).all()
+    ok = ~np.isnan(want)
+    if not power:
+        assert (np.abs(s - want)[ok] <= 43 * U * want[ok]).all()
+        return
+    # the power of two of a value within the tolerance
+    low, high = steps.scales(y * (1 - 43 * U), block, True), steps.scales(y * (1 + 43 * U), block, True)
+    assert ((s == low) | (s == high))[ok].all()
+
+
+def check_values(q, s, y, block):
+    """q * s against y, with the scales that came back."""
+    width = y.shape[1]
+    s = np.repeat(s, block or width, axis=1)[:, :width]
+    ok = ~np.isnan(s)
+    assert np.isnan(q[~ok]).all() and not np.isnan(q[ok]).any()
+    y, q, s = y[ok], q[ok], s[ok]
+    v = np.abs(y) / s * (1 + 1e-5)
+    step = 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(v, 2.0 ** -20))), -6.0) - 3.0)
+    assert (np.abs(q) <= 448.0).all()
+    assert (np.abs(q * s - y) <= step / 2 * s + 44 * U * np.abs(y)).all()
+
+
+def scale_values(t):
+    """Scales as numbers, from either form."""
+    import torch
+    if t.dtype == torch.float32:
+        return host(t)
+    b = t.view(torch.uint8).cpu().numpy().astype(np.float64)
+    return np.where(b == 255, np.nan, 2.0 ** (b - 127))
+
+
+WIDTHS = [1, 7, 8, 64, 100, 128, 129, 256, 520, 1000, 1024, 2049, 2056, 4096, 5000, 8192, 16384, 20480, 32768]
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,pad,shift", [(1, 0, 0), (9, 8, 8), (37, 3, 1)])
+def test_norm(cns, width, dtype, rows, pad, shift):
+    import torch
+    rng = np.random.RandomState(width + rows)
+    x, residual = matrix(rng, rows, width, dtype, pad, shift, 3.0), matrix(rng, rows, width, dtype, pad, shift)
+    sum32 = (x.float() + residual.float()).to(x.dtype)
+    for gain_type in (None, "f32", dtype):
+        gain = None if gain_type is None else matrix(rng, 1, width, gain_type, 0, shift)[0]
+        g = None if gain is None else host(gain)
+        for block, power, use_y, use_residual in ((None, False, True, True), (0, False, True, False), (32, True, False, True),
+                                                  (64, False, True, True), (128, False, False, False), (0, True, True, True),
+                                                  (128, True, True, True)):
+            n = cns.new_rms_norm(width, eps=EPS, y=use_y, scale_block=block,
+                                 scale_type=cns.CNS_SCALE_E8M0 if power else cns.CNS_SCALE_F32)
+            h, y, q, s = cns.run_rms_norm(n, x, gain, residual=residual if use_residual else None)
+            assert h is x if not use_residual else torch.equal(h, sum32)
+            want = steps.rms_norm(host(h), g, EPS)
+            if use_y:
+                assert (np.abs(host(y) - want) <= 41 * U * np.abs(want) + HALF[dtype] * np.abs(want) * (1 + 1e-5) +
+                        TINY[dtype]).all()
+            else:
+                assert y is None
+            if block is None:
+                assert q is None and s is None
+                continue
+            assert q.dtype == torch.float8_e4m3fn and s.shape == (rows, -(-width // block) if block else 1)
+            assert s.dtype == (torch.float8_e8m0fnu if power else torch.float32)
+            check_scales(scale_values(s), want, block, power)
+            check_values(host(q.float()), scale_values(s), want, block)
+
+
+@pytest.mark.parametrize("width,dtype", [(100, "bf16"), (1024, "f32"), (4096, "bf16"), (2049, "f16")])
+def test_given_outputs_and_their_surroundings(cns, width, dtype):
+    """Outputs at odd strides: what lies between the rows stays; h in x's or the residual's place."""
+    import torch
+    rng = np.random.RandomState(5)
+    rows, blocks = 11, -(-width // 32)
+    n = cns.new_rms_norm(width, scale_block=32)
+    x, residual = matrix(rng, rows, width, dtype), matrix(rng, rows, width, dtype)
+    gain = matrix(rng, 1, width, "f32")[0]
+    h, y, q, s = cns.run_rms_norm(n, x, gain, residual=residual)
+    for pad in (8, 5):
+        hb, yb = (torch.full((rows, width + pad), 7.0, dtype=x.dtype, device="cuda") for _ in range(2))
+        qb = torch.full((rows, width + pad), 99, dtype=torch.uint8, device="cuda")
+        sb = torch.full((rows, blocks + pad), 7.0, device="cuda")
+        got = cns.run_rms_norm(n, x, gain, residual=residual, h=hb[:, :width], y=yb[:, :width],
+                               q=qb[:, :width].view(torch.float8_e4m3fn), scales=sb[:, :blocks])
+        for a, b, t in zip(got, (h, y, q, s), (hb, yb, qb, sb)):
+            assert torch.equal(a.float(), b.float())
+            assert (t[:, b.shape[1]:].float() == (99.0 if t is qb else 7.0)).all()
+    for place in (x.clone(), residual.clone()):
+        a, b = (place, residual) if torch.equal(place, x) else (x, place)
+        got = cns.run_rms_norm(n, a, gain, residual=b, h=place)
+        assert got[0] is place and torch.equal(place, h) and torch.equal(got[1], y)
+
+
+def test_rows_at_the_edges_of_the_types(cns):
+    """Zeros, subnormals, the largest values, infinities and NaN."""
+    import torch
+    width = 256
+    for dtype in ("f32", "bf16", "f16"):
+        t = types()[dtype]
+        x = torch.randn(9, width, device="cuda").to(t)
+        x[1] = 0
+        x[2] = torch.finfo(t).tiny
+        x[3, 40] = float("inf")
+        x[4, 50] = float("nan")
+        x[5] = 0
+        x[5, 7] = 60000.0
+        x[6] *= 0.001
+        x[7, 128:] = 0
+        for block, power in ((32, False), (32, True), (0, False), (0, True)):
+            n = cns.new_rms_norm(width, scale_block=block, scale_type=cns.CNS_SCALE_E8M0 if power else cns.CNS_SCALE_F32)
+            _, y, q, s = cns.run_rms_norm(n, x)
+            sv, qv = scale_values(s), host(q.float())
+            assert (host(y)[1] == 0).all() and (qv[1] == 0).all()
+            assert (sv[1] == (2.0 ** -127 if power else 2.0 ** -126)).all()
+            # one infinity: r is 0, the other columns 0, its own NaN; with a NaN the whole row
+            where = torch.isnan(y)
+            assert where[3].sum() == 1 and where[3, 40] and where[4].all() and where.sum() == 1 + width
+            assert np.isnan(sv[3]).sum() == 1 and np.isnan(sv[4]).all()
+            fine = [i for i in range(9) if i not in (3, 4)]
+            want = steps.rms_norm(host(x)[fine], None, EPS)
+            assert (np.abs(host(y)[fine] - want) <= (41 * U + HALF[dtype] * (1 + 1e-5)) * np.abs(want) + TINY[dtype]).all()
+            check_scales(sv[fine], want, block, power)
+            check_values(qv[fine], sv[fine], want, block)
+            if block:
+                assert (sv[7, 4:] == (2.0 ** -127 if power else 2.0 ** -126)).all()
+
+
+@pytest.mark.parametrize("power", [False, True])
+def test_a_power_of_two_at_its_border(cns, power):
+    """Blocks whose largest value is 448 * 2^e, or the next number above, with r exactly 1."""
+    import torch
+    above = np.nextafter(np.float32(448.0), np.float32(1000.0))
+    for value, exponent in ((448.0, 0), (above, 1), (224.0, -1), (np.float32(above / 2), 0), (1.75, -8), (1.0, -8), (np.float32(1.8), -7)):
+        x = torch.zeros(1, 64, device="cuda")
+        x[0, 0], x[0, 63] = 1.0, 0.0
+        gain = torch.full((64,), float(value) / 2, device="cuda")
+        # mean of squares 1/64 and eps 15/64: r = 2
+        n = cns.new_rms_norm(64, eps=15 / 64, scale_block=64, scale_type=cns.CNS_SCALE_E8M0 if power else cns.CNS_SCALE_F32)
+        _, y, q, s = cns.run_rms_norm(n, x, gain)
+        assert y[0, 0].item() == value
+        got = scale_values(s)[0, 0]
+        assert got == (2.0 ** exponent if power else np.float32(value) / np.float32(448.0))
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,pad,shift", [(1, 0, 0), (9, 8, 8), (37, 3, 1), (1500, 0, 0)])
+def test_gradient(cns, width, dtype, rows, pad, shift):
+    import torch
+    if rows * width > 1500 * 5000:
+        rows = 700
+    rng = np.random.RandomState(width * 3 + rows)
+    h, dy, dh = (matrix(rng, rows, width, dtype, pad, shift, k) for k in (2.0, 1.0, 0.5))
+    n = cns.new_rms_norm(width, eps=EPS)
+    for gain_type, use_dh in ((None, False), ("f32", True), (dtype, True)):
+        gain = None if gain_type is None else matrix(rng, 1, width, gain_type, 0, shift)[0]
+        g = None if gain is None else host(gain)
+        want, want_gain, size, size_gain = steps.rms_norm_backward(host(h), g, host(dy), host(dh) if use_dh else None, EPS)
+        dx, dgain = cns.run_rms_norm_backward(n, h, gain, dy, dh=dh if use_dh else None)
+        assert (np.abs(host(dx) - want) <= 200 * U * size + HALF[dtype] * np.abs(want) * (1 + 1e-5) + TINY[dtype]).all()
+        if gain is None:
+            assert dgain is None
+            dgain = torch.empty(width, device="cuda")
+            cns.run_rms_norm_backward(n, h, None, dy, dx=dx, dgain=dgain)
+        assert (np.abs(host(dgain) - want_gain) <= (rows + 44) * U * size_gain).all()
+        alone, none = cns.run_rms_norm_backward(n, h, gain, dy, dh=dh if use_dh else None, dgain=False)
+        assert none is None and torch.equal(alone, dx if gain is not None else alone)
+
+
+def test_gradient_in_place_and_without_rows(cns):
+    import torch
+    torch.manual_seed(2)
+    n = cns.new_rms_norm(1000)
+    h, dy, dh = (torch.randn(300, 1000, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    gain = torch.randn(1000, device="cuda")
+    dx, dgain = cns.run_rms_norm_backward(n, h, gain, dy, dh=dh)
+    for place in (0, 1):
+        a, b = dy.clone(), dh.clone()
+        to = (a, b)[place]
+        got, again = cns.run_rms_norm_backward(n, h, gain, a, dh=b, dx=to)
+        assert got is to and torch.equal(to, dx) and torch.equal(again, dgain)
+    to = torch.full((1000,), 7.0, device="cuda")
+    dx, got = cns.run_rms_norm_backward(n, h[:0], gain, dy[:0], dgain=to)
+    assert dx.shape == (0, 1000) and got is to and to.count_nonzero() == 0
+    out = cns.run_rms_norm(n, h[:0], gain, residual=dy[:0])
+    assert [o.shape for o in out[:2]] == [(0, 1000)] * 2
+
+
+def test_gradient_of_the_norm_against_differences(cns):
+    """dL/dx and dL/dgain of L = sum(y * c) + sum(h * d) by the forward kernel's own central differences."""
+    import torch
+    torch.manual_seed(3)
+    rows, width = 4, 40
+    n = cns.new_rms_norm(width, eps=1e-3)
+    x, residual, c, d = (torch.randn(rows, width, device="cuda") for _ in range(4))
+    gain = torch.rand(width, device="cuda") + 0.5
+
+    def loss(a, g):
+        h, y, _, _ = cns.run_rms_norm(n, a, g, residual=residual)
+        return float((y.double() * c.double()).sum() + (h.double() * d.double()).sum())
+
+    h = cns.run_rms_norm(n, x, gain, residual=residual)[0]
+    dx, dgain = cns.run_rms_norm_backward(n, h, gain, c, dh=d)
+    step = 2.0 ** -7
+    # sums of 320 terms near 1 in 32 bits: off by 2^-22 or so, 2^-15 in the quotient; the third derivative's share is
+    # step^2 / 6 of values below 20
+    for i, j in ((0, 0), (1, 17), (2, 39), (3, 5)):
+        e = torch.zeros_like(x)
+        e[i, j] = step
+        assert abs((loss(x + e, gain) - loss(x - e, gain)) / (2 * step) - dx[i, j].item()) < 5e-4
+    for j in (0, 21, 39):
+        e = torch.zeros_like(gain)
+        e[j] = step
+        assert abs((loss(x, gain + e) - loss(x, gain - e)) / (2 * step) - dgain[j].item()) < 5e-4
+
+
+def test_streams_and_new_tensors(cns):
+    """New outputs and the gradient's workspace are the call's stream's memory."""
+    import torch
+    n = cns.new_rms_norm(1024, scale_block=128)
+    x, r = torch.randn(900, 1024, device="cuda"), torch.randn(900, 1024, device="cuda")
+    gain = torch.randn(1024, device="cuda")
+    calls = [lambda s: cns.run_rms_norm(n, x, gain, residual=r, stream=s), lambda s: cns.run_rms_norm_backward(n, x, gain, r, stream=s)]
+    want = [c(None) for c in calls]
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for current, given in ((torch.cuda.default_stream(), side), (side, None), (side, other), (side, side)):
+        for call, w in zip(calls, want):
+            torch.cuda.synchronize()
+            with torch.cuda.stream(current):
+                late = [torch.empty_like(t) for t in w] + [torch.empty(1 << 20, device="cuda")]
+                a = torch.randn(4096, 4096, device="cuda")
+                for _ in range(4):
+                    a @ a
+                for t in late:
+                    t.view(torch.uint8).fill_(7)
+                del late, t
+                got = call(given)
+            torch.cuda.synchronize()
+            assert all(torch.equal(p.float(), q.float()) for p, q in zip(got, w))
+
+
+def test_results_do_not_depend_on_timing(cns):
+    import torch
+    n = cns.new_rms_norm(2048)
+    h, dy = torch.randn(4001, 2048, device="cuda"), torch.randn(4001, 2048, device="cuda")
+    gain = torch.randn(2048, device="cuda")
+    dx, dgain = cns.run_rms_norm_backward(n, h, gain, dy)
+    for _ in range(5):
+        a, b = cns.run_rms_norm_backward(n, h, gain, dy)
+        assert torch.equal(a, dx) and torch.equal(b, dgain)
