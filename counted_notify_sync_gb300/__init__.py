@@ -321,38 +321,45 @@ def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogi
     return dlogits
 
 
-def _matrix(x, name, index, rows, cols, dtype):
-    """Elements from row to row (0: packed) of a [rows, cols] tensor."""
-    shape = x.shape
-    if len(shape) == 2 and shape[0] == rows and shape[1] == cols and x.dtype == dtype and x.get_device() == index:
-        step, one = x.stride()
-        if one == 1 or cols == 1:
-            if rows <= 1:
-                return 0
-            if step >= cols:
-                return step
-    raise ValueError(f"{name}: [{rows}, {cols}] {dtype} on CUDA device {index}, rows apart and of unit stride, expected; "
-                     f"got {tuple(shape)} {x.dtype}, strides {x.stride()}, on {x.device}")
+def _matrix(x, name, index, shape, dtype):
+    """Elements from row to row (0: packed) of a matrix."""
+    if x.shape == shape and x.dtype is dtype and x.get_device() == index:
+        if x.is_contiguous():
+            return 0
+        (rows, cols), (step, one) = shape, x.stride()
+        if (one == 1 or cols == 1) and (step >= cols or rows <= 1):
+            return step if rows > 1 else 0
+    raise ValueError(f"{name}: {shape} {dtype} on CUDA device {index}, rows apart and of unit stride, expected; got "
+                     f"{tuple(x.shape)} {x.dtype}, strides {x.stride()}, on {x.device}")
 
 
-def _places(route, places, rows):
-    """Address of the places of `rows` tokens: given ones, or those of the route's last call."""
+def _per_place(route, x, name, tokens, dtype):
+    """Address of a value for each place of `tokens` tokens, or of more."""
+    if x.is_contiguous() and x.dtype is dtype and x.get_device() == route.index:
+        shape = x.shape
+        if shape == (tokens, route.top_k) or (len(shape) == 2 and shape[0] > tokens and shape[1] == route.top_k):
+            return x.data_ptr()
+    raise ValueError(f"{name}: contiguous {dtype} [tokens, {route.top_k}] on {route.ids.device} expected")
+
+
+def _places(route, places, tokens):
+    """Address of the places of `tokens` tokens: given ones, or those of the route's last call."""
     if places is not None:
-        _check_rows(route, places, "places", rows, route.top_k, route.types[0])
-        return places.data_ptr()
+        return _per_place(route, places, "places", tokens, route.types[0])
     if route.places is None:
         raise ValueError("a route without a plan has no places")
-    if rows > route.tokens:
-        raise ValueError(f"{rows} tokens, and the route's last call had {route.tokens}")
-    return route.places_dev
+    if tokens > route.tokens:
+        raise ValueError(f"{tokens} tokens, and the route's last call had {route.tokens}")
+    return route.places_dev or 0
 
 
-def _tokens(route, places, *like):
-    """How many tokens a call is for: the rows of the first given tensor, or those of the places."""
-    for x in like:
-        if x is not None:
-            return x.shape[0]
-    return route.tokens if places is None else places.shape[0]
+def _weights(route, weights, places, tokens):
+    """Address of the weights of `tokens` tokens' places: given ones, or those of the route's last call."""
+    if weights is not None:
+        return _per_place(route, weights, "weights", tokens, route.types[1])
+    if places is not None:
+        raise ValueError("places come with their weights")
+    return route.weights_dev or 0
 
 
 def run_dispatch(route, x, *, places=None, rows=None, scales=None, row_scales=None, stream=None):
@@ -364,69 +371,68 @@ def run_dispatch(route, x, *, places=None, rows=None, scales=None, row_scales=No
     scales[t] too.  Returns rows, with scales (rows, row_scales).  run_dispatch_backward has the gradient."""
     if route.others:
         _check_current(route.index)
-    d, index = _native.Dispatch(), route.index
-    t, width = x.shape
-    dtype, size, top_k = x.dtype, x.element_size(), route.top_k
-    d.x_stride = _matrix(x, "x", index, t, width, dtype) * size
-    d.places_dev = _places(route, places, t)
+    index, shape, dtype, size, top_k = route.index, x.shape, x.dtype, x.element_size(), route.top_k
+    t, width = shape
+    x_step, places_at = _matrix(x, "x", index, shape, dtype) * size, _places(route, places, t)
     if rows is None:
-        rows = _empty_on(stream, x, (t * top_k, width))
-    n = rows.shape[0]
-    d.rows_stride = _matrix(rows, "rows", index, n, width, dtype) * size
+        n, rows_step, rows = t * top_k, 0, _empty_on(stream, x, (t * top_k, width))
+    else:
+        n = len(rows)
+        rows_step = _matrix(rows, "rows", index, (n, width), dtype) * size
+    each = scales_at = row_scales_at = scales_step = row_scales_step = 0
     if scales is not None:
-        cols, kind, each = scales.shape[-1], scales.dtype, scales.element_size()
-        d.scales_stride = _matrix(scales, "scales", index, t, cols, kind) * each
+        shape, kind, each = scales.shape, scales.dtype, scales.element_size()
+        cols = shape[-1]
+        scales_step = _matrix(scales, "scales", index, (t, cols), kind) * each
         if row_scales is None:
             row_scales = _empty_on(stream, scales, (n, cols))
-        d.row_scales_stride = _matrix(row_scales, "row_scales", index, n, cols, kind) * each
-        d.scales_dev, d.row_scales_dev, d.scale_bytes = scales.data_ptr(), row_scales.data_ptr(), cols * each
+        row_scales_step = _matrix(row_scales, "row_scales", index, (n, cols), kind) * each
+        scales_at, row_scales_at, each = scales.data_ptr(), row_scales.data_ptr(), cols * each
     elif row_scales is not None:
         raise ValueError("row_scales without scales")
-    d.x_dev, d.rows_dev, d.row_bytes = x.data_ptr(), rows.data_ptr(), width * size
-    d.tokens, d.rows, d.top_k = t, n, top_k
-    if stream is not None:
-        d.stream = _native.stream_handle(stream)
-    rc = _native.cns_dispatch(d)
+    rc = _native.cns_dispatch(_native.make_dispatch(
+        x.data_ptr(), rows.data_ptr(), scales_at, row_scales_at, places_at, _native.stream_handle(stream) or 0, t, n,
+        width * size, each, x_step, rows_step, scales_step, row_scales_step, top_k, 0))
     if rc:
         raise _native.CnsError(rc, "cns_dispatch")
     return rows if scales is None else (rows, row_scales)
 
 
-def _combine(route, rows, weights, places, base, y, stream, what):
-    """cns_combine; `what` names the rows and the result in errors."""
+def _combine(route, rows, t, weights_at, places, base, y, stream, what):
+    """cns_combine for `t` tokens; `what` names the rows and the result in errors."""
     if route.others:
         _check_current(route.index)
-    c, index = _native.Combine(), route.index
-    t = _tokens(route, places, y, base)
-    n, width = rows.shape
-    dtype, top_k = rows.dtype, route.top_k
-    c.dtype = _dtype_code(dtype)
-    c.rows_stride = _matrix(rows, what[0], index, n, width, dtype)
-    c.places_dev = _places(route, places, t)
-    if weights is not None:
-        _check_rows(route, weights, "weights", t, top_k, route.types[1])
-        c.weights_dev = weights.data_ptr()
+    index, shape, dtype, top_k = route.index, rows.shape, rows.dtype, route.top_k
+    n, width = shape
+    code, rows_step, places_at = _dtype_code(dtype), _matrix(rows, what[0], index, shape, dtype), _places(route, places, t)
+    base_at = base_step = y_step = 0
     if base is not None:
-        c.base_stride, c.base_dev = _matrix(base, "base", index, t, width, dtype), base.data_ptr()
+        base_at, base_step = base.data_ptr(), _matrix(base, "base", index, (t, width), dtype)
     if y is None:
         y = _empty_on(stream, rows, (t, width))
     else:
-        c.y_stride = _matrix(y, what[1], index, t, width, dtype)
-    c.rows_dev, c.y_dev = rows.data_ptr(), y.data_ptr()
-    c.tokens, c.rows, c.width, c.top_k = t, n, width, top_k
-    if stream is not None:
-        c.stream = _native.stream_handle(stream)
-    rc = _native.cns_combine(c)
+        y_step = _matrix(y, what[1], index, (t, width), dtype)
+    rc = _native.cns_combine(_native.make_combine(
+        rows.data_ptr(), places_at, weights_at, base_at, y.data_ptr(), _native.stream_handle(stream) or 0, t, n, rows_step,
+        base_step, y_step, width, top_k, code, 0))
     if rc:
         raise _native.CnsError(rc, "cns_combine")
     return y
+
+
+def _tokens(route, places, first, second):
+    """How many tokens a call is for: those of the first tensor given, else of the places."""
+    for x in (first, second, places):
+        if x is not None:
+            return len(x)
+    return route.tokens
 
 
 def run_dispatch_backward(route, drows, *, places=None, dx=None, stream=None):
     """dL/dx of run_dispatch from dL/drows (float32, bfloat16 or float16): dx[t] = the sum over j of
     drows[places[t, j]], in 32 bits, rounded once.  For the tokens of `dx` (default: a new tensor for those of
     `places`, or of run_route's last call)."""
-    return _combine(route, drows, None, places, None, dx, stream, ("drows", "dx"))
+    return _combine(route, drows, _tokens(route, places, dx, None), 0, places, None, dx, stream, ("drows", "dx"))
 
 
 def run_combine(route, rows, *, weights=None, places=None, base=None, y=None, stream=None):
@@ -434,11 +440,8 @@ def run_combine(route, rows, *, weights=None, places=None, base=None, y=None, st
     bits, rounded once, for rows [any number, width] in float32, bfloat16 or float16.  `weights` [tokens, top_k] float32
     and `places` default to those of run_route's last call; `base` [tokens, width] (the residual, say) is optional.  The
     result goes to `y` [tokens, width] (default: a new tensor, of `stream`'s memory), which may be `base`."""
-    if weights is None:
-        if places is not None:
-            raise ValueError("places come with their weights")
-        weights = route.weights
-    return _combine(route, rows, weights, places, base, y, stream, ("rows", "y"))
+    t = _tokens(route, places, y, base)
+    return _combine(route, rows, t, _weights(route, weights, places, t), places, base, y, stream, ("rows", "y"))
 
 
 def run_combine_backward(route, rows, dy, *, weights=None, places=None, drows=None, dweights=None, stream=None):
@@ -448,41 +451,35 @@ def run_combine_backward(route, rows, dy, *, weights=None, places=None, drows=No
     drows.  The base's gradient is dy."""
     if route.others:
         _check_current(route.index)
-    g, index = _native.CombineGrad(), route.index
-    t, width = dy.shape
-    dtype, top_k, (i32, f32) = dy.dtype, route.top_k, route.types
-    g.dtype = _dtype_code(dtype)
-    g.dy_stride = _matrix(dy, "dy", index, t, width, dtype)
-    if weights is None:
-        if places is not None:
-            raise ValueError("places come with their weights")
-        weights = route.weights
-    _check_rows(route, weights, "weights", t, top_k, f32)
-    g.places_dev = _places(route, places, t)
-    n = t * top_k
+    index, shape, dtype, top_k = route.index, dy.shape, dy.dtype, route.top_k
+    t, width = shape
+    code, dy_step = _dtype_code(dtype), _matrix(dy, "dy", index, shape, dtype)
+    weights_at, places_at = _weights(route, weights, places, t), _places(route, places, t)
+    n, rows_at, rows_step, dweights_at = t * top_k, 0, 0, 0
     if rows is not None:
-        n = rows.shape[0]
-        g.rows_stride, g.rows_dev = _matrix(rows, "rows", index, n, width, dtype), rows.data_ptr()
+        n = len(rows)
+        rows_step, rows_at = _matrix(rows, "rows", index, (n, width), dtype), rows.data_ptr()
         if dweights is None:
-            dweights = _empty_on(stream, weights, (t, top_k))
+            dweights = _empty_on(stream, dy, (t, top_k), route.types[1])
+            dweights_at = dweights.data_ptr()
         else:
-            _check_rows(route, dweights, "dweights", t, top_k, f32)
-        g.dweights_dev = dweights.data_ptr()
+            dweights_at = _per_place(route, dweights, "dweights", t, route.types[1])
     elif dweights is not None:
         raise ValueError("dweights without rows")
     elif drows is not None and drows is not False:
-        n = drows.shape[0]
+        n = len(drows)
+    drows_at = drows_step = 0
     if drows is False:
         drows = None
     else:
         if drows is None:
             drows = _empty_on(stream, dy, (n, width))
-        g.drows_stride, g.drows_dev = _matrix(drows, "drows", index, n, width, dtype), drows.data_ptr()
-    g.weights_dev, g.dy_dev = weights.data_ptr(), dy.data_ptr()
-    g.tokens, g.rows, g.width, g.top_k = t, n, width, top_k
-    if stream is not None:
-        g.stream = _native.stream_handle(stream)
-    rc = _native.cns_combine_backward(g)
+        else:
+            drows_step = _matrix(drows, "drows", index, (n, width), dtype)
+        drows_at = drows.data_ptr()
+    rc = _native.cns_combine_backward(_native.make_combine_grad(
+        rows_at, dy.data_ptr(), places_at, weights_at, drows_at, dweights_at, _native.stream_handle(stream) or 0, t, n,
+        rows_step, dy_step, drows_step, width, top_k, code, 0))
     if rc:
         raise _native.CnsError(rc, "cns_combine_backward")
     return drows, dweights
@@ -517,7 +514,7 @@ def new_rms_norm(width: int, *, eps: float = 1e-6, y: bool = True, scale_block: 
 def _gain(norm, gain):
     """(address, cns_dtype_t) of a norm's gain."""
     if gain is None:
-        return None, 0
+        return 0, 0
     if not (gain.is_contiguous() and gain.numel() == norm.width and gain.get_device() == norm.index):
         raise ValueError(f"gain: contiguous [{norm.width}] on CUDA device {norm.index} expected")
     return gain.data_ptr(), _dtype_code(gain.dtype)
@@ -529,51 +526,47 @@ def run_rms_norm(norm, x, gain=None, *, residual=None, h=None, y=None, q=None, s
     Returns (h, y, q, scales): h is x without a residual, and what the norm does not have is None.  The results go to
     the tensors given (h may be x or residual), or to new ones, of `stream`'s memory.  run_rms_norm_backward has the
     gradient."""
-    index, width = norm.index, norm.width
+    index, shape, dtype = norm.index, (len(x), norm.width), x.dtype
     if norm.others:
         _check_current(index)
-    n = _native.RmsNorm.from_buffer_copy(norm)
-    t, dtype = x.shape[0], x.dtype
-    n.dtype = _dtype_code(dtype)
-    n.x_stride, n.x_dev = _matrix(x, "x", index, t, width, dtype), x.data_ptr()
-    if gain is not None:
-        n.gain_dev, n.gain_dtype = _gain(norm, gain)
+    code, x_step, (gain_at, gain_code) = _dtype_code(dtype), _matrix(x, "x", index, shape, dtype), _gain(norm, gain)
+    residual_at = residual_step = h_at = h_step = y_at = y_step = q_at = q_step = scales_at = scales_step = 0
     if residual is not None:
-        n.residual_stride = _matrix(residual, "residual", index, t, width, dtype)
+        residual_step, residual_at = _matrix(residual, "residual", index, shape, dtype), residual.data_ptr()
         if h is None:
-            h = _empty_on(stream, x, (t, width))
+            h = _empty_on(stream, x, shape)
         else:
-            n.h_stride = _matrix(h, "h", index, t, width, dtype)
-        n.residual_dev, n.h_dev = residual.data_ptr(), h.data_ptr()
+            h_step = _matrix(h, "h", index, shape, dtype)
+        h_at = h.data_ptr()
     elif h is not None:
         raise ValueError("h without a residual is x")
     else:
         h = x
     if norm.has_y:
         if y is None:
-            y = _empty_on(stream, x, (t, width))
+            y = _empty_on(stream, x, shape)
         else:
-            n.y_stride = _matrix(y, "y", index, t, width, dtype)
-        n.y_dev = y.data_ptr()
+            y_step = _matrix(y, "y", index, shape, dtype)
+        y_at = y.data_ptr()
     elif y is not None:
         raise ValueError("y: this norm has none")
     if norm.has_q:
-        e4m3, kind, _ = norm.types
+        (e4m3, kind, _), blocks = norm.types, (shape[0], norm.blocks)
         if q is None:
-            q = _empty_on(stream, x, (t, width), e4m3)
+            q = _empty_on(stream, x, shape, e4m3)
         else:
-            n.q_stride = _matrix(q, "q", index, t, width, e4m3)
+            q_step = _matrix(q, "q", index, shape, e4m3)
         if scales is None:
-            scales = _empty_on(stream, x, (t, norm.blocks), kind)
+            scales = _empty_on(stream, x, blocks, kind)
         else:
-            n.scales_stride = _matrix(scales, "scales", index, t, norm.blocks, kind)
-        n.q_dev, n.scales_dev = q.data_ptr(), scales.data_ptr()
+            scales_step = _matrix(scales, "scales", index, blocks, kind)
+        q_at, scales_at = q.data_ptr(), scales.data_ptr()
     elif q is not None or scales is not None:
         raise ValueError("q, scales: this norm has none")
-    n.rows = t
-    if stream is not None:
-        n.stream = _native.stream_handle(stream)
-    rc = _native.cns_rms_norm(n)
+    rc = _native.cns_rms_norm(_native.make_rms_norm(
+        x.data_ptr(), residual_at, gain_at, h_at, y_at, q_at, scales_at, _native.stream_handle(stream) or 0, shape[0], x_step,
+        residual_step, h_step, y_step, q_step, scales_step, shape[1], code, gain_code, norm.scale_block, norm.scale_type,
+        norm.eps))
     if rc:
         raise _native.CnsError(rc, "cns_rms_norm")
     return h, y, q, scales
@@ -585,43 +578,39 @@ def run_rms_norm_backward(norm, h, gain, dy, *, dh=None, dx=None, dgain=None, wo
     may be dy or dh) and `dgain`, or to new tensors; without a gain, or with dgain False, dgain is None.  `workspace`:
     any tensor of cns_rms_norm_workspace_bytes that no other call uses meanwhile (default: a new one, of `stream`'s
     memory)."""
-    index, width = norm.index, norm.width
+    index, shape, dtype = norm.index, (len(h), norm.width), h.dtype
     if norm.others:
         _check_current(index)
-    n = _native.RmsNormGrad()
-    t, dtype = h.shape[0], h.dtype
-    n.dtype = _dtype_code(dtype)
-    n.h_stride, n.h_dev = _matrix(h, "h", index, t, width, dtype), h.data_ptr()
-    n.dy_stride, n.dy_dev = _matrix(dy, "dy", index, t, width, dtype), dy.data_ptr()
-    if gain is not None:
-        n.gain_dev, n.gain_dtype = _gain(norm, gain)
+    code, (gain_at, gain_code) = _dtype_code(dtype), _gain(norm, gain)
+    h_step, dy_step = _matrix(h, "h", index, shape, dtype), _matrix(dy, "dy", index, shape, dtype)
+    dh_at = dh_step = dx_step = dgain_at = workspace_at = nbytes = 0
     if dh is not None:
-        n.dh_stride, n.dh_dev = _matrix(dh, "dh", index, t, width, dtype), dh.data_ptr()
+        dh_step, dh_at = _matrix(dh, "dh", index, shape, dtype), dh.data_ptr()
     if dx is None:
-        dx = _empty_on(stream, h, (t, width))
+        dx = _empty_on(stream, h, shape)
     else:
-        n.dx_stride = _matrix(dx, "dx", index, t, width, dtype)
-    n.dx_dev = dx.data_ptr()
+        dx_step = _matrix(dx, "dx", index, shape, dtype)
     if dgain is False or (dgain is None and gain is None):
         dgain = None
     else:
+        t, width = shape
         f32 = norm.types[2]
         if dgain is None:
             dgain = _empty_on(stream, h, (width,), f32)
-        elif not (dgain.is_contiguous() and dgain.numel() == width and dgain.dtype == f32 and dgain.get_device() == index):
+        elif not (dgain.is_contiguous() and dgain.numel() == width and dgain.dtype is f32 and dgain.get_device() == index):
             raise ValueError(f"dgain: contiguous float32 [{width}] on CUDA device {index} expected")
         if workspace is None:
             rc, nbytes = _native.cns_rms_norm_workspace_bytes(t, width)
             _native.check(rc, "cns_rms_norm_workspace_bytes")
             workspace = _empty_on(stream, h, (nbytes // 4,), f32)
-        elif not (workspace.is_contiguous() and workspace.get_device() == index):
+        elif workspace.is_contiguous() and workspace.get_device() == index:
+            nbytes = workspace.numel() * workspace.element_size()
+        else:
             raise ValueError(f"workspace: contiguous, on CUDA device {index} expected")
-        n.dgain_dev, n.workspace_dev = dgain.data_ptr(), workspace.data_ptr()
-        n.workspace_bytes = workspace.numel() * workspace.element_size()
-    n.rows, n.width, n.eps = t, width, norm.eps
-    if stream is not None:
-        n.stream = _native.stream_handle(stream)
-    rc = _native.cns_rms_norm_backward(n)
+        dgain_at, workspace_at = dgain.data_ptr(), workspace.data_ptr()
+    rc = _native.cns_rms_norm_backward(_native.make_rms_norm_grad(
+        h.data_ptr(), gain_at, dy.data_ptr(), dh_at, dx.data_ptr(), dgain_at, workspace_at, nbytes,
+        _native.stream_handle(stream) or 0, shape[0], h_step, dy_step, dh_step, dx_step, shape[1], code, gain_code, norm.eps))
     if rc:
         raise _native.CnsError(rc, "cns_rms_norm_backward")
     return dx, dgain

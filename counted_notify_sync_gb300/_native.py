@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from ctypes import (POINTER, Structure, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint8, c_uint32,
                     c_uint64, c_void_p)
@@ -92,6 +93,7 @@ CNS_ROUTE_MAX_TOP_K = 32
 CNS_ROUTE_MAX_GROUPS = 32
 CNS_GRAD_MAX_TENSORS = 1048576
 CNS_ROWS_MAX_BYTES = 16777216
+CNS_ROWS_MAX_STRIDE = 536870912
 CNS_SCALE_F32 = 0
 CNS_SCALE_E8M0 = 1
 CNS_NORM_MAX_WIDTH = 32768
@@ -198,6 +200,19 @@ class RmsNormGrad(Structure):
         ("rows", c_int64), ("h_stride", c_int64), ("dy_stride", c_int64), ("dh_stride", c_int64),
         ("dx_stride", c_int64), ("width", c_int32), ("dtype", c_int32), ("gain_dtype", c_int32), ("eps", c_float),
     ]
+
+
+def _packer(cls):
+    """A function that makes a structure of `cls` of values for all its fields, in their order (addresses as integers,
+    0 for none): a third of the time of setting them one by one."""
+    codes = {c_void_p: "Q", c_uint64: "Q", c_int64: "q", c_int32: "i", c_uint32: "I", c_float: "f"}
+    pack, make = struct.Struct("=" + "".join(codes[t] for _, t in cls._fields_)).pack, cls.from_buffer_copy
+    assert struct.calcsize("=" + "".join(codes[t] for _, t in cls._fields_)) == ctypes.sizeof(cls)   # no padding
+    return lambda *values: make(pack(*values))
+
+
+make_dispatch, make_combine, make_combine_grad = _packer(Dispatch), _packer(Combine), _packer(CombineGrad)
+make_rms_norm, make_rms_norm_grad = _packer(RmsNorm), _packer(RmsNormGrad)
 
 
 class Tensor(Structure):

@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "cns.h"
 #include "cns_host.h"
@@ -21,38 +22,63 @@
 namespace cns {
 namespace {
 
-// How a CTA's threads lie over tokens and a row's accesses: `per` whole tokens of `units` accesses each, or
-// (per = 1) one of `parts` stretches of `span` accesses of a token.
+// How a CTA's threads lie over tokens and a row's accesses.
+//   Accesses of 16 bytes, one a thread: a CTA has `per` groups of `lanes` threads, each for tokens of its own, or (per =
+// 1) one of `parts` stretches of a row.
+//   Narrower ones (rows at odd addresses), several a thread, 16 bytes in all, so that it has more than one element's
+// work: a warp (lanes = 32, per = 8) has one of `parts` stretches of a row, its lanes neighbouring accesses each time.
 struct Tiling {
-    uint32_t units, per, parts, span, threads, ctas;
+    uint32_t units, lanes, per, parts, threads, ctas;
 };
 
 constexpr uint32_t kRowThreads = 256;
 
-bool tile(int64_t tokens, int64_t units, Tiling *t)
+// Accesses of A bytes that a thread holds of a row.
+__host__ __device__ constexpr int accesses(int a) { return a == 1 ? 8 : 16 / a; }
+
+// `tokens`: of a thread.
+bool tile(int64_t count, int64_t units, int access, uint32_t tokens, Tiling *t)
 {
     t->units = static_cast<uint32_t>(units);
-    t->per = std::max<uint32_t>(1u, kRowThreads / t->units);
-    t->parts = (t->units + kRowThreads - 1) / kRowThreads;
-    t->span = (t->units + t->parts - 1) / t->parts;
-    t->threads = (t->per * t->span + 31) / 32 * 32;
-    const int64_t ctas = (tokens + t->per - 1) / t->per * t->parts;
+    int64_t ctas;
+    if (access == 16) {
+        t->parts = (t->units + kRowThreads - 1) / kRowThreads;
+        t->lanes = (t->units + t->parts - 1) / t->parts;
+        t->per = std::max<uint32_t>(1u, kRowThreads / t->lanes);
+        t->threads = (t->per * t->lanes + 31) / 32 * 32;
+        const int64_t each = static_cast<int64_t>(t->per) * tokens;
+        ctas = (count + each - 1) / each * t->parts;
+    } else {
+        t->lanes = 32;
+        t->per = kRowThreads / 32;
+        t->parts = (t->units + 32 * accesses(access) - 1) / (32 * accesses(access));
+        t->threads = kRowThreads;
+        ctas = ((count + tokens - 1) / tokens * t->parts + t->per - 1) / t->per;
+    }
     t->ctas = static_cast<uint32_t>(ctas);
-    return ctas <= 0x7fffffff;
+    return ctas <= 0x7fffffff / 8;   // warps are counted in 32 bits
 }
 
-// The calling thread's token and access; false if it has none.
-__device__ __forceinline__ bool my_place(const Tiling &m, uint32_t cta, int64_t tokens, int64_t *t, uint32_t *u)
+// The first token of the calling thread (the others follow) and its first access (the others are 32 apart each).
+template <int A, int TOKENS>
+__device__ __forceinline__ void my_place(const Tiling &m, uint32_t cta, int64_t *t, uint32_t *u)
 {
-    if (m.parts == 1) {
-        const uint32_t k = threadIdx.x / m.units;
-        *t = static_cast<int64_t>(cta) * m.per + k;
-        *u = threadIdx.x - k * m.units;
-        return k < m.per && *t < tokens;
+    if constexpr (A < 16) {
+        const uint32_t warp = cta * (kRowThreads / 32) + threadIdx.x / 32, block = warp / m.parts;
+        *t = static_cast<int64_t>(block) * TOKENS;
+        *u = (warp - block * m.parts) * (32 * accesses(A)) + threadIdx.x % 32;
+    } else {
+        uint32_t group = 0, block = cta, part = 0;
+        if (m.parts == 1) {
+            group = threadIdx.x / m.lanes;
+        } else {
+            block = cta / m.parts;
+            part = cta % m.parts;
+        }
+        const uint32_t lane = threadIdx.x - group * m.lanes;
+        *t = (static_cast<int64_t>(block) * m.per + group) * TOKENS;
+        *u = group < m.per && lane < m.lanes ? part * m.lanes + lane : m.units;
     }
-    *t = cta / m.parts;
-    *u = cta % m.parts * m.span + threadIdx.x;
-    return threadIdx.x < m.span && *u < m.units;
 }
 
 struct DispatchParams {
@@ -61,29 +87,41 @@ struct DispatchParams {
     const uint8_t *scales;
     uint8_t *row_scales;
     const int32_t *places;
-    int64_t tokens, x_stride, rows_stride, scales_stride, row_scales_stride;
-    uint32_t limit;   // rows
+    int64_t tokens, x_stride, scales_stride;
+    uint32_t rows_stride, row_scales_stride;   // below 2^32, so that a row's offset is one product
+    uint32_t limit;                            // rows
     int32_t top_k, scale_access;
     Tiling data, scale;
 };
 
 template <int A>
 __device__ __forceinline__ void move(const DispatchParams &p, const Tiling &m, uint32_t cta, const uint8_t *from,
-                                     int64_t from_stride, uint8_t *to, int64_t to_stride)
+                                     int64_t from_stride, uint8_t *to, uint32_t to_stride)
 {
     using B = typename Bits<A>::type;
+    constexpr int H = accesses(A);
     int64_t t;
     uint32_t u;
-    if (!my_place(m, cta, p.tokens, &t, &u))
+    my_place<A, 1>(m, cta, &t, &u);
+    if (u >= m.units || t >= p.tokens)
         return;
-    const B v = *reinterpret_cast<const B *>(from + t * from_stride + static_cast<int64_t>(u) * A);
+    const B *x = reinterpret_cast<const B *>(from + t * from_stride) + u;
+    B v[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+        if (h == 0 || u + 32 * h < m.units)
+            v[h] = x[32 * h];
     const int32_t *place = p.places + t * p.top_k;
-    to += static_cast<int64_t>(u) * A;
 #pragma unroll 4
     for (int j = 0; j < p.top_k; ++j) {
         const uint32_t row = static_cast<uint32_t>(place[j]);
-        if (row < p.limit)
-            *reinterpret_cast<B *>(to + row * to_stride) = v;
+        if (row < p.limit) {
+            B *y = reinterpret_cast<B *>(to + static_cast<uint64_t>(row) * to_stride) + u;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                if (h == 0 || u + 32 * h < m.units)
+                    y[32 * h] = v[h];
+        }
     }
 }
 
@@ -110,59 +148,116 @@ struct CombineParams {
     const float *weights;
     const void *base;
     void *y;
-    int64_t tokens, rows_stride, base_stride, y_stride;   // elements
+    int64_t tokens, base_stride, y_stride;   // elements
+    int64_t step;                            // a thread's tokens from one round to the next
+    uint32_t rows_stride;                    // elements, below 2^30
     uint32_t limit;
     int32_t top_k;
     Tiling data;
 };
 
-constexpr int kBatch = 4;   // rows in flight a thread
+// CTAs to an SM that combine's registers are shared out for.
+constexpr int kCombineCtas = 4;
 
-template <int D, int A>
-__global__ void __launch_bounds__(kRowThreads) combine_kernel(const __grid_constant__ CombineParams p)
+// A thread has TOKENS tokens at a time and of each the rows of BATCH places, all in flight together; while they are on
+// their way it loads the places of the next ones.  As many CTAs as the GPU holds, so that only a thread's first rows
+// wait for their places.
+template <int D, int A, int BATCH, int TOKENS>
+__global__ void __launch_bounds__(kRowThreads, kCombineCtas) combine_kernel(const __grid_constant__ CombineParams p)
 {
     using T = typename Elem<D>::type;
     using B = typename Bits<A>::type;
-    constexpr int V = A / static_cast<int>(sizeof(T));
-    grid_dependency_wait();
+    constexpr int V = A / static_cast<int>(sizeof(T)), H = accesses(A);
     int64_t t;
     uint32_t u;
-    if (!my_place(p.data, blockIdx.x, p.tokens, &t, &u))
+    my_place<A, TOKENS>(p.data, blockIdx.x, &t, &u);
+    grid_dependency_wait();
+    if (u >= p.data.units)
         return;
     const T *rows = static_cast<const T *>(p.rows) + static_cast<int64_t>(u) * V;
-    const int32_t *place = p.places + t * p.top_k;
-    const float *weight = p.weights + t * p.top_k;
-    float sum[V] = {};
-    for (int j = 0; j < p.top_k; j += kBatch) {
-        B raw[kBatch];
-        float w[kBatch];
+    uint32_t next[TOKENS][BATCH];
+    const auto places = [&](int64_t of, int j) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const uint32_t row = j + i < p.top_k ? static_cast<uint32_t>(place[j + i]) : 0xffffffffu;
-            raw[i] = B{};
-            w[i] = 0.f;
-            if (row < p.limit) {
-                raw[i] = *reinterpret_cast<const B *>(rows + row * p.rows_stride);
-                w[i] = p.weights ? weight[j + i] : 1.f;
+        for (int n = 0; n < TOKENS; ++n)
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                next[n][i] = 0xffffffffu;
+                if (of + n < p.tokens && j + i < p.top_k)
+                    next[n][i] = static_cast<uint32_t>(p.places[(of + n) * p.top_k + j + i]);
+            }
+    };
+    places(t, 0);
+    float sum[TOKENS][H][V] = {};
+    int j = 0;
+    while (t < p.tokens) {
+        bool there[TOKENS][BATCH];
+        B raw[TOKENS][BATCH][H];
+#pragma unroll
+        for (int n = 0; n < TOKENS; ++n)
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                there[n][i] = next[n][i] < p.limit;
+                const B *row = reinterpret_cast<const B *>(rows + static_cast<uint64_t>(next[n][i]) * p.rows_stride);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    raw[n][i][h] = B{};
+                    if (there[n][i] && (h == 0 || u + 32 * h < p.data.units))
+                        raw[n][i][h] = row[32 * h];
+                }
+            }
+        const int64_t now = t;
+        const int place = j;
+        j += BATCH;
+        if (j >= p.top_k) {
+            j = 0;
+            t += p.step;
+        }
+        places(t, j);
+#pragma unroll
+        for (int n = 0; n < TOKENS; ++n)
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                // what is not there: 0 * 0
+                const float weight = !there[n][i] ? 0.f : p.weights ? p.weights[(now + n) * p.top_k + place + i] : 1.f;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    float v[V];
+                    unpack<D, A>(raw[n][i][h], v);
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        sum[n][h][k] = fmaf(weight, v[k], sum[n][h][k]);
+                }
+            }
+        if (j != 0)
+            continue;
+#pragma unroll
+        for (int n = 0; n < TOKENS; ++n) {
+            if (now + n >= p.tokens)
+                break;
+            const B *base = reinterpret_cast<const B *>(static_cast<const T *>(p.base) + (now + n) * p.base_stride) + u;
+            B *y = reinterpret_cast<B *>(static_cast<T *>(p.y) + (now + n) * p.y_stride) + u;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                if (h > 0 && u + 32 * h >= p.data.units)
+                    break;
+                if (p.base) {
+                    float v[V];
+                    unpack<D, A>(base[32 * h], v);
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        sum[n][h][k] += v[k];
+                }
+                y[32 * h] = pack<D, A>(sum[n][h]);
             }
         }
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            float v[V];
-            unpack<D, A>(raw[i], v);
+        for (int n = 0; n < TOKENS; ++n)
 #pragma unroll
-            for (int k = 0; k < V; ++k)
-                sum[k] = fmaf(w[i], v[k], sum[k]);
-        }
-    }
-    if (p.base) {
-        float v[V];
-        unpack<D, A>(*reinterpret_cast<const B *>(static_cast<const T *>(p.base) + t * p.base_stride + static_cast<int64_t>(u) * V), v);
+            for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-            sum[k] += v[k];
+                for (int k = 0; k < V; ++k)
+                    sum[n][h][k] = 0.f;
     }
-    *reinterpret_cast<B *>(static_cast<T *>(p.y) + t * p.y_stride + static_cast<int64_t>(u) * V) = pack<D, A>(sum);
 }
 
 struct CombineGradParams {
@@ -172,15 +267,37 @@ struct CombineGradParams {
     const float *weights;
     void *drows;
     float *dweights;
-    int64_t tokens, rows_stride, dy_stride, drows_stride;   // elements
+    int64_t tokens, dy_stride;             // elements
+    uint32_t rows_stride, drows_stride;    // elements, below 2^30
     uint32_t limit, units;
     int32_t top_k;
 };
 
-constexpr int kGradUnits = 2;   // accesses of a row that a thread holds
+// The sums of N values each over LANES neighbouring lanes: lane l gets that of value l % N.  Half of the values change
+// hands at each of the first steps, so four values take 6 exchanges over a warp, not 20.
+template <int N, int LANES>
+__device__ __forceinline__ float lanes_sums(float *v)
+{
+#pragma unroll
+    for (int d = 1, n = N; n > 1; d *= 2, n /= 2) {
+        const bool odd = threadIdx.x & d;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            // the even lane keeps the values whose number has this bit 0
+            const float keep = odd ? v[2 * i + 1] : v[2 * i], give = odd ? v[2 * i] : v[2 * i + 1];
+            v[i] = keep + __shfl_xor_sync(kFullWarp, give, d);
+        }
+    }
+    float sum = v[0];
+#pragma unroll
+    for (int d = N; d < LANES; d *= 2)
+        sum += __shfl_xor_sync(kFullWarp, sum, d);
+    return sum;
+}
 
-// LANES threads take a token: of a warp (8 or 32), or the CTA (0).
-template <int D, int A, int LANES>
+// LANES threads take a token: of a warp (8, 16 or 32), or the CTA (0).  A thread has HELD accesses of dy at a time, 32
+// apart (LANES, where fewer); the rows of BATCH places are in flight together.
+template <int D, int A, int LANES, int HELD, int BATCH>
 __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __grid_constant__ CombineGradParams p)
 {
     using T = typename Elem<D>::type;
@@ -188,9 +305,8 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __g
     constexpr int V = A / static_cast<int>(sizeof(T));
     constexpr int kLanes = LANES ? LANES : 32;   // that sum by shuffles
     __shared__ float s_dot[kRowThreads / kLanes][CNS_ROUTE_MAX_TOP_K];
-    const uint32_t lanes = LANES ? LANES : blockDim.x;
-    const uint32_t g = LANES ? threadIdx.x % lanes : threadIdx.x, slot = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
-    const int64_t t = LANES ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes : blockIdx.x;
+    const uint32_t slot = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+    const int64_t t = LANES ? static_cast<int64_t>(blockIdx.x) * (kRowThreads / kLanes) + slot : blockIdx.x;
     const bool token = t < p.tokens;
     grid_dependency_wait();
     for (int j = l; j < p.top_k; j += kLanes)
@@ -198,66 +314,67 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __g
     __syncwarp();
     const int32_t *place = p.places + t * p.top_k;
     const float *weight = p.weights + t * p.top_k;
-    for (uint32_t u0 = 0; u0 < p.units; u0 += lanes * kGradUnits) {
-        float dy[kGradUnits][V];
-        bool mine[kGradUnits];
+    const uint32_t stretch = LANES ? kLanes * HELD : blockDim.x * HELD;
+    for (uint32_t u0 = 0; u0 < p.units; u0 += stretch) {   // as often in every thread
+        const uint32_t u = u0 + (LANES ? 0u : slot * (32 * HELD)) + l;
+        const B *from = reinterpret_cast<const B *>(static_cast<const T *>(p.dy) + t * p.dy_stride) + u;
+        float dy[HELD][V];
+        bool mine[HELD];
 #pragma unroll
-        for (int k = 0; k < kGradUnits; ++k) {
-            const uint32_t u = u0 + k * lanes + g;
-            mine[k] = token && u < p.units;
+        for (int k = 0; k < HELD; ++k) {
+            mine[k] = token && u + k * kLanes < p.units;
             B raw = B{};
             if (mine[k])
-                raw = *reinterpret_cast<const B *>(static_cast<const T *>(p.dy) + t * p.dy_stride + static_cast<int64_t>(u) * V);
+                raw = from[k * kLanes];
             unpack<D, A>(raw, dy[k]);
         }
-        for (int j = 0; j < p.top_k; j += 2) {
-            uint32_t row[2];
-            B raw[2][kGradUnits];
+        for (int j = 0; j < p.top_k; j += BATCH) {
+            uint32_t row[BATCH];
+            B raw[BATCH][HELD];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < BATCH; ++i) {
                 row[i] = token && j + i < p.top_k ? static_cast<uint32_t>(place[j + i]) : 0xffffffffu;
+                const B *at = reinterpret_cast<const B *>(static_cast<const T *>(p.rows) + static_cast<uint64_t>(row[i]) * p.rows_stride) + u;
 #pragma unroll
-                for (int k = 0; k < kGradUnits; ++k) {
+                for (int k = 0; k < HELD; ++k) {
                     raw[i][k] = B{};
                     if (p.dweights && mine[k] && row[i] < p.limit)
-                        raw[i][k] = *reinterpret_cast<const B *>(static_cast<const T *>(p.rows) + row[i] * p.rows_stride +
-                                                                 static_cast<int64_t>(u0 + k * lanes + g) * V);
+                        raw[i][k] = at[k * kLanes];
                 }
             }
+            float dot[BATCH];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < BATCH; ++i) {
                 const bool there = row[i] < p.limit;
                 if (p.drows && there) {
                     const float w = p.weights ? weight[j + i] : 1.f;
+                    B *to = reinterpret_cast<B *>(static_cast<T *>(p.drows) + static_cast<uint64_t>(row[i]) * p.drows_stride) + u;
 #pragma unroll
-                    for (int k = 0; k < kGradUnits; ++k) {
+                    for (int k = 0; k < HELD; ++k) {
                         float v[V];
 #pragma unroll
                         for (int e = 0; e < V; ++e)
                             v[e] = w * dy[k][e];
                         if (mine[k])
-                            *reinterpret_cast<B *>(static_cast<T *>(p.drows) + row[i] * p.drows_stride +
-                                                   static_cast<int64_t>(u0 + k * lanes + g) * V) = pack<D, A>(v);
+                            to[k * kLanes] = pack<D, A>(v);
                     }
                 }
-                if (p.dweights && j + i < p.top_k) {
-                    float dot = 0.f;
-                    if (there) {
+                dot[i] = 0.f;
+                if (there) {
 #pragma unroll
-                        for (int k = 0; k < kGradUnits; ++k) {
-                            float v[V];
-                            unpack<D, A>(raw[i][k], v);
+                    for (int k = 0; k < HELD; ++k) {
+                        float v[V];
+                        unpack<D, A>(raw[i][k], v);
 #pragma unroll
-                            for (int e = 0; e < V; ++e)
-                                dot = fmaf(dy[k][e], v[e], dot);
-                        }
+                        for (int e = 0; e < V; ++e)
+                            dot[i] = fmaf(dy[k][e], v[e], dot[i]);
                     }
-#pragma unroll
-                    for (int d = kLanes / 2; d > 0; d >>= 1)
-                        dot += __shfl_xor_sync(kFullWarp, dot, d);
-                    if (l == 0)
-                        s_dot[slot][j + i] += dot;
                 }
+            }
+            if (p.dweights) {
+                const float sum = lanes_sums<BATCH, kLanes>(dot);
+                if (l < BATCH && j + static_cast<int>(l) < p.top_k)
+                    s_dot[slot][j + l] += sum;
             }
         }
     }
@@ -269,7 +386,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __g
         __syncthreads();
     if (!token)
         return;
-    for (int j = g; j < p.top_k; j += lanes) {
+    for (int j = LANES ? l : threadIdx.x; j < p.top_k; j += LANES ? kLanes : blockDim.x) {
         float dot = s_dot[slot][j];
         if (!LANES) {
             dot = 0.f;
@@ -291,37 +408,62 @@ cudaError_t launch(void (*kernel)(P), const P &p, uint32_t ctas, uint32_t thread
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <int D, int A, int BATCH, int TOKENS>
+cudaError_t launch_combine_as(CombineParams &p, int sms, cudaStream_t s)
+{
+    if (!tile(p.tokens, p.data.units, A, TOKENS, &p.data))
+        return cudaErrorInvalidConfiguration;
+    uint32_t ctas = p.data.ctas;
+    const uint32_t most = static_cast<uint32_t>(sms) * kCombineCtas;
+    if constexpr (A == 16) {
+        // whole rows of parts, so that a thread keeps its part
+        ctas = std::min(ctas, std::max<uint32_t>(most / p.data.parts, 1u) * p.data.parts);
+        p.step = static_cast<int64_t>(ctas / p.data.parts) * p.data.per * TOKENS;
+    } else {
+        p.step = p.tokens;   // one round: a warp's part is by its number
+    }
+    return launch<CombineParams>(combine_kernel<D, A, BATCH, TOKENS>, p, ctas, p.data.threads, s);
+}
+
 template <int D>
-cudaError_t launch_combine(const CombineParams &p, int access, cudaStream_t s)
+cudaError_t launch_combine(CombineParams &p, int access, int sms, cudaStream_t s)
 {
     constexpr int E = sizeof(typename Elem<D>::type);
-    return launch(access == 16  ? combine_kernel<D, 16>
-                  : access == 8 ? combine_kernel<D, 8>
-                  : access == 4 ? combine_kernel<D, 4>
-                                : combine_kernel<D, E>,
-                  p, p.data.ctas, p.data.threads, s);
+    if (access == 16)
+        return p.top_k <= 2 ? launch_combine_as<D, 16, 2, 2>(p, sms, s) : launch_combine_as<D, 16, 4, 1>(p, sms, s);
+    return access == 8   ? launch_combine_as<D, 8, 4, 1>(p, sms, s)
+           : access == 4 ? launch_combine_as<D, 4, 4, 1>(p, sms, s)
+                         : launch_combine_as<D, E, 4, 1>(p, sms, s);
 }
 
-template <int D, int A>
-cudaError_t launch_grad(const CombineGradParams &p, cudaStream_t s)
+template <int D, int A, int LANES, int HELD, int BATCH>
+cudaError_t launch_grad_as(const CombineGradParams &p, cudaStream_t s)
 {
-    // a token's lanes: enough for the row's accesses, so that few idle and few sums meet in shared memory
-    if (p.units <= 8 * kGradUnits)
-        return launch(combine_backward_kernel<D, A, 8>, p, static_cast<uint32_t>((p.tokens + 31) / 32), kRowThreads, s);
-    if (p.units <= 32 * kGradUnits)
-        return launch(combine_backward_kernel<D, A, 32>, p, static_cast<uint32_t>((p.tokens + 7) / 8), kRowThreads, s);
-    const uint32_t threads = std::min(kRowThreads, (p.units + 32 * kGradUnits - 1) / (32 * kGradUnits) * 32);
-    return launch(combine_backward_kernel<D, A, 0>, p, static_cast<uint32_t>(p.tokens), threads, s);
+    const int64_t per = kRowThreads / (LANES ? LANES : kRowThreads);
+    const uint32_t threads = LANES ? kRowThreads : std::min<uint32_t>(kRowThreads, (p.units + 32 * HELD - 1) / (32 * HELD) * 32);
+    return launch<CombineGradParams>(combine_backward_kernel<D, A, LANES, HELD, BATCH>, p,
+                                     static_cast<uint32_t>((p.tokens + per - 1) / per), threads, s);
 }
 
+// A token's lanes: enough for the row's accesses, so that few idle and few sums meet in shared memory.
 template <int D>
 cudaError_t launch_combine_backward(const CombineGradParams &p, int access, cudaStream_t s)
 {
     constexpr int E = sizeof(typename Elem<D>::type);
-    return access == 16  ? launch_grad<D, 16>(p, s)
-           : access == 8 ? launch_grad<D, 8>(p, s)
-           : access == 4 ? launch_grad<D, 4>(p, s)
-                         : launch_grad<D, E>(p, s);
+    if (access == 16)
+        return p.units <= 8    ? launch_grad_as<D, 16, 8, 1, 4>(p, s)
+               : p.units <= 16 ? launch_grad_as<D, 16, 16, 1, 4>(p, s)
+               : p.units <= 32 ? launch_grad_as<D, 16, 32, 1, 4>(p, s)
+               : p.units <= 64 ? launch_grad_as<D, 16, 32, 2, 4>(p, s)
+                               : launch_grad_as<D, 16, 0, 2, 2>(p, s);
+    const auto narrow = [&](auto bytes) {
+        constexpr int A = bytes();
+        return p.units <= 32 * accesses(A) ? launch_grad_as<D, A, 32, accesses(A), 2>(p, s)
+                                           : launch_grad_as<D, A, 0, accesses(A), 2>(p, s);
+    };
+    return access == 8   ? narrow(std::integral_constant<int, 8>())
+           : access == 4 ? narrow(std::integral_constant<int, 4>())
+                         : narrow(std::integral_constant<int, E>());
 }
 
 bool sizes_ok(int64_t tokens, int64_t rows, int32_t top_k, int32_t reserved)
@@ -330,11 +472,14 @@ bool sizes_ok(int64_t tokens, int64_t rows, int32_t top_k, int32_t reserved)
            reserved == 0;
 }
 
-// A matrix's stride in elements (`packed` where it is 0); false if it is too small or not to be counted in bytes.
-bool stride_ok(int64_t given, int64_t packed, int64_t *stride)
+// A matrix's stride (`packed` where it is 0); false if it is too small, or too large for kernels that multiply it in
+// 32 bits.
+template <class S>
+bool stride_ok(int64_t given, int64_t packed, S *stride)
 {
-    *stride = given ? given : packed;
-    return *stride >= packed && *stride <= (INT64_MAX >> 34);
+    const int64_t s = given ? given : packed;
+    *stride = static_cast<S>(s);
+    return s >= packed && s <= CNS_ROWS_MAX_STRIDE;
 }
 
 bool off(const void *p, int64_t bytes) { return address(p) % bytes != 0; }
@@ -375,12 +520,12 @@ extern "C" int cns_dispatch(const cns_dispatch_t *d)
     p.limit = row_limit(d->rows);
     p.top_k = d->top_k;
     const int access = access_bytes(address(p.x) | address(p.rows) | d->row_bytes | p.x_stride | p.rows_stride);
-    if (!tile(p.tokens, d->row_bytes / access, &p.data))
+    if (!tile(p.tokens, d->row_bytes / access, access, 1, &p.data))
         return CNS_ERR_INVALID_VALUE;
     if (scales) {
         const int a = access_bytes(address(p.scales) | address(p.row_scales) | d->scale_bytes | p.scales_stride | p.row_scales_stride);
         p.scale_access = a == 16 ? 16 : a >= 4 ? 4 : 1;
-        if (!tile(p.tokens, d->scale_bytes / p.scale_access, &p.scale))
+        if (!tile(p.tokens, d->scale_bytes / p.scale_access, p.scale_access, 1, &p.scale))
             return CNS_ERR_INVALID_VALUE;
     }
     const int64_t ctas = static_cast<int64_t>(p.data.ctas) + p.scale.ctas;
@@ -429,17 +574,16 @@ extern "C" int cns_combine(const cns_combine_t *c)
     if (p.base)
         bits |= address(p.base) | (p.base_stride * e);
     const int access = access_bytes(bits);
-    if (!tile(p.tokens, c->width * e / access, &p.data))
-        return CNS_ERR_INVALID_VALUE;
+    p.data.units = static_cast<uint32_t>(c->width * e / access);
     DeviceInfo dev;
     if (int rc = current_device(&dev))
         return rc;
     if (p.tokens == 0)
         return CNS_SUCCESS;
     cudaStream_t s = to_stream(c->stream);
-    CNS_CUDA(c->dtype == CNS_DT_F32    ? launch_combine<CNS_DT_F32>(p, access, s)
-             : c->dtype == CNS_DT_BF16 ? launch_combine<CNS_DT_BF16>(p, access, s)
-                                       : launch_combine<CNS_DT_F16>(p, access, s));
+    CNS_CUDA(c->dtype == CNS_DT_F32    ? launch_combine<CNS_DT_F32>(p, access, dev.sm_count, s)
+             : c->dtype == CNS_DT_BF16 ? launch_combine<CNS_DT_BF16>(p, access, dev.sm_count, s)
+                                       : launch_combine<CNS_DT_F16>(p, access, dev.sm_count, s));
     return CNS_SUCCESS;
 }
 

@@ -12,24 +12,38 @@
 namespace cns {
 namespace {
 
-constexpr int kJoinColumns = 32, kJoinRows = 32;
+constexpr int kJoinColumns = 8, kJoinRows = 64, kJoinHeld = 5;   // 8 columns: a sector of each part
 
-// dgain = the sum of the parts: 32 columns a CTA, the parts over its warps.
+// dgain = the sum of the parts.  A CTA has 8 columns, its 32 groups of 8 threads every 32nd part; so that there are
+// CTAs enough for few columns (W us for 777 x 1000 f32 with 32 columns a CTA, V so).
 __global__ void __launch_bounds__(kJoinColumns * kJoinRows) join_parts_kernel(const float *parts, int count, int width, float *dgain)
 {
-    __shared__ float s_sum[kJoinRows][kJoinColumns + 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * kJoinColumns + lane;
+    __shared__ float s_sum[kJoinRows * kJoinColumns / 32][kJoinColumns];
+    const int column = threadIdx.x % kJoinColumns, e = blockIdx.x * kJoinColumns + column;
     grid_dependency_wait();
-    float v = 0.f;
-    if (e < width)
-        for (int i = warp; i < count; i += kJoinRows)
-            v += parts[static_cast<int64_t>(i) * width + e];
-    s_sum[warp][lane] = v;
+    float sum = 0.f;
+    for (int i = threadIdx.x / kJoinColumns; i < count; i += kJoinRows * kJoinHeld) {
+        float v[kJoinHeld];
+#pragma unroll
+        for (int k = 0; k < kJoinHeld; ++k)
+            v[k] = i + k * kJoinRows < count && e < width ? parts[static_cast<int64_t>(i + k * kJoinRows) * width + e] : 0.f;
+#pragma unroll
+        for (int k = 0; k < kJoinHeld; ++k)
+            sum += v[k];
+    }
+#pragma unroll
+    for (int d = kJoinColumns; d < 32; d *= 2)
+        sum += __shfl_xor_sync(kFullWarp, sum, d);
+    if (threadIdx.x % 32 < kJoinColumns)
+        s_sum[threadIdx.x / 32][column] = sum;
     __syncthreads();
-    v = warp_sum(s_sum[lane][warp]);   // the warp's column
-    const int column = blockIdx.x * kJoinColumns + warp;
-    if (lane == 0 && column < width)
-        dgain[column] = v;
+    if (threadIdx.x < kJoinColumns && e < width) {
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kJoinRows * kJoinColumns / 32; ++i)
+            sum += s_sum[i][column];
+        dgain[e] = sum;
+    }
 }
 
 bool type_ok(int32_t dtype) { return dtype >= CNS_DT_F32 && dtype <= CNS_DT_F16; }

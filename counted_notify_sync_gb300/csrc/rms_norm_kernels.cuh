@@ -2,18 +2,23 @@
 // (cns_rms_norm, cns_rms_norm_backward); rms_norm_{f32,bf16,f16}.cu instantiate
 // them, a type each.
 //
-//   h = round(x + residual),  r = 1 / sqrt(mean h^2 + eps),  y = h r gain,
+//   h = round(x + residual),  r = 1 / sqrt(mean h^2 + eps),  y = h gain r,
 //   per block of columns: s from the largest |y|, q = e4m3(y / s)
 //   dx = dh + r g - h r^3 mean(g h) with g = gain dy;  dgain = sum over rows dy h r
 //
-// G threads take a row and hold it: one pass over the operands.  A thread has HOLD vectors of 16 bytes, G vectors
-// apart; a block of 32 columns or more is then the vectors of neighbouring lanes of one warp.  WIDE rows are read
-// and written by vectors, others by elements, at the same places.
+// A group of threads takes a row, one pass over the operands: a thread has HOLD vectors of 16 bytes, as far apart as the
+// group is large, so that a block of 32 columns or more is the vectors of neighbouring lanes of one warp.  As many CTAs as the GPU holds go
+// through the rows in steps, so a CTA's sums of dgain stay on the SM, and the next rows are on their way while one is
+// worked on: WIDE rows, whose vectors are aligned, are copied to shared memory ahead (every thread copies what it will
+// read itself, so no thread waits for another's copies), others pass through shared memory element by element, in
+// neighbouring lanes' order on the global side and by vectors on the registers'.
 #pragma once
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "rows_device.cuh"
 
@@ -44,57 +49,207 @@ struct NormGradParams {
     float eps;
 };
 
-// Most CTAs of a gradient, each of which leaves a part of dgain: four to an SM.
-constexpr int kNormMaxParts = 4 * kStepMaxCtas;
+// Most CTAs of a gradient, each of which leaves a part of dgain: 512 threads to an SM in CTAs of more than 128.
+constexpr int kNormMaxParts = 3 * kStepMaxCtas;
+// Rows that a group of a gradient has at least.
+constexpr int kNormLeastRows = 4;
+// Dynamic shared memory that every kernel here may be launched with.
+constexpr int kNormMaxSmem = 200 * 1024;
 
 template <int D> __host__ __device__ constexpr int norm_vec() { return 16 / static_cast<int>(sizeof(typename Elem<D>::type)); }
 
-// The vector of columns e .. of a row; what lies past the row is 0.
-template <int D, bool WIDE>
-__device__ __forceinline__ uint4 load_vec(const void *row, int e, int width)
+// A thread's vectors of a row at any address.  The lanes of a warp that share a row read or write neighbouring elements and
+// exchange them through `scratch`, 16 bytes a thread.
+template <int D, int G, int HOLD>
+__device__ __forceinline__ void load_narrow(const void *row, int width, uint4 *scratch, uint4 *to)
 {
     using T = typename Elem<D>::type;
-    const T *a = static_cast<const T *>(row) + e;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (WIDE) {
-        if (e < width)
-            raw = *reinterpret_cast<const uint4 *>(a);
-    } else {
-        T *to = reinterpret_cast<T *>(&raw);
+    constexpr int V = norm_vec<D>(), L = G < 32 ? G : 32;
+    const int g = threadIdx.x % G, l = g % L;
+    const T *from = static_cast<const T *>(row);
+    T *s = reinterpret_cast<T *>(scratch + (threadIdx.x - l));
+    T v[HOLD][V];
 #pragma unroll
-        for (int i = 0; i < norm_vec<D>(); ++i)
-            if (e + i < width)
-                to[i] = a[i];
+    for (int j = 0; j < HOLD; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = (j * G + g - l) * V + i * L + l;
+            v[j][i] = e < width ? from[e] : T(0.f);
+        }
+#pragma unroll
+    for (int j = 0; j < HOLD; ++j) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            s[i * L + l] = v[j][i];
+        __syncwarp();
+        to[j] = scratch[threadIdx.x];
     }
-    return raw;
 }
 
-template <int D, bool WIDE>
-__device__ __forceinline__ void store_vec(void *row, int e, int width, const uint4 &raw)
+// One vector of N-byte elements from every thread: its column is e, the threads of a row's warp hold neighbouring ones.
+template <class T, int V, int L, class Raw>
+__device__ __forceinline__ void store_narrow(T *row, int e, int width, uint4 *scratch, const Raw &raw)
 {
-    using T = typename Elem<D>::type;
-    T *a = static_cast<T *>(row) + e;
-    if constexpr (WIDE) {
-        if (e < width)
-            *reinterpret_cast<uint4 *>(a) = raw;
-    } else {
-        const T *from = reinterpret_cast<const T *>(&raw);
+    static_assert(sizeof(Raw) == V * sizeof(T), "one vector");
+    const int lane = threadIdx.x & 31, l = lane % L;
+    Raw *mine = reinterpret_cast<Raw *>(scratch + (threadIdx.x - lane)) + lane;   // within the warp's 512 bytes
+    const T *s = reinterpret_cast<const T *>(mine - l);
+    __syncwarp();
+    *mine = raw;
+    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < norm_vec<D>(); ++i)
-            if (e + i < width)
-                a[i] = from[i];
+    for (int i = 0; i < V; ++i) {
+        const int at = e - l * V + i * L + l;
+        if (at < width)
+            row[at] = s[i * L + l];
     }
 }
+
+template <int D, bool WIDE, int L>
+__device__ __forceinline__ void store_vec(void *row, int e, int width, uint4 *scratch, const uint4 &raw)
+{
+    using T = typename Elem<D>::type;
+    if constexpr (WIDE) {
+        if (e < width)
+            *reinterpret_cast<uint4 *>(static_cast<T *>(row) + e) = raw;
+    } else {
+        store_narrow<T, norm_vec<D>(), L>(static_cast<T *>(row), e, width, scratch, raw);
+    }
+}
+
+// A copy of 16 bytes to shared memory that the thread does not wait for; zeros where there is nothing to copy.
+__device__ __forceinline__ void copy_ahead(uint4 *to, const void *from, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                 "l"(from), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LATER>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory"); }
+
+// A vector as pairs, for the instructions that work on two numbers at once.
+template <int D>
+__device__ __forceinline__ void unpack_pairs(const uint4 &raw, float2 *v)
+{
+    float f[norm_vec<D>()];
+    unpack<D, 16>(raw, f);
+#pragma unroll
+    for (int i = 0; i < norm_vec<D>() / 2; ++i)
+        v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+
+template <int D>
+__device__ __forceinline__ uint4 pack_pairs(const float2 *v)
+{
+    float f[norm_vec<D>()];
+#pragma unroll
+    for (int i = 0; i < norm_vec<D>() / 2; ++i) {
+        f[2 * i] = v[i].x;
+        f[2 * i + 1] = v[i].y;
+    }
+    return pack<D, 16>(f);
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Rows of G threads: a CTA has GROUPS groups of them, each for a row at a time.
+template <int G, int GROUPS>
+struct Group {
+    static constexpr int kThreads = G * GROUPS, kLanes = G < 32 ? G : 32;   // kLanes: of a warp
+    static __device__ __forceinline__ int rank() { return threadIdx.x % G; }
+    static __device__ __forceinline__ int number() { return threadIdx.x / G; }
+    static __device__ __forceinline__ void sync()
+    {
+        if constexpr (GROUPS == 1) {
+            __syncthreads();
+        } else {
+            static_assert(GROUPS <= 4, "a barrier each");
+            const int n = number();   // barriers by number: the CTA then has five, not all sixteen
+            if (n == 0)
+                asm volatile("bar.sync 1, %0;" ::"n"(G) : "memory");
+            else if (n == 1)
+                asm volatile("bar.sync 2, %0;" ::"n"(G) : "memory");
+            else if (n == 2)
+                asm volatile("bar.sync 3, %0;" ::"n"(G) : "memory");
+            else
+                asm volatile("bar.sync 4, %0;" ::"n"(G) : "memory");
+        }
+    }
+};
+
+// One operand's rows as a thread goes through them: its first vector of the row at hand (the row's first column where
+// rows are narrow).  With DEPTH > 0 its vectors come through shared memory, the DEPTH rows from that one on being on
+// their way or there.
+template <int D, bool WIDE, int G, int HOLD, int DEPTH, int THREADS>
+struct Operand {
+    using T = typename Elem<D>::type;
+    static constexpr int V = norm_vec<D>();
+    const T *at;      // the next row to copy, or to load
+    int64_t apart;    // elements to the thread's next row
+    uint4 *ring;      // [DEPTH][HOLD][THREADS], the thread's own
+
+    __device__ __forceinline__ void start(const void *base, int64_t row, int64_t stride, int64_t step, uint4 *s)
+    {
+        at = static_cast<const T *>(base) + row * stride + (WIDE ? static_cast<int>(threadIdx.x) % G * V : 0);
+        apart = step * stride;
+        ring = s + threadIdx.x;
+    }
+    // into stage `stage`; `width`: 0 for a row past the last, whose vectors are zeros
+    __device__ __forceinline__ void copy(int stage, int width)
+    {
+        const int left = width - static_cast<int>(threadIdx.x) % G * V;
+#pragma unroll
+        for (int j = 0; j < HOLD; ++j)
+            copy_ahead(ring + (stage * HOLD + j) * THREADS, at + j * G * V, j * G * V < left);
+        at += apart;
+    }
+    // `scratch`: as load_narrow
+    __device__ __forceinline__ void get(int stage, int width, uint4 *scratch, uint4 *to)
+    {
+        if constexpr (DEPTH > 0) {
+#pragma unroll
+            for (int j = 0; j < HOLD; ++j)
+                to[j] = ring[(stage * HOLD + j) * THREADS];
+        } else if constexpr (WIDE) {
+            const int left = width - static_cast<int>(threadIdx.x) % G * V;
+#pragma unroll
+            for (int j = 0; j < HOLD; ++j) {
+                to[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (j * G * V < left)
+                    to[j] = *reinterpret_cast<const uint4 *>(at + j * G * V);
+            }
+            at += apart;
+        } else {
+            load_narrow<D, G, HOLD>(at, width, scratch, to);
+            at += apart;
+        }
+    }
+};
+
+// One result's rows: the row's first column.
+template <class T>
+struct Result {
+    T *at;
+    int64_t apart;
+    __device__ __forceinline__ void start(void *base, int64_t row, int64_t stride, int64_t step)
+    {
+        at = static_cast<T *>(base) + row * stride;
+        apart = step * stride;
+    }
+    __device__ __forceinline__ void next() { at += apart; }
+};
 
 // N columns of the gain from column e on, in 32 bits.
 template <int N, bool WIDE>
-__device__ __forceinline__ void load_gain(const void *gain, int dtype, int e, int width, float *v)
+__device__ __forceinline__ void load_gain(const void *gain, int dtype, int e, int width, float2 *pairs)
 {
+    float v[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
         v[i] = gain ? 0.f : 1.f;
-    if (!gain || e >= width)
-        return;
+    if (gain && e < width) {
     if constexpr (WIDE) {
         if (dtype == CNS_DT_F32) {
 #pragma unroll
@@ -115,30 +270,81 @@ __device__ __forceinline__ void load_gain(const void *gain, int dtype, int e, in
                        : dtype == CNS_DT_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(gain)[e + i])
                                               : __half2float(static_cast<const __half *>(gain)[e + i]);
     }
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+        pairs[i] = make_float2(v[2 * i], v[2 * i + 1]);
 }
 
-// The sum of `a` and the largest `b` (as whole numbers: magnitudes, NaN above all) over the G threads of a row.  The
-// halves of `s` alternate from call to call, so one barrier each is enough.
-template <int G>
-__device__ __forceinline__ void join_row(float &a, uint32_t &b, uint2 (*s)[32], int turn)
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Values of a row's warps to be joined: of each group from a multiple of four on, zeros between them.
+template <int G, int GROUPS>
+struct Joined {
+    static constexpr int kWarps = G / 32, kRoom = kWarps > 4 ? (kWarps + 3) / 4 * 4 : 4, kSize = G > 32 ? kRoom * GROUPS : 4;
+    float4 s[2][kSize / 4];   // the halves alternate from row to row, so one barrier each is enough
+    // the places that no warp fills: before the first row's barrier
+    __device__ __forceinline__ void start()
+    {
+        if (threadIdx.x < 2 * kSize && threadIdx.x % kRoom >= kWarps)
+            reinterpret_cast<float *>(s)[threadIdx.x] = 0.f;
+    }
+    __device__ __forceinline__ void put(int turn, float v)
+    {
+        if (threadIdx.x % 32 == 0)
+            reinterpret_cast<float *>(s[turn & 1])[Group<G, GROUPS>::number() * kRoom + threadIdx.x % G / 32] = v;
+    }
+    template <class F>
+    __device__ __forceinline__ float get(int turn, F join) const
+    {
+        const float4 *of = s[turn & 1] + Group<G, GROUPS>::number() * (kRoom / 4);
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRoom / 4; ++i) {
+            const float4 w = of[i];
+            const float part = join(join(w.x, w.y), join(w.z, w.w));
+            v = i ? join(v, part) : part;
+        }
+        return v;
+    }
+};
+
+template <int G, class F>
+__device__ __forceinline__ float join_lanes(float v, F join)
 {
 #pragma unroll
-    for (int d = (G < 32 ? G : 32) / 2; d > 0; d >>= 1) {
-        a += __shfl_xor_sync(kFullWarp, a, d);
-        b = max(b, __shfl_xor_sync(kFullWarp, b, d));
-    }
+    for (int d = (G < 32 ? G : 32) / 2; d > 0; d >>= 1)
+        v = join(v, __shfl_xor_sync(kFullWarp, v, d));
+    return v;
+}
+
+struct Add {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct Largest {
+    __device__ __forceinline__ float operator()(float a, float b) const { return max_nan(a, b); }
+};
+
+// `a` summed, and `b`, if `second`, joined over a row's threads.
+template <int G, int GROUPS, class F>
+__device__ __forceinline__ void join_row(float &a, float &b, F join, bool second, Joined<G, GROUPS> &sa, Joined<G, GROUPS> &sb, int turn)
+{
+    a = join_lanes<G>(a, Add());
+    if (second)
+        b = join_lanes<G>(b, join);
     if constexpr (G > 32) {
-        if (threadIdx.x % 32 == 0)
-            s[turn & 1][threadIdx.x / 32] = make_uint2(__float_as_uint(a), b);
-        __syncthreads();
-        a = 0.f;
-        b = 0u;
-#pragma unroll
-        for (int i = 0; i < G / 32; ++i) {
-            const uint2 v = s[turn & 1][i];
-            a += __uint_as_float(v.x);
-            b = max(b, v.y);
-        }
+        sa.put(turn, a);
+        if (second)
+            sb.put(turn, b);
+        Group<G, GROUPS>::sync();
+        a = sa.get(turn, Add());
+        if (second)
+            b = sb.get(turn, join);
     }
 }
 
@@ -150,266 +356,362 @@ __device__ __forceinline__ uint32_t e4m3_pair(float low, float high)
     return r;
 }
 
-// Threads of a CTA whose rows take G threads each.
-__host__ __device__ constexpr int norm_threads(int g) { return g < 128 ? 128 : g; }
+// 1 / sqrt(m) to within a unit in the last place: an approximation and a step of Newton's.
+__device__ __forceinline__ float root_reciprocal(float m)
+{
+    const float r = rsqrtf(m);
+    return m < INFINITY ? fmaf(0.5f * r, fmaf(-m * r, r, 1.f), r) : r;
+}
+
+// m / 448 for a magnitude whose quotient is a normal number, rounded to the nearest: the product with the reciprocal,
+// corrected by its remainder.
+__device__ __forceinline__ float over_448(float m)
+{
+    const float c = 1.f / 448.f, q = m * c;
+    return fmaf(fmaf(-448.f, q, m), c, q);
+}
+
+// Groups of a CTA: enough for 128 threads where a warp or less takes a row, for 256 in the gradient, whose CTAs each
+// leave a part to join.
+__host__ __device__ constexpr int norm_groups(int g, bool grad)
+{
+    return grad ? (g < 256 ? 256 / g : 1) : g <= 32 ? 128 / g : 1;
+}
+
+// CTAs to an SM that its registers and shared memory are shared out for: 768 threads with two vectors each, 512 of the
+// gradient or with more vectors.
+__host__ __device__ constexpr int norm_ctas_per_sm(int g, int hold, bool grad)
+{
+    const int threads = g * norm_groups(g, grad), all = grad || hold > 2 ? 512 : 768;
+    return threads > all ? 1 : all / threads;
+}
+
+// Whether the gradient's sums of dgain stay in registers; else they are in shared memory.
+__host__ __device__ constexpr bool norm_sums_in_registers(int g, int hold) { return g * hold <= 2048 && hold <= 4; }
+
+// Rows on their way ahead of the one at hand: one, two of the gradient; none where the shared memory lacks the room.
+// More of them cost time, presumably because the DRAM's pages are left and opened again in between: 16384 x 4096 bf16
+// takes the norm 84.5 us with one, 85.8 with two and 88.5 with four; its gradient 89.5, 82.6 and 88.5.
+__host__ __device__ constexpr int norm_depth(bool wide, int g, int hold, bool grad)
+{
+    const int depth = grad ? 2 : 1, threads = g * norm_groups(g, grad) * norm_ctas_per_sm(g, hold, grad);
+    return !wide || (grad && !norm_sums_in_registers(g, hold)) || 16 * threads * hold * depth * (grad ? 3 : 2) > 192 * 1024 ? 0 : depth;
+}
 
 template <int D, bool WIDE, int G, int HOLD>
-__global__ void __launch_bounds__(norm_threads(G)) rms_norm_kernel(const __grid_constant__ NormParams p)
+__global__ void __launch_bounds__(G * norm_groups(G, false), norm_ctas_per_sm(G, HOLD, false))
+rms_norm_kernel(const __grid_constant__ NormParams p)
 {
     using T = typename Elem<D>::type;
-    constexpr int V = norm_vec<D>();
-    constexpr int kGroups = norm_threads(G) / G;
-    __shared__ uint2 s_join[2][32];
-    const int g = threadIdx.x % G, group = threadIdx.x / G;
-    grid_dependency_wait();
-    // the gain: in registers, or, where a CTA of 512 threads or more has none left, loaded for each row
-    constexpr bool kHeld = G < 512;
-    float held_gain[kHeld ? HOLD : 1][V];
-    if constexpr (kHeld) {
-#pragma unroll
-        for (int j = 0; j < HOLD; ++j)
-            load_gain<V, WIDE>(p.gain, p.gain_dtype, (j * G + g) * V, p.width, held_gain[j]);
-    }
-    const auto gain_of = [&](int j, float *v) {
-        if constexpr (kHeld) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                v[i] = held_gain[j][i];
-        } else {
-            load_gain<V, WIDE>(p.gain, p.gain_dtype, (j * G + g) * V, p.width, v);
-        }
+    constexpr int V = norm_vec<D>(), kGroups = norm_groups(G, false), kDepth = norm_depth(WIDE, G, HOLD, false);
+    using Row = Group<G, kGroups>;
+    constexpr int kThreads = Row::kThreads, kLanes = Row::kLanes;
+    constexpr bool kGain = HOLD <= 2;   // the gain stays in registers
+    extern __shared__ uint4 s_rows[];   // the operands' rings; narrow rows: 16 bytes a thread
+    __shared__ Joined<G, kGroups> s_first, s_second;
+    s_first.start();
+    s_second.start();
+    const int g = Row::rank();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + Row::number();
+    Operand<D, WIDE, G, HOLD, kDepth, kThreads> x, residual;
+    x.start(p.x, row, p.x_stride, step, s_rows);
+    residual.start(p.residual, row, p.residual_stride, step, s_rows + kDepth * HOLD * kThreads);
+    const auto copy = [&](int stage, int64_t of) {
+        const int width = of < p.rows ? p.width : 0;   // past the last row, a row without columns
+        x.copy(stage, width);
+        if (p.residual)
+            residual.copy(stage, width);
+        copies_end();
     };
-    int turn = 0;
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups; first < p.rows;
-         first += static_cast<int64_t>(gridDim.x) * kGroups, ++turn) {
-        const int64_t row = first + group;
-        const int width = row < p.rows ? p.width : 0;   // past the last row, a row without columns
-        uint4 held[HOLD];
-        const T *x = static_cast<const T *>(p.x) + row * p.x_stride;
+    grid_dependency_wait();
+    if constexpr (kDepth > 0) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d)
+            copy(d, row + d * step);
+    }
+    Result<T> h, y;
+    Result<uint8_t> q;
+    h.start(p.h, row, p.h_stride, step);
+    y.start(p.y, row, p.y_stride, step);
+    q.start(p.q, row, p.q_stride, step);
+    float2 gain[HOLD][V / 2];
+    if constexpr (kGain) {
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
-            held[j] = load_vec<D, WIDE>(x, (j * G + g) * V, width);
+            load_gain<V, WIDE>(p.gain, p.gain_dtype, (j * G + g) * V, p.width, gain[j]);
+    }
+    const float share = 1.f / static_cast<float>(p.width);
+    const bool whole = p.q && p.block == 0;
+    // The lanes of a block, which of them writes its scale, and that scale's number.  (The vectors of a thread are a
+    // multiple of 128 columns apart where there are blocks, so this holds for each of them.)
+    const int lanes = p.block / V, shift = p.block ? 31 - __clz(p.block) : 0;
+    const bool writes = p.block ? (g * V & (p.block - 1)) == 0 : g == 0;
+    int64_t scale_at = row * p.scales_stride + (g * V >> shift);
+    int stage = 0, turn = 0;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups; first < p.rows; first += step, row += step, ++turn) {
+        const int width = row < p.rows ? p.width : 0;
+        if constexpr (kDepth > 0)
+            copies_wait<(kDepth > 0 ? kDepth - 1 : 0)>();
+        uint4 held[HOLD];
+        x.get(stage, width, s_rows, held);
         if (p.residual) {
-            const T *residual = static_cast<const T *>(p.residual) + row * p.residual_stride;
             uint4 more[HOLD];
-#pragma unroll
-            for (int j = 0; j < HOLD; ++j)
-                more[j] = load_vec<D, WIDE>(residual, (j * G + g) * V, width);
-            T *h = static_cast<T *>(p.h) + row * p.h_stride;
+            residual.get(stage, width, s_rows, more);
 #pragma unroll
             for (int j = 0; j < HOLD; ++j) {
-                float a[V], b[V];
-                unpack<D, 16>(held[j], a);
-                unpack<D, 16>(more[j], b);
+                float2 a[V / 2], b[V / 2];
+                unpack_pairs<D>(held[j], a);
+                unpack_pairs<D>(more[j], b);
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    a[i] += b[i];
-                held[j] = pack<D, 16>(a);
-                store_vec<D, WIDE>(h, (j * G + g) * V, width, held[j]);
+                for (int i = 0; i < V / 2; ++i)
+                    a[i] = __fadd2_rn(a[i], b[i]);
+                held[j] = pack_pairs<D>(a);
+                store_vec<D, WIDE, kLanes>(h.at, (j * G + g) * V, width, s_rows, held[j]);
             }
+            h.next();
         }
-        const bool whole = p.q && p.block == 0;
-        float sum = 0.f;
-        uint32_t top = 0u;
+        if constexpr (kDepth > 0) {
+            copy(stage, row + kDepth * step);   // into the stage just read
+            stage = stage + 1 == kDepth ? 0 : stage + 1;
+        }
+        float2 v[HOLD][V / 2], sums = both(0.f);
+        float top = 0.f;
 #pragma unroll
         for (int j = 0; j < HOLD; ++j) {
-            float v[V];
-            unpack<D, 16>(held[j], v);
+            unpack_pairs<D>(held[j], v[j]);
+            if constexpr (!kGain)
+                load_gain<V, WIDE>(p.gain, p.gain_dtype, (j * G + g) * V, p.width, gain[j]);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                sum = fmaf(v[i], v[i], sum);
+            for (int i = 0; i < V / 2; ++i) {
+                sums = __ffma2_rn(v[j][i], v[j][i], sums);
+                v[j][i] = __fmul2_rn(v[j][i], gain[j][i]);   // of 16-bit numbers exact
+            }
             if (whole) {
-                float gain[V];
-                gain_of(j, gain);
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    top = max(top, __float_as_uint(fabsf(v[i] * gain[i])));
+                for (int i = 0; i < V / 2; ++i)
+                    top = max_nan(top, max_nan(fabsf(v[j][i].x), fabsf(v[j][i].y)));
             }
         }
-        join_row<G>(sum, top, s_join, turn);
-        const float r = 1.f / sqrtf(sum / static_cast<float>(p.width) + p.eps);
-        if (whole)
-            top = __float_as_uint(fabsf(__uint_as_float(top) * r));
-        T *y = static_cast<T *>(p.y) + row * p.y_stride;
+        float sum = sums.x + sums.y;
+        join_row<G, kGroups>(sum, top, Largest(), whole, s_first, s_second, turn);
+        const float r = root_reciprocal(fmaf(sum, share, p.eps));
+        top = fabsf(top * r);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j) {
-            const int e = (j * G + g) * V;
-            float v[V], gain[V];
-            unpack<D, 16>(held[j], v);
-            gain_of(j, gain);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                v[i] = v[i] * r * gain[i];
+            for (int i = 0; i < V / 2; ++i)
+                v[j][i] = __fmul2_rn(v[j][i], both(r));
             if (p.y)
-                store_vec<D, WIDE>(y, e, width, pack<D, 16>(v));
-            if (!p.q)
-                continue;
-            uint32_t m = top;
-            if (p.block) {
+                store_vec<D, WIDE, kLanes>(y.at, (j * G + g) * V, width, s_rows, pack_pairs<D>(v[j]));
+        }
+        float largest[HOLD];
+        if (p.q) {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    m = max(m, __float_as_uint(fabsf(v[i])));
-                for (int d = p.block / V / 2; d > 0; d >>= 1)
-                    m = max(m, __shfl_xor_sync(kFullWarp, m, d));
+            for (int j = 0; j < HOLD; ++j) {
+                largest[j] = whole ? top : 0.f;
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i)
+                        largest[j] = max_nan(largest[j], max_nan(fabsf(v[j][i].x), fabsf(v[j][i].y)));
+                }
             }
-            const bool finite = m < 0x7f800000u;
+            for (int d = 1; d < lanes; d *= 2)
+#pragma unroll
+                for (int j = 0; j < HOLD; ++j)
+                    largest[j] = max_nan(largest[j], __shfl_xor_sync(kFullWarp, largest[j], d));
+        }
+#pragma unroll
+        for (int j = 0; j < HOLD; ++j) {
+            if (!p.q)
+                break;
+            const int e = (j * G + g) * V;
+            const float m = largest[j];
+            const bool write = writes && e < width && (j == 0 || !whole);
+            const int64_t at = scale_at + (j * G * V >> shift);
             float inverse;
-            const bool writes = p.block ? e < width && e % p.block == 0 : e == 0 && width > 0;
-            const int64_t at = row * p.scales_stride + (p.block ? e / p.block : 0);
             if (p.power) {
                 // m = c 2^a with c in [1, 2), 448 = 1.75 * 2^8: the exponent is a - 8, and one more where c > 1.75
-                const int biased = max(static_cast<int>(m >> 23) - 8 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0), 0);
+                const int biased = max(static_cast<int>((__float_as_uint(m) + 0x1fffffu) >> 23) - 8, 0);
+                const bool finite = m < INFINITY;
                 inverse = __uint_as_float(finite ? static_cast<uint32_t>(254 - biased) << 23 : 0x7fffffffu);
-                if (writes)
+                if (write)
                     static_cast<uint8_t *>(p.scales)[at] = finite ? static_cast<uint8_t>(biased) : 255u;
             } else {
-                const float scale = finite ? fmaxf(__uint_as_float(m) / 448.f, 1.17549435e-38f) : __uint_as_float(0x7fffffffu);
-                inverse = 1.f / scale;
-                if (writes)
+                constexpr float kLeast = 1.17549435e-38f;   // 2^-126
+                const float scale = m <= 448.f * kLeast ? kLeast : m < INFINITY ? over_448(m) : __uint_as_float(0x7fffffffu);
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(scale));
+                inverse = fmaf(fmaf(-scale, inverse, 1.f), inverse, inverse);
+                if (write)
                     static_cast<float *>(p.scales)[at] = scale;
             }
             uint32_t bytes[V / 4];
 #pragma unroll
-            for (int i = 0; i < V; i += 4)
-                bytes[i / 4] = e4m3_pair(v[i] * inverse, v[i + 1] * inverse) |
-                               e4m3_pair(v[i + 2] * inverse, v[i + 3] * inverse) << 16;
-            uint8_t *q = p.q + row * p.q_stride + e;
-            if constexpr (WIDE) {
-                if (e < width) {
-                    if constexpr (V == 8)
-                        *reinterpret_cast<uint2 *>(q) = make_uint2(bytes[0], bytes[1]);
-                    else
-                        *reinterpret_cast<uint32_t *>(q) = bytes[0];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (e + i < width)
-                        q[i] = static_cast<uint8_t>(bytes[i / 4] >> (8 * (i % 4)));
+            for (int i = 0; i < V / 2; i += 2) {
+                const float2 low = __fmul2_rn(v[j][i], both(inverse)), high = __fmul2_rn(v[j][i + 1], both(inverse));
+                bytes[i / 2] = e4m3_pair(low.x, low.y) | e4m3_pair(high.x, high.y) << 16;
             }
+            typename Bits<V>::type raw;
+            if constexpr (V == 8)
+                raw = make_uint2(bytes[0], bytes[1]);
+            else
+                raw = bytes[0];
+            if constexpr (!WIDE)
+                store_narrow<uint8_t, V, kLanes>(q.at, e, width, s_rows, raw);
+            else if (e < width)
+                *reinterpret_cast<typename Bits<V>::type *>(q.at + e) = raw;
         }
+        y.next();
+        q.next();
+        scale_at += step * p.scales_stride;
     }
+    if constexpr (kDepth > 0)
+        copies_wait<0>();
 }
 
 template <int D, bool WIDE, int G, int HOLD>
-__global__ void __launch_bounds__(norm_threads(G)) rms_norm_backward_kernel(const __grid_constant__ NormGradParams p)
+__global__ void __launch_bounds__(G * norm_groups(G, true), norm_ctas_per_sm(G, HOLD, true))
+rms_norm_backward_kernel(const __grid_constant__ NormGradParams p)
 {
     using T = typename Elem<D>::type;
-    constexpr int V = norm_vec<D>();
-    constexpr int kGroups = norm_threads(G) / G;
-    __shared__ float2 s_join[2][32];
-    // where a CTA takes several rows at once, their sums of dgain at the end, [groups][width]; from 512 threads on,
-    // whose registers do not hold them, the sums all along, [HOLD][V][threads]
-    extern __shared__ float s_gain[];
-    constexpr bool kHeld = G < 512;
-    const int g = threadIdx.x % G, group = threadIdx.x / G;
+    constexpr int V = norm_vec<D>(), kGroups = norm_groups(G, true), kDepth = norm_depth(WIDE, G, HOLD, true);
+    using Row = Group<G, kGroups>;
+    constexpr int kThreads = Row::kThreads, kLanes = Row::kLanes;
+    constexpr bool kGain = HOLD <= 2, kRegisters = norm_sums_in_registers(G, HOLD);   // the gain and the sums of dgain
+    static_assert(kRegisters || kGroups == 1, "several rows and sums in shared memory");
+    // The operands' rings; narrow rows: 16 bytes a thread.  Then the sums of dgain where the registers do not have them,
+    // [HOLD][V][G].  At the end, where a CTA takes several rows at once, [groups][width] of these sums from the start on.
+    extern __shared__ uint4 s_rows[];
+    float *s_gain = reinterpret_cast<float *>(s_rows + (WIDE ? 0 : kThreads));
+    __shared__ Joined<G, kGroups> s_first, s_second;
+    s_first.start();
+    s_second.start();
+    const int g = Row::rank();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + Row::number();
+    Operand<D, WIDE, G, HOLD, kDepth, kThreads> h, dy, dh;
+    h.start(p.h, row, p.h_stride, step, s_rows);
+    dy.start(p.dy, row, p.dy_stride, step, s_rows + kDepth * HOLD * kThreads);
+    dh.start(p.dh, row, p.dh_stride, step, s_rows + 2 * kDepth * HOLD * kThreads);
+    const auto copy = [&](int stage, int64_t of) {
+        const int width = of < p.rows ? p.width : 0;
+        h.copy(stage, width);
+        dy.copy(stage, width);
+        if (p.dh)
+            dh.copy(stage, width);
+        copies_end();
+    };
     grid_dependency_wait();
-    float held_gain[kHeld ? HOLD : 1][V], dgain[kHeld ? HOLD : 1][V];
+    if constexpr (kDepth > 0) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d)
+            copy(d, row + d * step);
+    }
+    if (p.parts)
+        grid_launch_dependents();   // their join, which sets up meanwhile
+    Result<T> dx;
+    dx.start(p.dx, row, p.dx_stride, step);
+    float2 gain[HOLD][V / 2], dgain[kRegisters ? HOLD : 1][V / 2];
 #pragma unroll
     for (int j = 0; j < HOLD; ++j) {
-        if constexpr (kHeld)
-            load_gain<V, WIDE>(p.gain, p.gain_dtype, (j * G + g) * V, p.width, held_gain[j]);
+        if constexpr (kGain)
+            load_gain<V, WIDE>(p.gain, p.gain_dtype, (j * G + g) * V, p.width, gain[j]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if constexpr (kHeld)
-                dgain[j][i] = 0.f;
+        for (int i = 0; i < V / 2; ++i) {
+            if constexpr (kRegisters)
+                dgain[j][i] = both(0.f);
             else
-                s_gain[(j * V + i) * G + g] = 0.f;
+                s_gain[(j * V + 2 * i) * G + g] = s_gain[(j * V + 2 * i + 1) * G + g] = 0.f;
         }
     }
-    const auto gain_of = [&](int j, float *v) {
-        if constexpr (kHeld) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                v[i] = held_gain[j][i];
-        } else {
-            load_gain<V, WIDE>(p.gain, p.gain_dtype, (j * G + g) * V, p.width, v);
-        }
-    };
     const float share = 1.f / static_cast<float>(p.width);
-    int turn = 0;
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups; first < p.rows;
-         first += static_cast<int64_t>(gridDim.x) * kGroups, ++turn) {
-        const int64_t row = first + group;
+    int stage = 0, turn = 0;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups; first < p.rows; first += step, row += step, ++turn) {
         const int width = row < p.rows ? p.width : 0;
-        const T *h = static_cast<const T *>(p.h) + row * p.h_stride, *dy = static_cast<const T *>(p.dy) + row * p.dy_stride;
-        uint4 held[HOLD], grad[HOLD];
-#pragma unroll
-        for (int j = 0; j < HOLD; ++j) {
-            held[j] = load_vec<D, WIDE>(h, (j * G + g) * V, width);
-            grad[j] = load_vec<D, WIDE>(dy, (j * G + g) * V, width);
+        if constexpr (kDepth > 0)
+            copies_wait<(kDepth > 0 ? kDepth - 1 : 0)>();
+        uint4 held[HOLD], grad[HOLD], more[HOLD];
+        h.get(stage, width, s_rows, held);
+        dy.get(stage, width, s_rows, grad);
+        if (p.dh)
+            dh.get(stage, width, s_rows, more);
+        if constexpr (kDepth > 0) {
+            copy(stage, row + kDepth * step);   // into the stage just read
+            stage = stage + 1 == kDepth ? 0 : stage + 1;
         }
-        float sum = 0.f, inner = 0.f;
+        float2 sums = both(0.f), inners = both(0.f);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j) {
-            float a[V], b[V], gain[V];
-            unpack<D, 16>(held[j], a);
-            unpack<D, 16>(grad[j], b);
-            gain_of(j, gain);
+            float2 a[V / 2], b[V / 2];
+            unpack_pairs<D>(held[j], a);
+            unpack_pairs<D>(grad[j], b);
+            if constexpr (!kGain)
+                load_gain<V, WIDE>(p.gain, p.gain_dtype, (j * G + g) * V, p.width, gain[j]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                sum = fmaf(a[i], a[i], sum);
-                inner = fmaf(b[i] * gain[i], a[i], inner);
+            for (int i = 0; i < V / 2; ++i) {
+                sums = __ffma2_rn(a[i], a[i], sums);
+                inners = __ffma2_rn(__fmul2_rn(b[i], gain[j][i]), a[i], inners);
             }
         }
-#pragma unroll
-        for (int d = (G < 32 ? G : 32) / 2; d > 0; d >>= 1) {
-            sum += __shfl_xor_sync(kFullWarp, sum, d);
-            inner += __shfl_xor_sync(kFullWarp, inner, d);
-        }
-        if constexpr (G > 32) {
-            if (threadIdx.x % 32 == 0)
-                s_join[turn & 1][threadIdx.x / 32] = make_float2(sum, inner);
-            __syncthreads();
-            sum = inner = 0.f;
-#pragma unroll
-            for (int i = 0; i < G / 32; ++i) {
-                sum += s_join[turn & 1][i].x;
-                inner += s_join[turn & 1][i].y;
-            }
-        }
-        const float r = 1.f / sqrtf(sum * share + p.eps);
-        const float back = inner * share * r * r;   // of h r
-        const T *dh = static_cast<const T *>(p.dh) + row * p.dh_stride;
-        T *dx = static_cast<T *>(p.dx) + row * p.dx_stride;
+        float sum = sums.x + sums.y, inner = inners.x + inners.y;
+        join_row<G, kGroups>(sum, inner, Add(), true, s_first, s_second, turn);
+        const float r = root_reciprocal(fmaf(sum, share, p.eps));
+        const float2 back = both(-(inner * share) * r * r), rs = both(r), mine = both(width ? r : 0.f);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j) {
-            float a[V], b[V], v[V], gain[V];
-            unpack<D, 16>(held[j], a);
-            unpack<D, 16>(grad[j], b);
-            gain_of(j, gain);
+            float2 a[V / 2], b[V / 2], v[V / 2];
+            unpack_pairs<D>(held[j], a);
+            unpack_pairs<D>(grad[j], b);
+            if constexpr (!kGain)
+                load_gain<V, WIDE>(p.gain, p.gain_dtype, (j * G + g) * V, p.width, gain[j]);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                v[i] = 0.f;
+            for (int i = 0; i < V / 2; ++i)
+                v[i] = both(0.f);
             if (p.dh)
-                unpack<D, 16>(load_vec<D, WIDE>(dh, (j * G + g) * V, width), v);
+                unpack_pairs<D>(more[j], v);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float &sum_of = kHeld ? dgain[kHeld ? j : 0][i] : s_gain[(j * V + i) * G + g];
-                if (width)
-                    sum_of = fmaf(b[i], a[i] * r, sum_of);
-                v[i] = fmaf(r, fmaf(-a[i], back, b[i] * gain[i]), v[i]);
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 unit = __fmul2_rn(a[i], mine);   // past the last row 0
+                if constexpr (kRegisters) {
+                    dgain[j][i] = __ffma2_rn(b[i], unit, dgain[j][i]);
+                } else {
+                    float *sum_of = s_gain + (j * V + 2 * i) * G + g;
+                    sum_of[0] = fmaf(b[i].x, unit.x, sum_of[0]);
+                    sum_of[G] = fmaf(b[i].y, unit.y, sum_of[G]);
+                }
+                v[i] = __ffma2_rn(rs, __ffma2_rn(a[i], back, __fmul2_rn(b[i], gain[j][i])), v[i]);
             }
-            store_vec<D, WIDE>(dx, (j * G + g) * V, width, pack<D, 16>(v));
+            store_vec<D, WIDE, kLanes>(dx.at, (j * G + g) * V, width, s_rows, pack_pairs<D>(v));
         }
+        dx.next();
     }
+    if constexpr (kDepth > 0)
+        copies_wait<0>();
     if (!p.parts)
         return;
     float *part = p.parts + static_cast<int64_t>(blockIdx.x) * p.width;
+    const auto sum_of = [&](int j, int i) {
+        if constexpr (kRegisters)
+            return i % 2 ? dgain[j][i / 2].y : dgain[j][i / 2].x;
+        else
+            return s_gain[(j * V + i) * G + g];
+    };
     if constexpr (kGroups > 1) {
+        __syncthreads();
+        float *sums = reinterpret_cast<float *>(s_rows);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int e = (j * G + g) * V + i;
                 if (e < p.width)
-                    s_gain[group * p.width + e] = dgain[kHeld ? j : 0][i];
+                    sums[Row::number() * p.width + e] = sum_of(j, i);
             }
         __syncthreads();
-        for (int e = threadIdx.x; e < p.width; e += norm_threads(G)) {
+        for (int e = threadIdx.x; e < p.width; e += kThreads) {
             float v = 0.f;
             for (int i = 0; i < kGroups; ++i)
-                v += s_gain[i * p.width + e];
+                v += sums[i * p.width + e];
             part[e] = v;
         }
     } else {
@@ -419,96 +721,110 @@ __global__ void __launch_bounds__(norm_threads(G)) rms_norm_backward_kernel(cons
             for (int i = 0; i < V; ++i) {
                 const int e = (j * G + g) * V + i;
                 if (e < p.width)
-                    part[e] = kHeld ? dgain[kHeld ? j : 0][i] : s_gain[(j * V + i) * G + g];
+                    part[e] = sum_of(j, i);
             }
     }
 }
 
+// The launch of a kernel whose CTAs take `groups` rows at once: as many CTAs as the rows need (`each` of them at least
+// to a group), `most` at most.
 template <class P>
-cudaError_t launch_norm(void (*kernel)(P), const P &p, int g, int ctas, size_t smem, cudaStream_t s)
+cudaError_t launch_norm(void (*kernel)(P), const P &p, int threads, int groups, int each, int most, int smem, int *ctas, cudaStream_t s)
 {
+    const int64_t per = static_cast<int64_t>(groups) * each, need = (p.rows + per - 1) / per;
+    *ctas = static_cast<int>(need < most ? need : most);
+    if (smem > 47 * 1024) {   // the kernels have up to 512 bytes of their own
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem);
+        if (e != cudaSuccess)
+            return e;
+    }
     cudaLaunchAttribute early;
     cudaLaunchConfig_t cfg = early_launch(&early);
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(norm_threads(g));
+    cfg.gridDim = dim3(*ctas);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// CTAs of a call: as many as rows need, up to `most`.
-inline int norm_ctas(int64_t rows, int g, int most)
+template <int D, bool WIDE, int G, int HOLD>
+cudaError_t launch_forward_as(const NormParams &p, int sms, cudaStream_t s)
 {
-    const int64_t groups = norm_threads(g) / g, ctas = (rows + groups - 1) / groups;
-    return static_cast<int>(ctas < most ? ctas : most);
-}
-
-// The threads of a row and the vectors each holds, by the row's vectors.  With 8-bit blocks a row has a warp at least
-// (a block's vectors are neighbouring lanes').
-template <int D, bool WIDE>
-cudaError_t launch_forward(const NormParams &p, int sms, cudaStream_t s)
-{
-    const int vecs = (p.width + norm_vec<D>() - 1) / norm_vec<D>();
-    const auto go = [&](auto kernel, int g) {
-        return launch_norm<NormParams>(kernel, p, g, norm_ctas(p.rows, g, sms * 16), 0, s);
-    };
-    if (vecs <= 16 && !(p.q && p.block))
-        return go(rms_norm_kernel<D, WIDE, 8, 2>, 8);
-    if (vecs <= 64)
-        return go(rms_norm_kernel<D, WIDE, 32, 2>, 32);
-    if (vecs <= 128)
-        return go(rms_norm_kernel<D, WIDE, 32, 4>, 32);
-    if (vecs <= 256)
-        return go(rms_norm_kernel<D, WIDE, 128, 2>, 128);
-    if (vecs <= 512)
-        return go(rms_norm_kernel<D, WIDE, 128, 4>, 128);
-    if (vecs <= 1024)
-        return go(rms_norm_kernel<D, WIDE, 256, 4>, 256);
-    if (vecs <= 2048)
-        return go(rms_norm_kernel<D, WIDE, 512, 4>, 512);
-    if (vecs <= 4096)
-        return go(rms_norm_kernel<D, WIDE, 1024, 4>, 1024);
-    return go(rms_norm_kernel<D, WIDE, 1024, norm_vec<D>() == 8 ? 4 : 8>, 1024);   // 32768 columns in 32 bits
+    constexpr int kGroups = norm_groups(G, false), kThreads = G * kGroups;
+    constexpr int kSmem = 16 * kThreads * (WIDE ? norm_depth(WIDE, G, HOLD, false) * 2 * HOLD : 1);
+    int ctas;
+    return launch_norm<NormParams>(rms_norm_kernel<D, WIDE, G, HOLD>, p, kThreads, kGroups, 1,
+                                   sms * norm_ctas_per_sm(G, HOLD, false), kSmem, &ctas, s);
 }
 
 template <int D, bool WIDE, int G, int HOLD>
-cudaError_t launch_backward_as(const NormGradParams &p, int most, int *parts, cudaStream_t s)
+cudaError_t launch_backward_as(const NormGradParams &p, int sms, int *parts, cudaStream_t s)
 {
-    constexpr int kGroups = norm_threads(G) / G;
-    const auto kernel = rms_norm_backward_kernel<D, WIDE, G, HOLD>;
-    size_t smem = kGroups > 1 ? sizeof(float) * kGroups * p.width : 0;
-    if constexpr (G >= 512) {
-        smem = sizeof(float) * HOLD * norm_vec<D>() * G;
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess)
-            return e;
+    constexpr int kGroups = norm_groups(G, true), kThreads = G * kGroups;
+    int smem = 16 * kThreads * (WIDE ? norm_depth(WIDE, G, HOLD, true) * 3 * HOLD : 1);
+    if (!norm_sums_in_registers(G, HOLD))
+        smem += 4 * HOLD * norm_vec<D>() * kThreads;
+    if (kGroups > 1)
+        smem = std::max(smem, 4 * kGroups * p.width);
+    const int most = std::min<int>(sms, kStepMaxCtas) * norm_ctas_per_sm(G, HOLD, true);
+    static_assert(norm_ctas_per_sm(G, HOLD, true) * kStepMaxCtas <= kNormMaxParts, "room for the parts");
+    return launch_norm<NormGradParams>(rms_norm_backward_kernel<D, WIDE, G, HOLD>, p, kThreads, kGroups, kNormLeastRows, most,
+                                       smem, parts, s);
+}
+
+// Calls what(G, HOLD) for rows of `vecs` vectors.  Two vectors a thread up to 512 (4096 columns of 16 bits), and as few
+// warps as hold them; more vectors beyond.  `narrow` rows have fewer kernels to choose from.  Blocks of columns need a
+// warp to a row at least (a block's vectors are neighbouring lanes').
+template <bool WIDE, int V, class F>
+cudaError_t with_shape(int vecs, bool blocks, F what)
+{
+#define CNS_NORM_SHAPE(G, HOLD) \
+    if (vecs <= G * HOLD)       \
+        return what(std::integral_constant<int, G>(), std::integral_constant<int, HOLD>())
+    if (!blocks)
+        CNS_NORM_SHAPE(8, 2);
+    CNS_NORM_SHAPE(32, 2);
+    CNS_NORM_SHAPE(64, 2);
+    if constexpr (WIDE) {
+        CNS_NORM_SHAPE(96, 2);
+        CNS_NORM_SHAPE(128, 2);
+        CNS_NORM_SHAPE(160, 2);
+        CNS_NORM_SHAPE(192, 2);
+        CNS_NORM_SHAPE(224, 2);
+    } else {
+        CNS_NORM_SHAPE(128, 2);
     }
-    *parts = norm_ctas(p.rows, G, most < kNormMaxParts ? most : kNormMaxParts);
-    return launch_norm<NormGradParams>(kernel, p, G, *parts, smem, s);
+    CNS_NORM_SHAPE(256, 2);
+    if constexpr (WIDE) {
+        CNS_NORM_SHAPE(320, 2);
+        CNS_NORM_SHAPE(384, 2);
+        CNS_NORM_SHAPE(448, 2);
+    }
+    CNS_NORM_SHAPE(512, 2);
+    CNS_NORM_SHAPE(512, 4);
+    CNS_NORM_SHAPE(1024, 4);
+    if constexpr (V == 4)
+        CNS_NORM_SHAPE(1024, 8);   // 32768 columns in 32 bits
+    return cudaErrorInvalidValue;
+#undef CNS_NORM_SHAPE
+}
+
+template <int D, bool WIDE>
+cudaError_t launch_forward(const NormParams &p, int sms, cudaStream_t s)
+{
+    constexpr int V = norm_vec<D>();
+    return with_shape<WIDE, V>((p.width + V - 1) / V, p.q && p.block, [&](auto g, auto hold) {
+        return launch_forward_as<D, WIDE, g(), hold()>(p, sms, s);
+    });
 }
 
 template <int D, bool WIDE>
 cudaError_t launch_backward(const NormGradParams &p, int sms, int *parts, cudaStream_t s)
 {
     constexpr int V = norm_vec<D>();
-    const int vecs = (p.width + V - 1) / V;
-    if (vecs <= 16)
-        return launch_backward_as<D, WIDE, 8, 2>(p, 4 * sms, parts, s);
-    if (vecs <= 64)
-        return launch_backward_as<D, WIDE, 32, 2>(p, 4 * sms, parts, s);
-    if (vecs <= 128)
-        return launch_backward_as<D, WIDE, 32, 4>(p, 4 * sms, parts, s);
-    if (vecs <= 256)
-        return launch_backward_as<D, WIDE, 128, 2>(p, 4 * sms, parts, s);
-    if (vecs <= 512)
-        return launch_backward_as<D, WIDE, 128, 4>(p, 4 * sms, parts, s);
-    if (vecs <= 1024)
-        return launch_backward_as<D, WIDE, 256, 4>(p, 2 * sms, parts, s);
-    if (vecs <= 2048)
-        return launch_backward_as<D, WIDE, 512, 4>(p, 2 * sms, parts, s);
-    if (vecs <= 4096 || V == 8)
-        return launch_backward_as<D, WIDE, 1024, 4>(p, sms, parts, s);
-    return launch_backward_as<D, WIDE, 1024, V == 8 ? 4 : 8>(p, sms, parts, s);
+    return with_shape<WIDE, V>((p.width + V - 1) / V, false, [&](auto g, auto hold) {
+        return launch_backward_as<D, WIDE, g(), hold()>(p, sms, parts, s);
+    });
 }
 
 // A type's kernels (rms_norm_*.cu); `parts`: how many parts of dgain the call leaves.

@@ -836,7 +836,8 @@ int cns_route_backward(const cns_route_grad_t *g);
  * A place outside 0 .. rows - 1 (-1, or past the end of a buffer of limited
  * capacity) has no row: nothing is read, written or added for it.  The others
  * are all different.  Rows that no place names are neither read nor written.
- * Outputs must not overlap inputs.  Strides are from row to row; 0 = packed. */
+ * Outputs must not overlap inputs.  Strides are from row to row, at most
+ * CNS_ROWS_MAX_STRIDE; 0 = packed. */
 
 /* Dispatch: rows[places[t][j]] = x[t], as bytes, whatever the elements are;
  * and, with scales_dev, row_scales[places[t][j]] = scales[t] (the scales of
@@ -861,6 +862,7 @@ typedef struct {
 } cns_dispatch_t;
 
 #define CNS_ROWS_MAX_BYTES 16777216
+#define CNS_ROWS_MAX_STRIDE 536870912
 
 /*
  * cns_dispatch -- asynchronous; may be captured into a CUDA graph.

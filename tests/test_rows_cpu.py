@@ -235,7 +235,7 @@ def handles(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     r = _native.Route()
     r.places, r.weights = torch.zeros((8, 2), dtype=torch.int32), torch.zeros(8, 2)
-    r.ids, r.places_dev = torch.zeros((8, 2), dtype=torch.int32), r.places.data_ptr()
+    r.ids, r.places_dev, r.weights_dev = r.places.clone(), r.places.data_ptr(), r.weights.data_ptr()
     r.capacity, r.index, r.others, r.types = 8, -1, True, (torch.int32, torch.float32)
     r.experts, r.top_k, r.tokens = 16, 2, 8
     n = _native.RmsNorm(width=16, scale_block=32, eps=1e-6)
@@ -318,7 +318,7 @@ def test_strides_and_sizes_that_reach_the_library(handles):
     cns.run_dispatch(r, wide[:, 4:20], rows=rows[:, :16], scales=torch.zeros(8, 3), row_scales=torch.zeros(11, 5)[:, 1:4])
     d = calls[-1][1]
     assert (d.tokens, d.rows, d.row_bytes, d.x_stride, d.rows_stride) == (8, 11, 32, 80, 48)
-    assert (d.scale_bytes, d.scales_stride, d.row_scales_stride, d.top_k) == (12, 12, 20, 2)
+    assert (d.scale_bytes, d.scales_stride, d.row_scales_stride, d.top_k) == (12, 0, 20, 2)
     assert d.x_dev == wide.data_ptr() + 8
     cns.run_dispatch(r, wide[:1, 4:20], rows=rows[:, :16])             # one row: no stride
     assert calls[-1][1].x_stride == 0 and calls[-1][1].tokens == 1
