@@ -106,23 +106,30 @@ __device__ __forceinline__ void move(const DispatchParams &p, const Tiling &m, u
     if (u >= m.units || t >= p.tokens)
         return;
     const B *x = reinterpret_cast<const B *>(from + t * from_stride) + u;
-    B v[H];
-#pragma unroll
-    for (int h = 0; h < H; ++h)
-        if (h == 0 || u + 32 * h < m.units)
-            v[h] = x[32 * h];
     const int32_t *place = p.places + t * p.top_k;
-#pragma unroll 4
-    for (int j = 0; j < p.top_k; ++j) {
-        const uint32_t row = static_cast<uint32_t>(place[j]);
-        if (row < p.limit) {
-            B *y = reinterpret_cast<B *>(to + static_cast<uint64_t>(row) * to_stride) + u;
+    const auto go = [&](auto full) {   // whether all its accesses are within the row
+        const auto within = [&](int h) { return decltype(full)::value || u + 32 * h < m.units; };
+        B v[H];
 #pragma unroll
-            for (int h = 0; h < H; ++h)
-                if (h == 0 || u + 32 * h < m.units)
-                    y[32 * h] = v[h];
+        for (int h = 0; h < H; ++h)
+            if (within(h))
+                v[h] = x[32 * h];
+#pragma unroll 4
+        for (int j = 0; j < p.top_k; ++j) {
+            const uint32_t row = static_cast<uint32_t>(place[j]);
+            if (row < p.limit) {
+                B *y = reinterpret_cast<B *>(to + static_cast<uint64_t>(row) * to_stride) + u;
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    if (within(h))
+                        y[32 * h] = v[h];
+            }
         }
-    }
+    };
+    if (A == 16 || u - threadIdx.x % 32 + 32 * H <= m.units)
+        go(std::true_type());
+    else
+        go(std::false_type());
 }
 
 template <int A>
@@ -156,24 +163,19 @@ struct CombineParams {
     Tiling data;
 };
 
-// CTAs to an SM that combine's registers are shared out for.
-constexpr int kCombineCtas = 4;
+// CTAs to an SM that combine's registers are shared out for: 64 registers a thread.  With three or two of them, and more
+// rows in flight a thread, k = 8 took up to 1.4 times as long (spills at 80 registers, too few threads at 128); narrow
+// accesses have three (four spill).
+__host__ __device__ constexpr int combine_ctas(int a) { return a == 16 ? 4 : 3; }
 
-// A thread has TOKENS tokens at a time and of each the rows of BATCH places, all in flight together; while they are on
-// their way it loads the places of the next ones.  As many CTAs as the GPU holds, so that only a thread's first rows
-// wait for their places.
-template <int D, int A, int BATCH, int TOKENS>
-__global__ void __launch_bounds__(kRowThreads, kCombineCtas) combine_kernel(const __grid_constant__ CombineParams p)
+// What a thread of combine_kernel does; FULL: all its accesses are within the row.
+template <int D, int A, int BATCH, int TOKENS, bool FULL>
+__device__ __forceinline__ void combine_rows(const CombineParams &p, int64_t t, uint32_t u)
 {
     using T = typename Elem<D>::type;
     using B = typename Bits<A>::type;
     constexpr int V = A / static_cast<int>(sizeof(T)), H = accesses(A);
-    int64_t t;
-    uint32_t u;
-    my_place<A, TOKENS>(p.data, blockIdx.x, &t, &u);
-    grid_dependency_wait();
-    if (u >= p.data.units)
-        return;
+    const auto within = [&](int h) { return FULL || u + 32 * h < p.data.units; };
     const T *rows = static_cast<const T *>(p.rows) + static_cast<int64_t>(u) * V;
     uint32_t next[TOKENS][BATCH];
     const auto places = [&](int64_t of, int j) {
@@ -199,10 +201,13 @@ __global__ void __launch_bounds__(kRowThreads, kCombineCtas) combine_kernel(cons
                 there[n][i] = next[n][i] < p.limit;
                 const B *row = reinterpret_cast<const B *>(rows + static_cast<uint64_t>(next[n][i]) * p.rows_stride);
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
+                for (int h = 0; h < H; ++h)
                     raw[n][i][h] = B{};
-                    if (there[n][i] && (h == 0 || u + 32 * h < p.data.units))
-                        raw[n][i][h] = row[32 * h];
+                if (there[n][i]) {
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        if (within(h))
+                            raw[n][i][h] = row[32 * h];
                 }
             }
         const int64_t now = t;
@@ -236,19 +241,27 @@ __global__ void __launch_bounds__(kRowThreads, kCombineCtas) combine_kernel(cons
                 break;
             const B *base = reinterpret_cast<const B *>(static_cast<const T *>(p.base) + (now + n) * p.base_stride) + u;
             B *y = reinterpret_cast<B *>(static_cast<T *>(p.y) + (now + n) * p.y_stride) + u;
+            if (p.base) {
+                B raw_base[H];
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                if (h > 0 && u + 32 * h >= p.data.units)
-                    break;
-                if (p.base) {
+                for (int h = 0; h < H; ++h) {
+                    raw_base[h] = B{};
+                    if (within(h))
+                        raw_base[h] = base[32 * h];
+                }
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
                     float v[V];
-                    unpack<D, A>(base[32 * h], v);
+                    unpack<D, A>(raw_base[h], v);
 #pragma unroll
                     for (int k = 0; k < V; ++k)
                         sum[n][h][k] += v[k];
                 }
-                y[32 * h] = pack<D, A>(sum[n][h]);
             }
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                if (within(h))
+                    y[32 * h] = pack<D, A>(sum[n][h]);
         }
 #pragma unroll
         for (int n = 0; n < TOKENS; ++n)
@@ -258,6 +271,24 @@ __global__ void __launch_bounds__(kRowThreads, kCombineCtas) combine_kernel(cons
                 for (int k = 0; k < V; ++k)
                     sum[n][h][k] = 0.f;
     }
+}
+
+// A thread has TOKENS tokens at a time and of each the rows of BATCH places, all in flight together; while they are on
+// their way it loads the places of the next ones.  As many CTAs as the GPU holds, so that only a thread's first rows
+// wait for their places.
+template <int D, int A, int BATCH, int TOKENS>
+__global__ void __launch_bounds__(kRowThreads, combine_ctas(A)) combine_kernel(const __grid_constant__ CombineParams p)
+{
+    int64_t t;
+    uint32_t u;
+    my_place<A, TOKENS>(p.data, blockIdx.x, &t, &u);
+    grid_dependency_wait();
+    if (u >= p.data.units)
+        return;
+    if (A == 16 || u - threadIdx.x % 32 + 32 * accesses(A) <= p.data.units)
+        combine_rows<D, A, BATCH, TOKENS, true>(p, t, u);
+    else
+        combine_rows<D, A, BATCH, TOKENS, false>(p, t, u);
 }
 
 struct CombineGradParams {
@@ -317,14 +348,13 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __g
     const uint32_t stretch = LANES ? kLanes * HELD : blockDim.x * HELD;
     for (uint32_t u0 = 0; u0 < p.units; u0 += stretch) {   // as often in every thread
         const uint32_t u = u0 + (LANES ? 0u : slot * (32 * HELD)) + l;
+        const auto mine = [&](int k) { return token && u + k * kLanes < p.units; };
         const B *from = reinterpret_cast<const B *>(static_cast<const T *>(p.dy) + t * p.dy_stride) + u;
         float dy[HELD][V];
-        bool mine[HELD];
 #pragma unroll
         for (int k = 0; k < HELD; ++k) {
-            mine[k] = token && u + k * kLanes < p.units;
             B raw = B{};
-            if (mine[k])
+            if (mine(k))
                 raw = from[k * kLanes];
             unpack<D, A>(raw, dy[k]);
         }
@@ -336,10 +366,13 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __g
                 row[i] = token && j + i < p.top_k ? static_cast<uint32_t>(place[j + i]) : 0xffffffffu;
                 const B *at = reinterpret_cast<const B *>(static_cast<const T *>(p.rows) + static_cast<uint64_t>(row[i]) * p.rows_stride) + u;
 #pragma unroll
-                for (int k = 0; k < HELD; ++k) {
+                for (int k = 0; k < HELD; ++k)
                     raw[i][k] = B{};
-                    if (p.dweights && mine[k] && row[i] < p.limit)
-                        raw[i][k] = at[k * kLanes];
+                if (p.dweights && row[i] < p.limit) {
+#pragma unroll
+                    for (int k = 0; k < HELD; ++k)
+                        if (mine(k))
+                            raw[i][k] = at[k * kLanes];
                 }
             }
             float dot[BATCH];
@@ -355,7 +388,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __g
 #pragma unroll
                         for (int e = 0; e < V; ++e)
                             v[e] = w * dy[k][e];
-                        if (mine[k])
+                        if (mine(k))
                             to[k * kLanes] = pack<D, A>(v);
                     }
                 }
@@ -414,8 +447,8 @@ cudaError_t launch_combine_as(CombineParams &p, int sms, cudaStream_t s)
     if (!tile(p.tokens, p.data.units, A, TOKENS, &p.data))
         return cudaErrorInvalidConfiguration;
     uint32_t ctas = p.data.ctas;
-    const uint32_t most = static_cast<uint32_t>(sms) * kCombineCtas;
     if constexpr (A == 16) {
+        const uint32_t most = static_cast<uint32_t>(sms) * combine_ctas(A);
         // whole rows of parts, so that a thread keeps its part
         ctas = std::min(ctas, std::max<uint32_t>(most / p.data.parts, 1u) * p.data.parts);
         p.step = static_cast<int64_t>(ctas / p.data.parts) * p.data.per * TOKENS;

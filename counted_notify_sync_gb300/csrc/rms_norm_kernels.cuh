@@ -49,9 +49,10 @@ struct NormGradParams {
     float eps;
 };
 
-// Most CTAs of a gradient, each of which leaves a part of dgain: 512 threads to an SM in CTAs of more than 128.
+// Most CTAs of a gradient, each of which leaves a part of dgain: 512 threads to an SM in CTAs of 160 or more.
 constexpr int kNormMaxParts = 3 * kStepMaxCtas;
-// Rows that a group of a gradient has at least.
+// Rows that a group of a gradient has at least, so that few parts are left to join: 777 x 1000 f32 takes 5.0 us with
+// four, 6.5 with one, two or eight.
 constexpr int kNormLeastRows = 4;
 // Dynamic shared memory that every kernel here may be launched with.
 constexpr int kNormMaxSmem = 200 * 1024;
@@ -66,16 +67,22 @@ __device__ __forceinline__ void load_narrow(const void *row, int width, uint4 *s
     using T = typename Elem<D>::type;
     constexpr int V = norm_vec<D>(), L = G < 32 ? G : 32;
     const int g = threadIdx.x % G, l = g % L;
-    const T *from = static_cast<const T *>(row);
+    const T *from = static_cast<const T *>(row) + (g - l) * V + l;
     T *s = reinterpret_cast<T *>(scratch + (threadIdx.x - l));
     T v[HOLD][V];
 #pragma unroll
-    for (int j = 0; j < HOLD; ++j)
+    for (int j = 0; j < HOLD; ++j) {
+        const int first = (j * G + g - l) * V;   // of the lanes' stretch
+        if (first + L * V <= width) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = (j * G + g - l) * V + i * L + l;
-            v[j][i] = e < width ? from[e] : T(0.f);
+            for (int i = 0; i < V; ++i)
+                v[j][i] = from[j * G * V + i * L];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                v[j][i] = first + i * L + l < width ? from[j * G * V + i * L] : T(0.f);
         }
+    }
 #pragma unroll
     for (int j = 0; j < HOLD; ++j) {
         __syncwarp();
@@ -98,11 +105,17 @@ __device__ __forceinline__ void store_narrow(T *row, int e, int width, uint4 *sc
     __syncwarp();
     *mine = raw;
     __syncwarp();
+    const int first = e - l * V;   // of the lanes' stretch
+    row += first + l;
+    if (first + L * V <= width) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int at = e - l * V + i * L + l;
-        if (at < width)
-            row[at] = s[i * L + l];
+        for (int i = 0; i < V; ++i)
+            row[i * L] = s[i * L + l];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (first + i * L + l < width)
+                row[i * L] = s[i * L + l];
     }
 }
 
@@ -291,8 +304,9 @@ struct Joined {
     // the places that no warp fills: before the first row's barrier
     __device__ __forceinline__ void start()
     {
-        if (threadIdx.x < 2 * kSize && threadIdx.x % kRoom >= kWarps)
-            reinterpret_cast<float *>(s)[threadIdx.x] = 0.f;
+        if constexpr (kWarps > 0 && kWarps < kRoom)
+            if (threadIdx.x < 2 * kSize && threadIdx.x % kRoom >= kWarps)
+                reinterpret_cast<float *>(s)[threadIdx.x] = 0.f;
     }
     __device__ __forceinline__ void put(int turn, float v)
     {
@@ -751,17 +765,17 @@ template <int D, bool WIDE, int G, int HOLD>
 cudaError_t launch_forward_as(const NormParams &p, int sms, cudaStream_t s)
 {
     constexpr int kGroups = norm_groups(G, false), kThreads = G * kGroups;
-    constexpr int kSmem = 16 * kThreads * (WIDE ? norm_depth(WIDE, G, HOLD, false) * 2 * HOLD : 1);
+    const int smem = 16 * kThreads * (WIDE ? norm_depth(WIDE, G, HOLD, false) * (p.residual ? 2 : 1) * HOLD : 1);
     int ctas;
     return launch_norm<NormParams>(rms_norm_kernel<D, WIDE, G, HOLD>, p, kThreads, kGroups, 1,
-                                   sms * norm_ctas_per_sm(G, HOLD, false), kSmem, &ctas, s);
+                                   sms * norm_ctas_per_sm(G, HOLD, false), smem, &ctas, s);
 }
 
 template <int D, bool WIDE, int G, int HOLD>
 cudaError_t launch_backward_as(const NormGradParams &p, int sms, int *parts, cudaStream_t s)
 {
     constexpr int kGroups = norm_groups(G, true), kThreads = G * kGroups;
-    int smem = 16 * kThreads * (WIDE ? norm_depth(WIDE, G, HOLD, true) * 3 * HOLD : 1);
+    int smem = 16 * kThreads * (WIDE ? norm_depth(WIDE, G, HOLD, true) * (p.dh ? 3 : 2) * HOLD : 1);
     if (!norm_sums_in_registers(G, HOLD))
         smem += 4 * HOLD * norm_vec<D>() * kThreads;
     if (kGroups > 1)
@@ -772,10 +786,10 @@ cudaError_t launch_backward_as(const NormGradParams &p, int sms, int *parts, cud
                                        smem, parts, s);
 }
 
-// Calls what(G, HOLD) for rows of `vecs` vectors.  Two vectors a thread up to 512 (4096 columns of 16 bits), and as few
-// warps as hold them; more vectors beyond.  `narrow` rows have fewer kernels to choose from.  Blocks of columns need a
-// warp to a row at least (a block's vectors are neighbouring lanes').
-template <bool WIDE, int V, class F>
+// Calls what(G, HOLD) for rows of `vecs` vectors.  Two vectors a thread up to 1024 (8192 columns of 16 bits), and as few
+// warps as hold them; four vectors beyond.  Blocks of columns need a warp to a row at least (a block's vectors are
+// neighbouring lanes').
+template <int V, class F>
 cudaError_t with_shape(int vecs, bool blocks, F what)
 {
 #define CNS_NORM_SHAPE(G, HOLD) \
@@ -785,21 +799,15 @@ cudaError_t with_shape(int vecs, bool blocks, F what)
         CNS_NORM_SHAPE(8, 2);
     CNS_NORM_SHAPE(32, 2);
     CNS_NORM_SHAPE(64, 2);
-    if constexpr (WIDE) {
-        CNS_NORM_SHAPE(96, 2);
-        CNS_NORM_SHAPE(128, 2);
-        CNS_NORM_SHAPE(160, 2);
-        CNS_NORM_SHAPE(192, 2);
-        CNS_NORM_SHAPE(224, 2);
-    } else {
-        CNS_NORM_SHAPE(128, 2);
-    }
+    CNS_NORM_SHAPE(96, 2);
+    CNS_NORM_SHAPE(128, 2);
+    CNS_NORM_SHAPE(160, 2);
+    CNS_NORM_SHAPE(192, 2);
+    CNS_NORM_SHAPE(224, 2);
     CNS_NORM_SHAPE(256, 2);
-    if constexpr (WIDE) {
-        CNS_NORM_SHAPE(320, 2);
-        CNS_NORM_SHAPE(384, 2);
-        CNS_NORM_SHAPE(448, 2);
-    }
+    CNS_NORM_SHAPE(320, 2);
+    CNS_NORM_SHAPE(384, 2);
+    CNS_NORM_SHAPE(448, 2);
     CNS_NORM_SHAPE(512, 2);
     CNS_NORM_SHAPE(512, 4);
     CNS_NORM_SHAPE(1024, 4);
@@ -813,7 +821,7 @@ template <int D, bool WIDE>
 cudaError_t launch_forward(const NormParams &p, int sms, cudaStream_t s)
 {
     constexpr int V = norm_vec<D>();
-    return with_shape<WIDE, V>((p.width + V - 1) / V, p.q && p.block, [&](auto g, auto hold) {
+    return with_shape<V>((p.width + V - 1) / V, p.q && p.block, [&](auto g, auto hold) {
         return launch_forward_as<D, WIDE, g(), hold()>(p, sms, s);
     });
 }
@@ -822,7 +830,7 @@ template <int D, bool WIDE>
 cudaError_t launch_backward(const NormGradParams &p, int sms, int *parts, cudaStream_t s)
 {
     constexpr int V = norm_vec<D>();
-    return with_shape<WIDE, V>((p.width + V - 1) / V, false, [&](auto g, auto hold) {
+    return with_shape<V>((p.width + V - 1) / V, false, [&](auto g, auto hold) {
         return launch_backward_as<D, WIDE, g(), hold()>(p, sms, parts, s);
     });
 }
