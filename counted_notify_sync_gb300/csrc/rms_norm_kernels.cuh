@@ -403,24 +403,28 @@ __host__ __device__ constexpr int norm_ctas_per_sm(int g, int hold, bool grad)
 // Whether the gradient's sums of dgain stay in registers; else they are in shared memory.
 __host__ __device__ constexpr bool norm_sums_in_registers(int g, int hold) { return g * hold <= 2048 && hold <= 4; }
 
-// Rows on their way ahead of the one at hand: one, two of the gradient; none where the shared memory lacks the room.
-// More of them cost time, presumably because the DRAM's pages are left and opened again in between: 16384 x 4096 bf16
-// takes the norm 84.5 us with one, 85.8 with two and 88.5 with four; its gradient 89.5, 82.6 and 88.5.
-__host__ __device__ constexpr int norm_depth(bool wide, int g, int hold, bool grad)
+// Rows on their way ahead of the one at hand, of `operands` tensors each (3: the gradient): two, one of a norm with a
+// residual; none where the shared memory lacks the room.  More of them cost time, presumably because the DRAM's pages are
+// left and opened again in between: 16384 x 4096 bf16 takes the norm with a residual 84.5 us with one, 85.8 with two and
+// 88.5 with four, without one 46.9, 41.7 and (three) 45.5; its gradient 89.5, 82.6 and (four) 88.5.
+__host__ __device__ constexpr int norm_depth(bool wide, int g, int hold, int operands)
 {
-    const int depth = grad ? 2 : 1, threads = g * norm_groups(g, grad) * norm_ctas_per_sm(g, hold, grad);
-    return !wide || (grad && !norm_sums_in_registers(g, hold)) || 16 * threads * hold * depth * (grad ? 3 : 2) > 192 * 1024 ? 0 : depth;
+    const bool grad = operands == 3;
+    const int depth = operands == 2 ? 1 : 2, threads = g * norm_groups(g, grad) * norm_ctas_per_sm(g, hold, grad);
+    return !wide || (grad && !norm_sums_in_registers(g, hold)) || 16 * threads * hold * depth * operands > 192 * 1024 ? 0 : depth;
 }
 
-template <int D, bool WIDE, int G, int HOLD>
+// RESIDUAL: whether there is one (narrow rows: whether there may be one).
+template <int D, bool WIDE, int G, int HOLD, bool RESIDUAL>
 __global__ void __launch_bounds__(G * norm_groups(G, false), norm_ctas_per_sm(G, HOLD, false))
 rms_norm_kernel(const __grid_constant__ NormParams p)
 {
     using T = typename Elem<D>::type;
-    constexpr int V = norm_vec<D>(), kGroups = norm_groups(G, false), kDepth = norm_depth(WIDE, G, HOLD, false);
+    constexpr int V = norm_vec<D>(), kGroups = norm_groups(G, false), kDepth = norm_depth(WIDE, G, HOLD, RESIDUAL ? 2 : 1);
     using Row = Group<G, kGroups>;
     constexpr int kThreads = Row::kThreads, kLanes = Row::kLanes;
-    constexpr bool kGain = HOLD <= 2;   // the gain stays in registers
+    constexpr bool kGain = G * HOLD <= 1024;   // the gain stays in registers
+    const bool add = RESIDUAL && (WIDE || p.residual);
     extern __shared__ uint4 s_rows[];   // the operands' rings; narrow rows: 16 bytes a thread
     __shared__ Joined<G, kGroups> s_first, s_second;
     s_first.start();
@@ -434,7 +438,7 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
     const auto copy = [&](int stage, int64_t of) {
         const int width = of < p.rows ? p.width : 0;   // past the last row, a row without columns
         x.copy(stage, width);
-        if (p.residual)
+        if constexpr (RESIDUAL)
             residual.copy(stage, width);
         copies_end();
     };
@@ -469,7 +473,7 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
             copies_wait<(kDepth > 0 ? kDepth - 1 : 0)>();
         uint4 held[HOLD];
         x.get(stage, width, s_rows, held);
-        if (p.residual) {
+        if (add) {
             uint4 more[HOLD];
             residual.get(stage, width, s_rows, more);
 #pragma unroll
@@ -588,7 +592,7 @@ __global__ void __launch_bounds__(G * norm_groups(G, true), norm_ctas_per_sm(G, 
 rms_norm_backward_kernel(const __grid_constant__ NormGradParams p)
 {
     using T = typename Elem<D>::type;
-    constexpr int V = norm_vec<D>(), kGroups = norm_groups(G, true), kDepth = norm_depth(WIDE, G, HOLD, true);
+    constexpr int V = norm_vec<D>(), kGroups = norm_groups(G, true), kDepth = norm_depth(WIDE, G, HOLD, 3);
     using Row = Group<G, kGroups>;
     constexpr int kThreads = Row::kThreads, kLanes = Row::kLanes;
     constexpr bool kGain = HOLD <= 2, kRegisters = norm_sums_in_registers(G, HOLD);   // the gain and the sums of dgain
@@ -761,21 +765,21 @@ cudaError_t launch_norm(void (*kernel)(P), const P &p, int threads, int groups, 
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int D, bool WIDE, int G, int HOLD>
+template <int D, bool WIDE, int G, int HOLD, bool RESIDUAL>
 cudaError_t launch_forward_as(const NormParams &p, int sms, cudaStream_t s)
 {
-    constexpr int kGroups = norm_groups(G, false), kThreads = G * kGroups;
-    const int smem = 16 * kThreads * (WIDE ? norm_depth(WIDE, G, HOLD, false) * (p.residual ? 2 : 1) * HOLD : 1);
+    constexpr int kGroups = norm_groups(G, false), kThreads = G * kGroups, kOperands = RESIDUAL ? 2 : 1;
+    constexpr int kSmem = 16 * kThreads * (WIDE ? norm_depth(WIDE, G, HOLD, kOperands) * kOperands * HOLD : 1);
     int ctas;
-    return launch_norm<NormParams>(rms_norm_kernel<D, WIDE, G, HOLD>, p, kThreads, kGroups, 1,
-                                   sms * norm_ctas_per_sm(G, HOLD, false), smem, &ctas, s);
+    return launch_norm<NormParams>(rms_norm_kernel<D, WIDE, G, HOLD, RESIDUAL>, p, kThreads, kGroups, 1,
+                                   sms * norm_ctas_per_sm(G, HOLD, false), kSmem, &ctas, s);
 }
 
 template <int D, bool WIDE, int G, int HOLD>
 cudaError_t launch_backward_as(const NormGradParams &p, int sms, int *parts, cudaStream_t s)
 {
     constexpr int kGroups = norm_groups(G, true), kThreads = G * kGroups;
-    int smem = 16 * kThreads * (WIDE ? norm_depth(WIDE, G, HOLD, true) * (p.dh ? 3 : 2) * HOLD : 1);
+    int smem = 16 * kThreads * (WIDE ? norm_depth(WIDE, G, HOLD, 3) * (p.dh ? 3 : 2) * HOLD : 1);
     if (!norm_sums_in_registers(G, HOLD))
         smem += 4 * HOLD * norm_vec<D>() * kThreads;
     if (kGroups > 1)
@@ -788,9 +792,11 @@ cudaError_t launch_backward_as(const NormGradParams &p, int sms, int *parts, cud
 
 // Calls what(G, HOLD) for rows of `vecs` vectors.  Two vectors a thread up to 1024 (8192 columns of 16 bits), and as few
 // warps as hold them; four vectors beyond.  Blocks of columns need a warp to a row at least (a block's vectors are
-// neighbouring lanes').
-template <int V, class F>
-cudaError_t with_shape(int vecs, bool blocks, F what)
+// neighbouring lanes').  `few`: four vectors a thread from 128 on; where little memory traffic comes with much arithmetic
+// it pays that half as many threads do what each does once a row (16384 x 4096 bf16 to e4m3 alone 40.3 us, with two
+// vectors 47.5; with a residual and y 101.2 against 98.9).
+template <int V, bool FEW, class F>
+cudaError_t with_shape(int vecs, bool blocks, bool few, F what)
 {
 #define CNS_NORM_SHAPE(G, HOLD) \
     if (vecs <= G * HOLD)       \
@@ -799,6 +805,17 @@ cudaError_t with_shape(int vecs, bool blocks, F what)
         CNS_NORM_SHAPE(8, 2);
     CNS_NORM_SHAPE(32, 2);
     CNS_NORM_SHAPE(64, 2);
+    if constexpr (FEW) {
+        if (few) {
+            CNS_NORM_SHAPE(64, 4);
+            CNS_NORM_SHAPE(96, 4);
+            CNS_NORM_SHAPE(128, 4);
+            CNS_NORM_SHAPE(160, 4);
+            CNS_NORM_SHAPE(192, 4);
+            CNS_NORM_SHAPE(224, 4);
+            CNS_NORM_SHAPE(256, 4);
+        }
+    }
     CNS_NORM_SHAPE(96, 2);
     CNS_NORM_SHAPE(128, 2);
     CNS_NORM_SHAPE(160, 2);
@@ -817,20 +834,29 @@ cudaError_t with_shape(int vecs, bool blocks, F what)
 #undef CNS_NORM_SHAPE
 }
 
+template <int D, bool WIDE, bool RESIDUAL>
+cudaError_t launch_forward_with(const NormParams &p, int sms, cudaStream_t s)
+{
+    constexpr int V = norm_vec<D>();
+    return with_shape<V, WIDE && !RESIDUAL>((p.width + V - 1) / V, p.q && p.block, p.q && !p.y, [&](auto g, auto hold) {
+        return launch_forward_as<D, WIDE, g(), hold(), RESIDUAL>(p, sms, s);
+    });
+}
+
 template <int D, bool WIDE>
 cudaError_t launch_forward(const NormParams &p, int sms, cudaStream_t s)
 {
-    constexpr int V = norm_vec<D>();
-    return with_shape<V>((p.width + V - 1) / V, p.q && p.block, [&](auto g, auto hold) {
-        return launch_forward_as<D, WIDE, g(), hold()>(p, sms, s);
-    });
+    if constexpr (WIDE)
+        if (!p.residual)
+            return launch_forward_with<D, WIDE, false>(p, sms, s);
+    return launch_forward_with<D, WIDE, true>(p, sms, s);
 }
 
 template <int D, bool WIDE>
 cudaError_t launch_backward(const NormGradParams &p, int sms, int *parts, cudaStream_t s)
 {
     constexpr int V = norm_vec<D>();
-    return with_shape<V>((p.width + V - 1) / V, false, [&](auto g, auto hold) {
+    return with_shape<V, false>((p.width + V - 1) / V, false, false, [&](auto g, auto hold) {
         return launch_backward_as<D, WIDE, g(), hold()>(p, sms, parts, s);
     });
 }

@@ -178,3 +178,46 @@ def test_the_examples_block(cns):
     assert np.isfinite(losses).all()
     for before, after in norms:
         assert after <= min(before, 0.05) * (1 + 1e-5)
+
+
+def test_threads_share_handles(cns):
+    """Calls of several threads, each on a stream and tensors of its own, by one route and one norm."""
+    import threading
+
+    import torch
+    torch.manual_seed(8)
+    t, width, e, k = 900, 520, 16, 4
+    norm, route = cns.new_rms_norm(width, scale_block=128), cns.new_route(t, e, k)
+    cns.run_route(route, torch.randn(t, e, device="cuda"), sync=True)
+    places, weights = route.places.clone(), route.weights.clone()
+    gain = torch.randn(width, device="cuda")
+
+    def step(x, dy, stream):
+        h, y, q, scales = cns.run_rms_norm(norm, x, gain, residual=dy, stream=stream)
+        rows = cns.run_dispatch(route, y, places=places, stream=stream)
+        out = cns.run_combine(route, rows, weights=weights, places=places, base=h, stream=stream)
+        drows, dweights = cns.run_combine_backward(route, rows, dy, weights=weights, places=places, stream=stream)
+        dx, dgain = cns.run_rms_norm_backward(norm, h, gain, cns.run_dispatch_backward(route, drows, places=places, stream=stream),
+                                              dh=dy, stream=stream)
+        return h, y, q, scales, rows, out, drows, dweights, dx, dgain
+
+    inputs = [(torch.randn(t, width, device="cuda"), torch.randn(t, width, device="cuda")) for _ in range(4)]
+    want = [step(x, dy, None) for x, dy in inputs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(30):
+                got = step(*inputs[i], s)
+                s.synchronize()
+                if not all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want[i])):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong
