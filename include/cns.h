@@ -947,7 +947,8 @@ typedef enum { CNS_SCALE_F32 = 0, CNS_SCALE_E8M0 = 1 } cns_scale_t;
  *   CNS_SCALE_F32   s = max(m / 448, 2^-126);
  *   CNS_SCALE_E8M0  s = the least power of two >= m / 448, from 2^-127 on;
  *   q = y / s rounded to the nearest e4m3 (ties to even).
- * A block with an infinity or a NaN has s = NaN and q = NaN throughout. */
+ * A block with an infinity or a NaN has s = NaN and q = NaN throughout.
+ *   But for h as said below, no output may overlap another tensor of the call. */
 typedef struct {
     const void *x_dev;         /* (in) [rows][width] */
     const void *residual_dev;  /* (in, optional) [rows][width] */
