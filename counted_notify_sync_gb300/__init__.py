@@ -368,7 +368,8 @@ def run_dispatch(route, x, *, places=None, rows=None, scales=None, row_scales=No
     are then rows[offsets[e]:offsets[e + 1]].  `rows` [any number, width] (default: a new tensor of tokens * top_k, of
     `stream`'s memory); places outside it are passed over (a limited capacity), and rows that no place names stay as they
     were, in a new tensor whatever its memory held.  With `scales` [tokens, n], of any type, row_scales[places[t, j]] =
-    scales[t] too.  Returns rows, with scales (rows, row_scales).  run_dispatch_backward has the gradient."""
+    scales[t] too.  Returns rows, with scales (rows, row_scales), no part of torch's graph: run_dispatch_backward has the
+    gradient."""
     if route.others:
         _check_current(route.index)
     index, shape, dtype, size, top_k = route.index, x.shape, x.dtype, x.element_size(), route.top_k
@@ -501,6 +502,8 @@ def new_rms_norm(width: int, *, eps: float = 1e-6, y: bool = True, scale_block: 
         raise ValueError("a norm with neither y nor 8-bit values")
     n = _native.RmsNorm()
     device = torch.device(device or "cuda")
+    if device.type != "cuda":
+        raise ValueError(f"a norm on {device}, a CUDA device expected")
     n.index = torch.cuda.current_device() if device.index is None else device.index
     n.others = torch.cuda.device_count() > 1
     n.has_y, n.has_q = y, scale_block is not None
@@ -524,8 +527,8 @@ def run_rms_norm(norm, x, gain=None, *, residual=None, h=None, y=None, q=None, s
     """Normalise the rows of `x` ([rows, width], float32, bfloat16 or float16, rows at any stride) on `stream` (None:
     the default stream): h = x + residual, y = h / sqrt(mean(h^2) + eps) * gain, q and scales as new_rms_norm says.
     Returns (h, y, q, scales): h is x without a residual, and what the norm does not have is None.  The results go to
-    the tensors given (h may be x or residual), or to new ones, of `stream`'s memory.  run_rms_norm_backward has the
-    gradient."""
+    the tensors given (h may be x or residual), or to new ones, of `stream`'s memory.  They are no part of torch's graph:
+    run_rms_norm_backward has the gradient."""
     index, shape, dtype = norm.index, (len(x), norm.width), x.dtype
     if norm.others:
         _check_current(index)

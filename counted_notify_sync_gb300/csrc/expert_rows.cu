@@ -168,10 +168,9 @@ struct CombineParams {
     Tiling data;
 };
 
-// CTAs to an SM that combine's registers are shared out for: 64 registers a thread.  With three or two of them, and more
-// rows in flight a thread, k = 8 took up to 1.4 times as long (spills at 80 registers, too few threads at 128); narrow
-// accesses have three (four spill).
-__host__ __device__ constexpr int combine_ctas(int a) { return a == 16 ? 4 : 3; }
+// CTAs to an SM that combine's registers are shared out for, by the rows that a thread has in flight: 64 registers a
+// thread where those are up to four, else 80.  Narrow accesses have three CTAs (four spill).
+__host__ __device__ constexpr int combine_ctas(int a, int rows) { return a == 16 && rows <= 4 ? 4 : 3; }
 
 // What a thread of combine_kernel does; FULL: all its accesses are within the row.
 template <int D, int A, int BATCH, int TOKENS, bool FULL>
@@ -278,13 +277,12 @@ __device__ __forceinline__ void combine_rows(const CombineParams &p, int64_t t, 
     }
 }
 
-// A thread has TOKENS tokens at a time and of each the rows of BATCH places, all in flight together (four loads of 16
-// bytes); while they are on their way it loads the places of the next ones.  As many CTAs as the GPU holds, so that only a
+// A thread has TOKENS tokens at a time and of each the rows of BATCH places, all in flight together; while they are on their way it loads the places of the next ones.  As many CTAs as the GPU holds, so that only a
 // thread's first rows wait for their places: 65536 x 1024 bf16 with two places takes 66.4 us, 90 % of the copy rate; a CTA
 // for every 256 accesses, each waiting for its places, took 91.  16384 x 4096 bf16, 8 places: 180 us as a dispatch's
 // gradient (99 %), 203 with weights and a base (98 %).  8192 x 2049 bf16, 4 places: 46.3 us (53 %; instructions).
 template <int D, int A, int BATCH, int TOKENS>
-__global__ void __launch_bounds__(kRowThreads, combine_ctas(A)) combine_kernel(const __grid_constant__ CombineParams p)
+__global__ void __launch_bounds__(kRowThreads, combine_ctas(A, BATCH * TOKENS)) combine_kernel(const __grid_constant__ CombineParams p)
 {
     int64_t t;
     uint32_t u;
@@ -458,7 +456,7 @@ cudaError_t launch_combine_as(CombineParams &p, int sms, cudaStream_t s)
         return cudaErrorInvalidConfiguration;
     uint32_t ctas = p.data.ctas;
     if constexpr (A == 16) {
-        const uint32_t most = static_cast<uint32_t>(sms) * combine_ctas(A);
+        const uint32_t most = static_cast<uint32_t>(sms) * combine_ctas(A, BATCH * TOKENS);
         // whole rows of parts, so that a thread keeps its part
         ctas = std::min(ctas, std::max<uint32_t>(most / p.data.parts, 1u) * p.data.parts);
         p.step = static_cast<int64_t>(ctas / p.data.parts) * p.data.per * TOKENS;
@@ -468,12 +466,20 @@ cudaError_t launch_combine_as(CombineParams &p, int sms, cudaStream_t s)
     return launch<CombineParams>(combine_kernel<D, A, BATCH, TOKENS>, p, ctas, p.data.threads, s);
 }
 
+// Rows in flight a thread, by the places of a token: four of one token, or of two, with 64 registers; six with 80 where
+// four would leave a second batch of one or two (16384 x 4096 bf16, 6 places: 142 us, with four 154; 3 places of two
+// tokens 85.8, of one with a batch of four 89.1).  One place is best with two tokens (50.0 us; three and four spill or
+// lack threads: 50.5 to 162).
 template <int D>
 cudaError_t launch_combine(CombineParams &p, int access, int sms, cudaStream_t s)
 {
     constexpr int E = sizeof(typename Elem<D>::type);
     if (access == 16)
-        return p.top_k <= 2 ? launch_combine_as<D, 16, 2, 2>(p, sms, s) : launch_combine_as<D, 16, 4, 1>(p, sms, s);
+        return p.top_k == 1                   ? launch_combine_as<D, 16, 1, 2>(p, sms, s)
+               : p.top_k == 2                 ? launch_combine_as<D, 16, 2, 2>(p, sms, s)
+               : p.top_k == 3                 ? launch_combine_as<D, 16, 3, 2>(p, sms, s)
+               : p.top_k == 5 || p.top_k == 6 ? launch_combine_as<D, 16, 6, 1>(p, sms, s)
+                                              : launch_combine_as<D, 16, 4, 1>(p, sms, s);
     return access == 8   ? launch_combine_as<D, 8, 4, 1>(p, sms, s)
            : access == 4 ? launch_combine_as<D, 4, 4, 1>(p, sms, s)
                          : launch_combine_as<D, E, 4, 1>(p, sms, s);

@@ -56,6 +56,7 @@ SHAPES = [
     # tokens, top_k, width, rows more (or fewer) than places
     (1, 1, 1, 0), (1, 8, 4096, 0), (7, 2, 64, 5), (8, 8, 4096, 0), (33, 6, 100, 3), (130, 3, 8, 0), (513, 2, 1000, -200),
     (64, 32, 520, 7), (300, 1, 2048, 0), (5, 4, 8192, 1), (17, 5, 129, 0), (40, 7, 1032, 0), (3, 2, 16392, 0),
+    (50, 5, 256, 0), (41, 3, 512, 2), (70, 6, 64, 0), (19, 1, 264, 0), (35, 9, 128, -3),
 ]
 
 
@@ -242,6 +243,30 @@ def test_offsets_past_32_bits(cns):
     cns.run_combine_backward(r, None, x, weights=w, places=p, drows=rows)
     assert torch.equal(rows, drows)
     del buf, rows
+
+
+def test_many_tokens(cns):
+    """More tokens than the CTAs that the GPU holds take at once, in each form of a row."""
+    import torch
+    torch.manual_seed(9)
+    for t, k, width, dtype in ((200_003, 1, 8, torch.bfloat16), (70_001, 3, 72, torch.float16), (30_011, 6, 260, torch.float32),
+                               (50_021, 2, 33, torch.bfloat16)):
+        r = cns.new_route(t, 16, k, plan=False)
+        p = torch.randperm(t * k, device="cuda").to(torch.int32).view(t, k)
+        x, w = torch.randn(t, width, device="cuda").to(dtype), torch.rand(t, k, device="cuda")
+        rows = cns.run_dispatch(r, x, places=p)
+        want = torch.empty_like(rows)
+        want[p.reshape(-1).long()] = x.repeat_interleave(k, 0)
+        assert torch.equal(rows, want)
+        half = torch.finfo(dtype).eps / 2
+        y = cns.run_combine(r, rows, weights=w, places=p)
+        exact = x.double() * w.double().sum(1, keepdim=True)
+        assert ((y.double() - exact).abs() <= (half * (1 + 1e-6) + 8 * 2.0 ** -24) * exact.abs() + 2.0 ** -25).all()
+        drows, dw = cns.run_combine_backward(r, rows, x, weights=w, places=p)
+        want[p.reshape(-1).long()] = (x.repeat_interleave(k, 0).float() * w.reshape(-1, 1)).to(dtype)
+        assert torch.equal(drows, want)
+        square = x.double().square().sum(1, keepdim=True)
+        assert ((dw.double() - square).abs() <= 64 * 2.0 ** -24 * square).all()
 
 
 def busy(torch, n=12):

@@ -219,6 +219,55 @@ def test_gradient(cns, width, dtype, rows, pad, shift):
         assert none is None and torch.equal(alone, dx if gain is not None else alone)
 
 
+@pytest.mark.parametrize("rows,width,dtype", [(100_003, 40, "bf16"), (60_007, 264, "f32"), (20_011, 1000, "f16"), (9_001, 4096, "bf16"),
+                                              (30_001, 77, "bf16")])
+def test_many_rows(cns, rows, width, dtype):
+    """Rows by the tens of thousands: each CTA goes through many."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(rows)
+    x, residual, dy = (torch.randn(rows, width, generator=gen, device="cuda").to(types()[dtype]) for _ in range(3))
+    gain = torch.rand(width, generator=gen, device="cuda") + 0.5
+    n = cns.new_rms_norm(width, eps=EPS, scale_block=32)
+    h, y, q, s = cns.run_rms_norm(n, x, gain, residual=residual)
+    assert torch.equal(h, (x.float() + residual.float()).to(x.dtype))
+    h64, g = h.double(), gain.double() * dy.double()
+    r = 1 / torch.sqrt(h64.square().mean(1, keepdim=True) + EPS)
+    want = h64 * r * gain.double()
+    assert ((y.double() - want).abs() <= (41 * U + HALF[dtype] * (1 + 1e-5)) * want.abs() + TINY[dtype]).all()
+    # half a step of e4m3, 2^-4 of the value or 2^-10 of the scale
+    back = q.double() * s.double().repeat_interleave(32, 1)[:, :width]
+    assert ((back - want).abs() <= (want.abs() * 2.0 ** -4 + s.double().repeat_interleave(32, 1)[:, :width] * 2.0 ** -10) * (1 + 1e-5)).all()
+    dx, dgain = cns.run_rms_norm_backward(n, h, gain, dy, dh=residual)
+    inner = (g * h64).mean(1, keepdim=True)
+    want = residual.double() + r * g - h64 * r ** 3 * inner
+    size = residual.double().abs() + (r * g).abs() + h64.abs() * r ** 3 * (g * h64).abs().mean(1, keepdim=True)
+    assert ((dx.double() - want).abs() <= 200 * U * size + HALF[dtype] * want.abs() * (1 + 1e-5) + TINY[dtype]).all()
+    part = dy.double() * h64 * r
+    assert ((dgain.double() - part.sum(0)).abs() <= (rows + 44) * U * part.abs().sum(0)).all()
+
+
+def test_offsets_past_32_bits(cns):
+    """Rows whose distance takes their last ones past 2^32 bytes, and past 2^31 elements."""
+    import torch
+    step, rows, width = 2 ** 27 + 8, 20, 264
+    buf = torch.empty(step * rows, dtype=torch.bfloat16, device="cuda")
+    far = lambda at: buf.as_strided((rows, width), (step, 1), at * 1024)  # noqa: E731
+    x, residual, h, y, dy, dx = (far(i) for i in range(6))
+    for v in (x, residual, dy):
+        v.copy_(torch.randn(rows, width, device="cuda"))
+    near = [v.clone() for v in (x, residual, dy)]
+    gain = torch.rand(width, device="cuda") + 0.5
+    n = cns.new_rms_norm(width, scale_block=64)
+    want = cns.run_rms_norm(n, near[0], gain, residual=near[1])
+    got = cns.run_rms_norm(n, x, gain, residual=residual, h=h, y=y)
+    assert all(torch.equal(a.float(), b.float()) for a, b in zip(got, want))
+    want = cns.run_rms_norm_backward(n, want[0], gain, near[2], dh=near[1])
+    got = cns.run_rms_norm_backward(n, h, gain, dy, dh=residual, dx=dx)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del buf, x, residual, h, y, dy, dx
+
+
 def test_gradient_in_place_and_without_rows(cns):
     import torch
     torch.manual_seed(2)
