@@ -164,7 +164,8 @@ extern "C" int cns_rms_norm_backward(const cns_rms_norm_grad_t *n)
     p.dy = n->dy_dev;
     p.dh = n->dh_dev;
     p.dx = n->dx_dev;
-    p.parts = n->dgain_dev ? static_cast<float *>(n->workspace_dev) : nullptr;
+    p.dgain = n->dgain_dev;
+    p.parts = static_cast<float *>(n->workspace_dev);
     p.rows = n->rows;
     p.width = n->width;
     p.gain_dtype = n->gain_dtype;
@@ -181,7 +182,7 @@ extern "C" int cns_rms_norm_backward(const cns_rms_norm_grad_t *n)
                  : n->dtype == CNS_DT_BF16 ? launch_rms_norm_backward_bf16(p, wide, dev.sm_count, &parts, s)
                                            : launch_rms_norm_backward_f16(p, wide, dev.sm_count, &parts, s));
     }
-    if (!n->dgain_dev)
+    if (!n->dgain_dev || parts == 1)   // the only part is dgain
         return CNS_SUCCESS;
     cudaLaunchAttribute early;
     cudaLaunchConfig_t cfg = early_launch(&early);

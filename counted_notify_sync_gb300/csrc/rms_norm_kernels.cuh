@@ -50,9 +50,11 @@ struct NormGradParams {
     const void *dy;
     const void *dh;
     void *dx;
-    float *parts;   // [CTAs][width]: the CTAs' sums of dgain
+    float *dgain;   // NULL: not wanted
+    float *parts;   // [CTAs][width]: the CTAs' sums of dgain; of one CTA dgain itself
     int64_t rows, h_stride, dy_stride, dh_stride, dx_stride;
     int32_t width, gain_dtype;
+    bool joined;    // whether a grid that joins the parts follows
     float eps;
 };
 
@@ -633,8 +635,8 @@ rms_norm_backward_kernel(const __grid_constant__ NormGradParams p)
         for (int d = 0; d < kDepth; ++d)
             copy(d, row + d * step);
     }
-    if (p.parts)
-        grid_launch_dependents();   // their join, which sets up meanwhile
+    if (p.joined)
+        grid_launch_dependents();   // the join of the parts, which sets up meanwhile
     Result<T> dx;
     dx.start(p.dx, row, p.dx_stride, step);
     float2 gain[HOLD][V / 2], dgain[kRegisters ? HOLD : 1][V / 2];
@@ -752,13 +754,17 @@ rms_norm_backward_kernel(const __grid_constant__ NormGradParams p)
     }
 }
 
-// The launch of a kernel whose CTAs take `groups` rows at once: as many CTAs as the rows need (`each` of them at least
-// to a group), `most` at most.
-template <class P>
-cudaError_t launch_norm(void (*kernel)(P), const P &p, int threads, int groups, int each, int most, int smem, int *ctas, cudaStream_t s)
+// CTAs of a call whose CTAs take `groups` rows at once: as many as the rows need (`each` of them at least to a group),
+// `most` at most.
+inline int norm_ctas(int64_t rows, int groups, int each, int most)
 {
-    const int64_t per = static_cast<int64_t>(groups) * each, need = (p.rows + per - 1) / per;
-    *ctas = static_cast<int>(need < most ? need : most);
+    const int64_t per = static_cast<int64_t>(groups) * each, need = (rows + per - 1) / per;
+    return static_cast<int>(need < most ? need : most);
+}
+
+template <class P>
+cudaError_t launch_norm(void (*kernel)(P), const P &p, int threads, int ctas, int smem, cudaStream_t s)
+{
     if (smem > 47 * 1024) {   // the kernels have up to 512 bytes of their own
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem);
         if (e != cudaSuccess)
@@ -766,7 +772,7 @@ cudaError_t launch_norm(void (*kernel)(P), const P &p, int threads, int groups, 
     }
     cudaLaunchAttribute early;
     cudaLaunchConfig_t cfg = early_launch(&early);
-    cfg.gridDim = dim3(*ctas);
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -778,9 +784,8 @@ cudaError_t launch_forward_as(const NormParams &p, int sms, cudaStream_t s)
 {
     constexpr int kGroups = norm_groups(G, false), kThreads = G * kGroups, kOperands = RESIDUAL ? 2 : 1;
     constexpr int kSmem = 16 * kThreads * (WIDE ? norm_depth(WIDE, G, HOLD, kOperands) * kOperands * HOLD : 1);
-    int ctas;
-    return launch_norm<NormParams>(rms_norm_kernel<D, WIDE, G, HOLD, RESIDUAL>, p, kThreads, kGroups, 1,
-                                   sms * norm_ctas_per_sm(G, HOLD, false), kSmem, &ctas, s);
+    return launch_norm<NormParams>(rms_norm_kernel<D, WIDE, G, HOLD, RESIDUAL>, p, kThreads,
+                                   norm_ctas(p.rows, kGroups, 1, sms * norm_ctas_per_sm(G, HOLD, false)), kSmem, s);
 }
 
 template <int D, bool WIDE, int G, int HOLD>
@@ -794,8 +799,12 @@ cudaError_t launch_backward_as(const NormGradParams &p, int sms, int *parts, cud
         smem = std::max(smem, 4 * kGroups * p.width);
     const int most = std::min<int>(sms, kStepMaxCtas) * norm_ctas_per_sm(G, HOLD, true);
     static_assert(norm_ctas_per_sm(G, HOLD, true) * kStepMaxCtas <= kNormMaxParts, "room for the parts");
-    return launch_norm<NormGradParams>(rms_norm_backward_kernel<D, WIDE, G, HOLD>, p, kThreads, kGroups, kNormLeastRows, most,
-                                       smem, parts, s);
+    *parts = norm_ctas(p.rows, kGroups, kNormLeastRows, most);
+    NormGradParams with = p;
+    with.joined = p.dgain && *parts > 1;
+    if (!with.joined)
+        with.parts = p.dgain;
+    return launch_norm<NormGradParams>(rms_norm_backward_kernel<D, WIDE, G, HOLD>, with, kThreads, *parts, smem, s);
 }
 
 // Calls what(G, HOLD) for rows of `vecs` vectors.  Two vectors a thread up to 1024 (8192 columns of 16 bits), and as few

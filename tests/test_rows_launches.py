@@ -61,10 +61,11 @@ def run(tmp_path_factory):
 
 def test_one_launch_each_on_the_calls_stream(run):
     got = run("print(json.dumps([dispatch(), dispatch(scales_dev=A[5], row_scales_dev=A[6], scale_bytes=16), combine(), "
-              "combine_grad(), norm(), norm_grad(dgain_dev=None), norm_grad()]))")
+              "combine_grad(), norm(), norm_grad(dgain_dev=None), norm_grad(rows=1000), norm_grad(rows=3)]))")
     for i, (rc, calls) in enumerate(got):
         assert rc == 0
-        assert [c[0] for c in calls] == [0] * (2 if i == 6 else 1)         # the gain's gradient is joined by a second grid
+        assert [c[0] for c in calls] == [0] * (2 if i == 6 else 1)         # the gain's gradient is joined by a second grid,
+        # where more than one CTA has a part of it
         assert all(c[4] == 0x50 for c in calls)
 
 
@@ -78,7 +79,7 @@ def test_nothing_to_do_launches_nothing(run):
 
 
 def test_a_refused_launch_is_reported(run):
-    got = run("print(json.dumps([dispatch(1), combine(1), combine_grad(1), norm(1), norm_grad(1), norm_grad(2)]))")
+    got = run("print(json.dumps([dispatch(1), combine(1), combine_grad(1), norm(1), norm_grad(1, rows=1000), norm_grad(2, rows=1000)]))")
     assert all(rc != 0 for rc, _ in got)
     assert [len(calls) for _, calls in got] == [1, 1, 1, 1, 1, 2]          # no join of parts that are not there
 
