@@ -331,10 +331,10 @@ __device__ __forceinline__ float lanes_sums(float *v)
     return sum;
 }
 
-// LANES threads take a token: of a warp (8, 16 or 32), or the CTA (0).  A thread has HELD accesses of dy at a time, 32
+// LANES threads take a token: of a warp (4, 8, 16 or 32), or the CTA (0).  A thread has HELD accesses of dy at a time, 32
 // apart (LANES, where fewer); the rows of BATCH places are in flight together, and while dy is in registers each row's
 // gradient is written and its product summed: one pass.  16384 x 4096 bf16, 8 places: 328 us, 103 % of the copy rate;
-// 65536 x 256, 4 places: 58.6 us (77 %), 65536 x 64, 8 places: 29.3 us (75 %; the sums' exchanges), 8192 x 2049, 4 places:
+// 65536 x 256, 4 places: 49.7 us (91 %), 65536 x 64, 8 places: 27.3 us (80 %; the sums' exchanges), 8192 x 2049, 4 places:
 // 89.7 us (50 %; instructions).
 template <int D, int A, int LANES, int HELD, int BATCH>
 __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __grid_constant__ CombineGradParams p)
@@ -494,16 +494,18 @@ cudaError_t launch_grad_as(const CombineGradParams &p, cudaStream_t s)
                                      static_cast<uint32_t>((p.tokens + per - 1) / per), threads, s);
 }
 
-// A token's lanes: enough for the row's accesses, so that few idle and few sums meet in shared memory.
+// A token's lanes: enough for the row's accesses, two each, so that few idle, few exchanges are left and few sums meet in
+// shared memory.  One access a lane, or four rows at once: 65536 x 256, 4 places, 58.4 and 53.0 us against 49.7; the CTA's
+// four rows at once 371 us against 328 at 16384 x 4096.
 template <int D>
 cudaError_t launch_combine_backward(const CombineGradParams &p, int access, cudaStream_t s)
 {
     constexpr int E = sizeof(typename Elem<D>::type);
     if (access == 16)
-        return p.units <= 8    ? launch_grad_as<D, 16, 8, 1, 4>(p, s)
-               : p.units <= 16 ? launch_grad_as<D, 16, 16, 1, 4>(p, s)
-               : p.units <= 32 ? launch_grad_as<D, 16, 32, 1, 4>(p, s)
-               : p.units <= 64 ? launch_grad_as<D, 16, 32, 2, 4>(p, s)
+        return p.units <= 8    ? launch_grad_as<D, 16, 4, 2, 2>(p, s)
+               : p.units <= 16 ? launch_grad_as<D, 16, 8, 2, 2>(p, s)
+               : p.units <= 32 ? launch_grad_as<D, 16, 16, 2, 2>(p, s)
+               : p.units <= 64 ? launch_grad_as<D, 16, 32, 2, 2>(p, s)
                                : launch_grad_as<D, 16, 0, 2, 2>(p, s);
     const auto narrow = [&](auto bytes) {
         constexpr int A = bytes();
