@@ -53,11 +53,11 @@ int64_t bytes_of(int32_t dtype) { return dtype == CNS_DT_F32 ? 4 : 2; }
 
 bool off(const void *p, int64_t bytes) { return address(p) % bytes != 0; }
 
-// A matrix's stride (`packed` where it is 0); false if it is too small or not to be counted in bytes.
+// A matrix's stride (`packed` where it is 0); false if it is out of range.
 bool stride_ok(int64_t given, int64_t packed, int64_t *stride)
 {
     *stride = given ? given : packed;
-    return *stride >= packed && *stride <= (INT64_MAX >> 34);
+    return *stride >= packed && *stride <= CNS_ROWS_MAX_STRIDE;
 }
 
 }  // namespace

@@ -902,7 +902,7 @@ int cns_combine(const cns_combine_t *c);
 /* Combine's gradient: drows[places[t][j]] = weights[t][j] * dy[t], the product
  * in 32 bits, rounded once; dweights[t][j] = the sum over the columns of
  * dy[t] * rows[places[t][j]] in 32 bits, in an order that depends on the width
- * alone, 0 for a place without a row.  The base's gradient is dy itself. */
+ * and the rows' alignment alone, 0 for a place without a row.  The base's gradient is dy itself. */
 typedef struct {
     const void *rows_dev;       /* (in) [rows][width], the forward call's; NULL without dweights_dev */
     const void *dy_dev;         /* (in) [tokens][width] */
@@ -960,7 +960,8 @@ typedef struct {
     void *scales_dev;          /* (out) [rows][blocks] of scale_type; NULL if q_dev is */
     cns_stream_t stream;       /* (in) */
     int64_t rows;              /* (in) >= 0 */
-    int64_t x_stride;          /* (in) elements from row to row, >= width; 0 = width (scales_stride: blocks) */
+    int64_t x_stride;          /* (in) elements from row to row, width .. CNS_ROWS_MAX_STRIDE; 0 = width
+                                  (scales_stride: blocks) */
     int64_t residual_stride;   /* (in) */
     int64_t h_stride;          /* (in) */
     int64_t y_stride;          /* (in) */
@@ -984,7 +985,7 @@ int cns_rms_norm(const cns_rms_norm_t *n);
  *   dx = dh + r * g - h * r^3 * mean of (g * h),  g = gain * dy,
  * in 32 bits, rounded once; it is the residual's gradient too; and
  *   dgain = sum over the rows of dy * h * r, in 32 bits, in an order that
- * depends on the sizes alone. */
+ * depends on the sizes and the rows' alignment alone. */
 typedef struct {
     const void *h_dev;         /* (in) [rows][width], the forward call's h (its x without a residual) */
     const void *gain_dev;      /* (in, optional) */
@@ -997,7 +998,7 @@ typedef struct {
     uint64_t workspace_bytes;  /* (in) >= cns_rms_norm_workspace_bytes */
     cns_stream_t stream;       /* (in) */
     int64_t rows;              /* (in) >= 0 */
-    int64_t h_stride;          /* (in) elements from row to row, >= width; 0 = width */
+    int64_t h_stride;          /* (in) elements from row to row, width .. CNS_ROWS_MAX_STRIDE; 0 = width */
     int64_t dy_stride;         /* (in) */
     int64_t dh_stride;         /* (in) */
     int64_t dx_stride;         /* (in) */

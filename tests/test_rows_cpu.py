@@ -182,7 +182,8 @@ NORM = dict(x_dev=0x10000, residual_dev=0x20000, gain_dev=0x30000, h_dev=0x40000
     (dict(width=cns.CNS_NORM_MAX_WIDTH + 1), INVALID), (dict(dtype=3), INVALID), (dict(gain_dtype=-1), INVALID),
     (dict(scale_block=16), INVALID), (dict(scale_block=256), INVALID), (dict(scale_block=-1), INVALID),
     (dict(scale_type=2), INVALID), (dict(eps=-1e-6), INVALID), (dict(eps=float("nan")), INVALID),
-    (dict(eps=float("inf")), INVALID), (dict(x_stride=255), INVALID), (dict(residual_stride=1), INVALID),
+    (dict(eps=float("inf")), INVALID), (dict(x_stride=255), INVALID),
+    (dict(x_stride=cns.CNS_ROWS_MAX_STRIDE + 1), INVALID), (dict(residual_stride=1), INVALID),
     (dict(h_stride=255), INVALID), (dict(y_stride=255), INVALID), (dict(q_stride=255), INVALID),
     (dict(scales_stride=1), INVALID), (dict(x_dev=0x10001), INVALID), (dict(gain_dev=0x30002), INVALID),
     (dict(scales_dev=0x70001), INVALID), (dict(y_dev=0x10000), INVALID), (dict(y_dev=0x20000), INVALID),
