@@ -218,6 +218,9 @@ def new_route(tokens: int, experts: int, top_k: int, *, score: int = _native.CNS
         r.workspace = new_step_workspace(nbytes, device, stream)
     r.capacity, r.index, r.others = tokens, r.ids.get_device(), torch.cuda.device_count() > 1
     r.types = (torch.int32, torch.float32)
+    r.call_dispatch = _native.packed_call("cns_dispatch", _native.Dispatch)
+    r.call_combine = _native.packed_call("cns_combine", _native.Combine)
+    r.call_combine_backward = _native.packed_call("cns_combine_backward", _native.CombineGrad)
     b = r.backward = _native.RouteGrad()   # run_route_backward's, but for the call's own tensors
     b.experts, b.top_k, b.score, b.renorm, b.scale = experts, top_k, score, int(renorm), scale
     r.ids_dev, r.weights_dev, r.scores_dev = _native.ptr(r.ids), _native.ptr(r.weights), _native.ptr(r.scores)
@@ -278,7 +281,7 @@ def _empty_on(stream, like, shape, dtype=None):
     still be using, which comes before that stream's work alone."""
     import torch
     handle = _native.stream_handle(stream) or 0
-    if torch.cuda.current_stream().cuda_stream == handle:
+    if torch._C._cuda_getCurrentRawStream(like.get_device()) == handle:   # (a Stream object takes some us)
         return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()):
         return like.new_empty(shape, dtype=dtype)
@@ -321,6 +324,10 @@ def run_route_backward(route, logits, dweights, *, ids=None, dscores=None, dlogi
     return dlogits
 
 
+# The calls below check their tensors in place where these are as most are (dense, of the shape, type and device
+# expected), and ask a function about the others: with that and packed arguments a combine takes the host 4.6 us, where a
+# function for each tensor and a structure filled in took 6.6.
+
 def _matrix(x, name, index, shape, dtype):
     """Elements from row to row (0: packed) of a matrix."""
     if x.shape == shape and x.dtype is dtype and x.get_device() == index:
@@ -329,7 +336,7 @@ def _matrix(x, name, index, shape, dtype):
         (rows, cols), (step, one) = shape, x.stride()
         if (one == 1 or cols == 1) and (step >= cols or rows <= 1):
             return step if rows > 1 else 0
-    raise ValueError(f"{name}: {shape} {dtype} on CUDA device {index}, rows apart and of unit stride, expected; got "
+    raise ValueError(f"{name}: {tuple(shape)} {dtype} on CUDA device {index}, rows apart and of unit stride, expected; got "
                      f"{tuple(x.shape)} {x.dtype}, strides {x.stride()}, on {x.device}")
 
 
@@ -370,20 +377,25 @@ def run_dispatch(route, x, *, places=None, rows=None, scales=None, row_scales=No
     were, in a new tensor whatever its memory held.  With `scales` [tokens, n], of any type, row_scales[places[t, j]] =
     scales[t] too.  Returns rows, with scales (rows, row_scales), no part of torch's graph: run_dispatch_backward has the
     gradient."""
-    if route.others:
-        _check_current(route.index)
     index, shape, dtype, size, top_k = route.index, x.shape, x.dtype, x.element_size(), route.top_k
+    if route.others:
+        _check_current(index)
     t, width = shape
-    x_step, places_at = _matrix(x, "x", index, shape, dtype) * size, _places(route, places, t)
+    x_step = 0 if x.is_contiguous() and x.get_device() == index else _matrix(x, "x", index, shape, dtype) * size
+    if places is not None and (places.shape == (t, top_k) and places.dtype is route.types[0] and
+                               places.get_device() == index and places.is_contiguous()):
+        places_at = places.data_ptr()
+    else:
+        places_at = _places(route, places, t)
     if rows is None:
         n, rows_step, rows = t * top_k, 0, _empty_on(stream, x, (t * top_k, width))
     else:
-        n = len(rows)
-        rows_step = _matrix(rows, "rows", index, (n, width), dtype) * size
+        n = rows.shape[0]
+        rows_step = 0 if (rows.shape == (n, width) and rows.dtype is dtype and rows.get_device() == index and
+                          rows.is_contiguous()) else _matrix(rows, "rows", index, (n, width), dtype) * size
     each = scales_at = row_scales_at = scales_step = row_scales_step = 0
     if scales is not None:
-        shape, kind, each = scales.shape, scales.dtype, scales.element_size()
-        cols = shape[-1]
+        kind, each, cols = scales.dtype, scales.element_size(), scales.shape[-1]
         scales_step = _matrix(scales, "scales", index, (t, cols), kind) * each
         if row_scales is None:
             row_scales = _empty_on(stream, scales, (n, cols))
@@ -391,49 +403,62 @@ def run_dispatch(route, x, *, places=None, rows=None, scales=None, row_scales=No
         scales_at, row_scales_at, each = scales.data_ptr(), row_scales.data_ptr(), cols * each
     elif row_scales is not None:
         raise ValueError("row_scales without scales")
-    rc = _native.cns_dispatch(_native.make_dispatch(
-        x.data_ptr(), rows.data_ptr(), scales_at, row_scales_at, places_at, _native.stream_handle(stream) or 0, t, n,
-        width * size, each, x_step, rows_step, scales_step, row_scales_step, top_k, 0))
+    call, pack = route.call_dispatch
+    rc = call(pack(x.data_ptr(), rows.data_ptr(), scales_at, row_scales_at, places_at,
+                   0 if stream is None else _native.stream_handle(stream), t, n, width * size, each, x_step, rows_step,
+                   scales_step, row_scales_step, top_k, 0))
     if rc:
         raise _native.CnsError(rc, "cns_dispatch")
     return rows if scales is None else (rows, row_scales)
 
 
-def _combine(route, rows, t, weights_at, places, base, y, stream, what):
-    """cns_combine for `t` tokens; `what` names the rows and the result in errors."""
+def _combine(route, rows, weighted, weights, places, base, y, stream, what):
+    """cns_combine, with weights or without; `what` names the rows and the result in errors."""
+    index, shape, dtype, top_k, (i32, f32) = route.index, rows.shape, rows.dtype, route.top_k, route.types
     if route.others:
-        _check_current(route.index)
-    index, shape, dtype, top_k = route.index, rows.shape, rows.dtype, route.top_k
+        _check_current(index)
+    code = _CODES.get(dtype)
+    if code is None:
+        code = _dtype_code(dtype)
     n, width = shape
-    code, rows_step, places_at = _dtype_code(dtype), _matrix(rows, what[0], index, shape, dtype), _places(route, places, t)
-    base_at = base_step = y_step = 0
-    if base is not None:
-        base_at, base_step = base.data_ptr(), _matrix(base, "base", index, (t, width), dtype)
-    if y is None:
-        y = _empty_on(stream, rows, (t, width))
+    rows_step = 0 if rows.is_contiguous() and rows.get_device() == index else _matrix(rows, what[0], index, shape, dtype)
+    first = y if y is not None else base if base is not None else places
+    t = route.tokens if first is None else first.shape[0]
+    shape, per = (t, width), (t, top_k)
+    weights_at = base_at = base_step = y_step = 0
+    if weighted:
+        if weights is not None and (weights.shape == per and weights.dtype is f32 and weights.get_device() == index and
+                                    weights.is_contiguous()):
+            weights_at = weights.data_ptr()
+        else:
+            weights_at = _weights(route, weights, places, t)
+    if places is not None and (places.shape == per and places.dtype is i32 and places.get_device() == index and
+                               places.is_contiguous()):
+        places_at = places.data_ptr()
     else:
-        y_step = _matrix(y, what[1], index, (t, width), dtype)
-    rc = _native.cns_combine(_native.make_combine(
-        rows.data_ptr(), places_at, weights_at, base_at, y.data_ptr(), _native.stream_handle(stream) or 0, t, n, rows_step,
-        base_step, y_step, width, top_k, code, 0))
+        places_at = _places(route, places, t)
+    if base is not None:
+        base_at = base.data_ptr()
+        base_step = 0 if (base.shape == shape and base.dtype is dtype and base.get_device() == index and
+                          base.is_contiguous()) else _matrix(base, "base", index, shape, dtype)
+    if y is None:
+        y = _empty_on(stream, rows, shape)
+    elif not (y.shape == shape and y.dtype is dtype and y.get_device() == index and y.is_contiguous()):
+        y_step = _matrix(y, what[1], index, shape, dtype)
+    call, pack = route.call_combine
+    rc = call(pack(rows.data_ptr(), places_at, weights_at, base_at, y.data_ptr(),
+                   0 if stream is None else _native.stream_handle(stream), t, n, rows_step, base_step, y_step, width, top_k,
+                   code, 0))
     if rc:
         raise _native.CnsError(rc, "cns_combine")
     return y
-
-
-def _tokens(route, places, first, second):
-    """How many tokens a call is for: those of the first tensor given, else of the places."""
-    for x in (first, second, places):
-        if x is not None:
-            return len(x)
-    return route.tokens
 
 
 def run_dispatch_backward(route, drows, *, places=None, dx=None, stream=None):
     """dL/dx of run_dispatch from dL/drows (float32, bfloat16 or float16): dx[t] = the sum over j of
     drows[places[t, j]], in 32 bits, rounded once.  For the tokens of `dx` (default: a new tensor for those of
     `places`, or of run_route's last call)."""
-    return _combine(route, drows, _tokens(route, places, dx, None), 0, places, None, dx, stream, ("drows", "dx"))
+    return _combine(route, drows, False, None, places, None, dx, stream, ("drows", "dx"))
 
 
 def run_combine(route, rows, *, weights=None, places=None, base=None, y=None, stream=None):
@@ -441,8 +466,7 @@ def run_combine(route, rows, *, weights=None, places=None, base=None, y=None, st
     bits, rounded once, for rows [any number, width] in float32, bfloat16 or float16.  `weights` [tokens, top_k] float32
     and `places` default to those of run_route's last call; `base` [tokens, width] (the residual, say) is optional.  The
     result goes to `y` [tokens, width] (default: a new tensor, of `stream`'s memory), which may be `base`."""
-    t = _tokens(route, places, y, base)
-    return _combine(route, rows, t, _weights(route, weights, places, t), places, base, y, stream, ("rows", "y"))
+    return _combine(route, rows, True, weights, places, base, y, stream, ("rows", "y"))
 
 
 def run_combine_backward(route, rows, dy, *, weights=None, places=None, drows=None, dweights=None, stream=None):
@@ -450,37 +474,56 @@ def run_combine_backward(route, rows, dy, *, weights=None, places=None, drows=No
     dy[t], and dweights[t, j] = dy[t] . rows[places[t, j]], 0 for a place without a row.  `drows` (default: a new tensor
     like rows): what no place names stays as it was.  `rows` None: no dweights (None is returned); `drows` False: no
     drows.  The base's gradient is dy."""
+    index, shape, dtype, top_k, (i32, f32) = route.index, dy.shape, dy.dtype, route.top_k, route.types
     if route.others:
-        _check_current(route.index)
-    index, shape, dtype, top_k = route.index, dy.shape, dy.dtype, route.top_k
+        _check_current(index)
+    code = _CODES.get(dtype)
+    if code is None:
+        code = _dtype_code(dtype)
     t, width = shape
-    code, dy_step = _dtype_code(dtype), _matrix(dy, "dy", index, shape, dtype)
-    weights_at, places_at = _weights(route, weights, places, t), _places(route, places, t)
+    dy_step = 0 if dy.is_contiguous() and dy.get_device() == index else _matrix(dy, "dy", index, shape, dtype)
+    per = (t, top_k)
+    if weights is not None and (weights.shape == per and weights.dtype is f32 and weights.get_device() == index and
+                                weights.is_contiguous()):
+        weights_at = weights.data_ptr()
+    else:
+        weights_at = _weights(route, weights, places, t)
+    if places is not None and (places.shape == per and places.dtype is i32 and places.get_device() == index and
+                               places.is_contiguous()):
+        places_at = places.data_ptr()
+    else:
+        places_at = _places(route, places, t)
     n, rows_at, rows_step, dweights_at = t * top_k, 0, 0, 0
     if rows is not None:
-        n = len(rows)
-        rows_step, rows_at = _matrix(rows, "rows", index, (n, width), dtype), rows.data_ptr()
+        n, rows_at = rows.shape[0], rows.data_ptr()
+        rows_step = 0 if (rows.shape == (n, width) and rows.dtype is dtype and rows.get_device() == index and
+                          rows.is_contiguous()) else _matrix(rows, "rows", index, (n, width), dtype)
         if dweights is None:
-            dweights = _empty_on(stream, dy, (t, top_k), route.types[1])
+            dweights = _empty_on(stream, dy, per, f32)
+            dweights_at = dweights.data_ptr()
+        elif (dweights.shape == per and dweights.dtype is f32 and dweights.get_device() == index and
+              dweights.is_contiguous()):
             dweights_at = dweights.data_ptr()
         else:
-            dweights_at = _per_place(route, dweights, "dweights", t, route.types[1])
+            dweights_at = _per_place(route, dweights, "dweights", t, f32)
     elif dweights is not None:
         raise ValueError("dweights without rows")
     elif drows is not None and drows is not False:
-        n = len(drows)
+        n = drows.shape[0]
     drows_at = drows_step = 0
     if drows is False:
         drows = None
     else:
         if drows is None:
             drows = _empty_on(stream, dy, (n, width))
-        else:
+        elif not (drows.shape == (n, width) and drows.dtype is dtype and drows.get_device() == index and
+                  drows.is_contiguous()):
             drows_step = _matrix(drows, "drows", index, (n, width), dtype)
         drows_at = drows.data_ptr()
-    rc = _native.cns_combine_backward(_native.make_combine_grad(
-        rows_at, dy.data_ptr(), places_at, weights_at, drows_at, dweights_at, _native.stream_handle(stream) or 0, t, n,
-        rows_step, dy_step, drows_step, width, top_k, code, 0))
+    call, pack = route.call_combine_backward
+    rc = call(pack(rows_at, dy.data_ptr(), places_at, weights_at, drows_at, dweights_at,
+                   0 if stream is None else _native.stream_handle(stream), t, n, rows_step, dy_step, drows_step, width, top_k,
+                   code, 0))
     if rc:
         raise _native.CnsError(rc, "cns_combine_backward")
     return drows, dweights
@@ -507,6 +550,8 @@ def new_rms_norm(width: int, *, eps: float = 1e-6, y: bool = True, scale_block: 
     n.index = torch.cuda.current_device() if device.index is None else device.index
     n.others = torch.cuda.device_count() > 1
     n.has_y, n.has_q = y, scale_block is not None
+    n.call = _native.packed_call("cns_rms_norm", _native.RmsNorm)
+    n.call_backward = _native.packed_call("cns_rms_norm_backward", _native.RmsNormGrad)
     n.blocks = -(-width // scale_block) if scale_block else 1
     n.types = (torch.float8_e4m3fn, torch.float8_e8m0fnu if scale_type == _native.CNS_SCALE_E8M0 else torch.float32,
                torch.float32)
@@ -516,8 +561,6 @@ def new_rms_norm(width: int, *, eps: float = 1e-6, y: bool = True, scale_block: 
 
 def _gain(norm, gain):
     """(address, cns_dtype_t) of a norm's gain."""
-    if gain is None:
-        return 0, 0
     if not (gain.is_contiguous() and gain.numel() == norm.width and gain.get_device() == norm.index):
         raise ValueError(f"gain: contiguous [{norm.width}] on CUDA device {norm.index} expected")
     return gain.data_ptr(), _dtype_code(gain.dtype)
@@ -529,16 +572,25 @@ def run_rms_norm(norm, x, gain=None, *, residual=None, h=None, y=None, q=None, s
     Returns (h, y, q, scales): h is x without a residual, and what the norm does not have is None.  The results go to
     the tensors given (h may be x or residual), or to new ones, of `stream`'s memory.  They are no part of torch's graph:
     run_rms_norm_backward has the gradient."""
-    index, shape, dtype = norm.index, (len(x), norm.width), x.dtype
+    index, dtype, width = norm.index, x.dtype, norm.width
     if norm.others:
         _check_current(index)
-    code, x_step, (gain_at, gain_code) = _dtype_code(dtype), _matrix(x, "x", index, shape, dtype), _gain(norm, gain)
+    code = _CODES.get(dtype)
+    if code is None:
+        code = _dtype_code(dtype)
+    t = x.shape[0]
+    shape = (t, width)
+    x_step = 0 if x.shape == shape and x.get_device() == index and x.is_contiguous() else _matrix(x, "x", index, shape, dtype)
+    gain_at, gain_code = (0, 0) if gain is None else _gain(norm, gain)
     residual_at = residual_step = h_at = h_step = y_at = y_step = q_at = q_step = scales_at = scales_step = 0
     if residual is not None:
-        residual_step, residual_at = _matrix(residual, "residual", index, shape, dtype), residual.data_ptr()
+        residual_at = residual.data_ptr()
+        if not (residual.shape == shape and residual.dtype is dtype and residual.get_device() == index and
+                residual.is_contiguous()):
+            residual_step = _matrix(residual, "residual", index, shape, dtype)
         if h is None:
             h = _empty_on(stream, x, shape)
-        else:
+        elif not (h.shape == shape and h.dtype is dtype and h.get_device() == index and h.is_contiguous()):
             h_step = _matrix(h, "h", index, shape, dtype)
         h_at = h.data_ptr()
     elif h is not None:
@@ -548,28 +600,29 @@ def run_rms_norm(norm, x, gain=None, *, residual=None, h=None, y=None, q=None, s
     if norm.has_y:
         if y is None:
             y = _empty_on(stream, x, shape)
-        else:
+        elif not (y.shape == shape and y.dtype is dtype and y.get_device() == index and y.is_contiguous()):
             y_step = _matrix(y, "y", index, shape, dtype)
         y_at = y.data_ptr()
     elif y is not None:
         raise ValueError("y: this norm has none")
     if norm.has_q:
-        (e4m3, kind, _), blocks = norm.types, (shape[0], norm.blocks)
+        (e4m3, kind, _), blocks = norm.types, (t, norm.blocks)
         if q is None:
             q = _empty_on(stream, x, shape, e4m3)
-        else:
+        elif not (q.shape == shape and q.dtype is e4m3 and q.get_device() == index and q.is_contiguous()):
             q_step = _matrix(q, "q", index, shape, e4m3)
         if scales is None:
             scales = _empty_on(stream, x, blocks, kind)
-        else:
+        elif not (scales.shape == blocks and scales.dtype is kind and scales.get_device() == index and
+                  scales.is_contiguous()):
             scales_step = _matrix(scales, "scales", index, blocks, kind)
         q_at, scales_at = q.data_ptr(), scales.data_ptr()
     elif q is not None or scales is not None:
         raise ValueError("q, scales: this norm has none")
-    rc = _native.cns_rms_norm(_native.make_rms_norm(
-        x.data_ptr(), residual_at, gain_at, h_at, y_at, q_at, scales_at, _native.stream_handle(stream) or 0, shape[0], x_step,
-        residual_step, h_step, y_step, q_step, scales_step, shape[1], code, gain_code, norm.scale_block, norm.scale_type,
-        norm.eps))
+    call, pack = norm.call
+    rc = call(pack(x.data_ptr(), residual_at, gain_at, h_at, y_at, q_at, scales_at,
+                   0 if stream is None else _native.stream_handle(stream), t, x_step, residual_step, h_step, y_step, q_step,
+                   scales_step, width, code, gain_code, norm.scale_block, norm.scale_type, norm.eps))
     if rc:
         raise _native.CnsError(rc, "cns_rms_norm")
     return h, y, q, scales
@@ -581,22 +634,30 @@ def run_rms_norm_backward(norm, h, gain, dy, *, dh=None, dx=None, dgain=None, wo
     may be dy or dh) and `dgain`, or to new tensors; without a gain, or with dgain False, dgain is None.  `workspace`:
     any tensor of cns_rms_norm_workspace_bytes that no other call uses meanwhile (default: a new one, of `stream`'s
     memory)."""
-    index, shape, dtype = norm.index, (len(h), norm.width), h.dtype
+    index, dtype, width = norm.index, h.dtype, norm.width
     if norm.others:
         _check_current(index)
-    code, (gain_at, gain_code) = _dtype_code(dtype), _gain(norm, gain)
-    h_step, dy_step = _matrix(h, "h", index, shape, dtype), _matrix(dy, "dy", index, shape, dtype)
+    code = _CODES.get(dtype)
+    if code is None:
+        code = _dtype_code(dtype)
+    t = h.shape[0]
+    shape = (t, width)
+    gain_at, gain_code = (0, 0) if gain is None else _gain(norm, gain)
+    h_step = 0 if h.shape == shape and h.get_device() == index and h.is_contiguous() else _matrix(h, "h", index, shape, dtype)
+    dy_step = 0 if (dy.shape == shape and dy.dtype is dtype and dy.get_device() == index and
+                    dy.is_contiguous()) else _matrix(dy, "dy", index, shape, dtype)
     dh_at = dh_step = dx_step = dgain_at = workspace_at = nbytes = 0
     if dh is not None:
-        dh_step, dh_at = _matrix(dh, "dh", index, shape, dtype), dh.data_ptr()
+        dh_at = dh.data_ptr()
+        if not (dh.shape == shape and dh.dtype is dtype and dh.get_device() == index and dh.is_contiguous()):
+            dh_step = _matrix(dh, "dh", index, shape, dtype)
     if dx is None:
         dx = _empty_on(stream, h, shape)
-    else:
+    elif not (dx.shape == shape and dx.dtype is dtype and dx.get_device() == index and dx.is_contiguous()):
         dx_step = _matrix(dx, "dx", index, shape, dtype)
     if dgain is False or (dgain is None and gain is None):
         dgain = None
     else:
-        t, width = shape
         f32 = norm.types[2]
         if dgain is None:
             dgain = _empty_on(stream, h, (width,), f32)
@@ -607,13 +668,14 @@ def run_rms_norm_backward(norm, h, gain, dy, *, dh=None, dx=None, dgain=None, wo
             _native.check(rc, "cns_rms_norm_workspace_bytes")
             workspace = _empty_on(stream, h, (nbytes // 4,), f32)
         elif workspace.is_contiguous() and workspace.get_device() == index:
-            nbytes = workspace.numel() * workspace.element_size()
+            nbytes = workspace.nbytes
         else:
             raise ValueError(f"workspace: contiguous, on CUDA device {index} expected")
         dgain_at, workspace_at = dgain.data_ptr(), workspace.data_ptr()
-    rc = _native.cns_rms_norm_backward(_native.make_rms_norm_grad(
-        h.data_ptr(), gain_at, dy.data_ptr(), dh_at, dx.data_ptr(), dgain_at, workspace_at, nbytes,
-        _native.stream_handle(stream) or 0, shape[0], h_step, dy_step, dh_step, dx_step, shape[1], code, gain_code, norm.eps))
+    call, pack = norm.call_backward
+    rc = call(pack(h.data_ptr(), gain_at, dy.data_ptr(), dh_at, dx.data_ptr(), dgain_at, workspace_at, nbytes,
+                   0 if stream is None else _native.stream_handle(stream), t, h_step, dy_step, dh_step, dx_step, width, code,
+                   gain_code, norm.eps))
     if rc:
         raise _native.CnsError(rc, "cns_rms_norm_backward")
     return dx, dgain

@@ -202,19 +202,6 @@ class RmsNormGrad(Structure):
     ]
 
 
-def _packer(cls):
-    """A function that makes a structure of `cls` of values for all its fields, in their order (addresses as integers,
-    0 for none): a third of the time of setting them one by one."""
-    codes = {c_void_p: "Q", c_uint64: "Q", c_int64: "q", c_int32: "i", c_uint32: "I", c_float: "f"}
-    pack, make = struct.Struct("=" + "".join(codes[t] for _, t in cls._fields_)).pack, cls.from_buffer_copy
-    assert struct.calcsize("=" + "".join(codes[t] for _, t in cls._fields_)) == ctypes.sizeof(cls)   # no padding
-    return lambda *values: make(pack(*values))
-
-
-make_dispatch, make_combine, make_combine_grad = _packer(Dispatch), _packer(Combine), _packer(CombineGrad)
-make_rms_norm, make_rms_norm_grad = _packer(RmsNorm), _packer(RmsNormGrad)
-
-
 class Tensor(Structure):
     _fields_ = [("data_dev", c_void_p), ("elems", c_int64), ("dtype", c_int32), ("reserved", c_int32)]
 
@@ -293,6 +280,22 @@ def lib() -> ctypes.CDLL:
                 fn.argtypes = args
             _lib = L
     return _lib
+
+
+_packed = {}
+
+
+def packed_call(name: str, cls):
+    """(call, pack): call(pack(*values)) is entry point `name` with a `cls` of these values for all its fields, in their
+    order (addresses as integers, 0 for none), and returns its code: for calls whose host time counts, which filling in a
+    structure field by field adds to."""
+    got = _packed.get(name)
+    if got is None:
+        codes = {c_void_p: "Q", c_uint64: "Q", c_int64: "q", c_int32: "i", c_uint32: "I", c_float: "f"}
+        form = struct.Struct("=" + "".join(codes[t] for _, t in cls._fields_))
+        assert form.size == ctypes.sizeof(cls), "padding"
+        got = _packed[name] = ctypes.CFUNCTYPE(c_int, c_char_p)((name, lib())), form.pack
+    return got
 
 
 def exported_names():

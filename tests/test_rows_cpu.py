@@ -2,6 +2,7 @@
 rows and by differences, the entry points' refusals, which come before any CUDA call, and the Python side's."""
 import ctypes
 import os
+import struct
 import subprocess
 
 import numpy as np
@@ -243,8 +244,15 @@ def handles(monkeypatch):
     n.index, n.others, n.has_y, n.has_q, n.blocks = -1, True, True, False, 1
     n.types = (torch.float8_e4m3fn, torch.float32, torch.float32)
     calls = []
-    for name in ("cns_dispatch", "cns_combine", "cns_combine_backward", "cns_rms_norm", "cns_rms_norm_backward"):
-        monkeypatch.setattr(_native, name, lambda s, name=name: calls.append((name, s)) or 0)
+
+    def entry(name, kind):
+        form = struct.Struct("=" + "".join({ctypes.c_void_p: "Q", ctypes.c_uint64: "Q", ctypes.c_int64: "q", ctypes.c_int32: "i",
+                                            ctypes.c_float: "f"}[t] for _, t in kind._fields_))
+        return lambda b: calls.append((name, kind.from_buffer_copy(b))) or 0, form.pack
+
+    r.call_dispatch, r.call_combine = entry("cns_dispatch", _native.Dispatch), entry("cns_combine", _native.Combine)
+    r.call_combine_backward = entry("cns_combine_backward", _native.CombineGrad)
+    n.call, n.call_backward = entry("cns_rms_norm", _native.RmsNorm), entry("cns_rms_norm_backward", _native.RmsNormGrad)
     return r, n, calls
 
 
@@ -291,6 +299,22 @@ def test_arguments_that_python_refuses(handles):
     assert not calls
 
 
+def test_packed_calls_reach_the_entry_points(built):
+    """The packed form has the structure's layout, and its answer is the entry point's."""
+    for name, kind, good in (("cns_dispatch", _native.Dispatch, DISPATCH), ("cns_combine", _native.Combine, COMBINE),
+                             ("cns_combine_backward", _native.CombineGrad, COMBINE_GRAD), ("cns_rms_norm", _native.RmsNorm, NORM),
+                             ("cns_rms_norm_backward", _native.RmsNormGrad, NORM_GRAD)):
+        call, pack = _native.packed_call(name, kind)
+        values = [good.get(f, 0) for f, _ in kind._fields_]
+        packed = kind.from_buffer_copy(pack(*values))
+        for (f, t), v in zip(kind._fields_, values):
+            assert (getattr(packed, f) or 0) == (ctypes.c_float(v).value if t is ctypes.c_float else v), f
+        whole = kind(*[v if t is not ctypes.c_void_p else v or None for (_, t), v in zip(kind._fields_, values)])
+        assert call(pack(*values)) == getattr(cns, name)(whole)
+        bad = [-1 if f in ("tokens", "rows") else v for (f, _), v in zip(kind._fields_, values)]
+        assert call(pack(*bad)) == INVALID
+
+
 def test_calls_of_another_device_are_refused(handles, monkeypatch):
     import torch
     r, n, calls = handles
@@ -302,7 +326,6 @@ def test_calls_of_another_device_are_refused(handles, monkeypatch):
         call()
     assert [c[0] for c in calls] == ["cns_dispatch", "cns_combine", "cns_combine", "cns_combine_backward", "cns_rms_norm",
                                      "cns_rms_norm_backward"]
-    assert len({ctypes.addressof(c[1]) for c in calls}) == len(calls)      # each call's arguments are its own
     assert calls[1][1].weights_dev is None and calls[2][1].weights_dev == r.weights.data_ptr()
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     for call in good:
