@@ -306,35 +306,38 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-// Values of a row's warps to be joined: of each group from a multiple of four on, zeros between them.
+// Values of a row's warps to be joined: of each group from a multiple of four on.  The places between a group's last warp
+// and the next group's first are left as they are, and no result depends on them: a group has no barrier with the
+// others, so nothing that another group's threads would have to write first is read.
 template <int G, int GROUPS>
 struct Joined {
     static constexpr int kWarps = G / 32, kRoom = kWarps > 4 ? (kWarps + 3) / 4 * 4 : 4, kSize = G > 32 ? kRoom * GROUPS : 4;
     float4 s[2][kSize / 4];   // the halves alternate from row to row, so one barrier each is enough
-    // the places that no warp fills: before the first row's barrier
-    __device__ __forceinline__ void start()
-    {
-        if constexpr (kWarps > 0 && kWarps < kRoom)
-            if (threadIdx.x < 2 * kSize && threadIdx.x % kRoom >= kWarps)
-                reinterpret_cast<float *>(s)[threadIdx.x] = 0.f;
-    }
     __device__ __forceinline__ void put(int turn, float v)
     {
         if (threadIdx.x % 32 == 0)
             reinterpret_cast<float *>(s[turn & 1])[Group<G, GROUPS>::number() * kRoom + threadIdx.x % G / 32] = v;
     }
+    // the values of a group's kWarps warps, joined
+#pragma nv_exec_check_disable
     template <class F>
-    __device__ __forceinline__ float get(int turn, F join) const
+    static __host__ __device__ __forceinline__ float fold(const float4 *of, F join)
     {
-        const float4 *of = s[turn & 1] + Group<G, GROUPS>::number() * (kRoom / 4);
         float v = 0.f;
 #pragma unroll
         for (int i = 0; i < kRoom / 4; ++i) {
             const float4 w = of[i];
-            const float part = join(join(w.x, w.y), join(w.z, w.w));
+            float part = 4 * i + 1 < kWarps ? join(w.x, w.y) : w.x;
+            if (4 * i + 2 < kWarps)
+                part = join(part, 4 * i + 3 < kWarps ? join(w.z, w.w) : w.z);
             v = i ? join(v, part) : part;
         }
         return v;
+    }
+    template <class F>
+    __device__ __forceinline__ float get(int turn, F join) const
+    {
+        return fold(s[turn & 1] + Group<G, GROUPS>::number() * (kRoom / 4), join);
     }
 };
 
@@ -437,8 +440,6 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
     const bool add = RESIDUAL && (WIDE || p.residual);
     extern __shared__ uint4 s_rows[];   // the operands' rings; narrow rows: 16 bytes a thread
     __shared__ Joined<G, kGroups> s_first, s_second;
-    s_first.start();
-    s_second.start();
     const int g = Row::rank();
     const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
     int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + Row::number();
@@ -612,8 +613,6 @@ rms_norm_backward_kernel(const __grid_constant__ NormGradParams p)
     extern __shared__ uint4 s_rows[];
     float *s_gain = reinterpret_cast<float *>(s_rows + (WIDE ? 0 : kThreads));
     __shared__ Joined<G, kGroups> s_first, s_second;
-    s_first.start();
-    s_second.start();
     const int g = Row::rank();
     const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
     int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + Row::number();
