@@ -15,7 +15,7 @@
 //
 // Bound by HBM where a residual or y comes along, by instructions (14.5 an element of bf16, 65 % of the issue slots, by 16
 // warps an SM) where rows only become e4m3.  16384 x 4096 bf16: with a residual to h and y 84.5 us (94 % of the copy rate), and e4m3 by 32
-// columns too 99.4 us (90 %), from x to y 41.6 us (95 %), to e4m3 alone 39.0 us (77 %); the gradient 82.4 us (96 %), in
+// columns too 99.4 us (90 %), from x to y 41.6 us (95 %), to e4m3 alone 42.7 us (70 %), with powers of two 34.4 us (86 %); the gradient 82.4 us (96 %), in
 // 32 bits at 2048 columns 78.4 us (101 %).  8192 x 2049 (narrow): 49.1 us with e4m3 (46 %), gradient 60.7 us (33 %).  The
 // products and sums by pairs (f32x2 instructions), the gain in registers and threads that fit the row took the norm with
 // all its outputs from 36 instructions an element to 25, the gradient from 36 to 19.
@@ -390,12 +390,71 @@ __device__ __forceinline__ float root_reciprocal(float m)
     return m < INFINITY ? fmaf(0.5f * r, fmaf(-m * r, r, 1.f), r) : r;
 }
 
-// m / 448 for a magnitude whose quotient is a normal number, rounded to the nearest: the product with the reciprocal,
-// corrected by its remainder.
+// m / 448 for a magnitude whose quotient is a normal number, rounded to the nearest: the product with the reciprocal, off by
+// less than 1.25 units in the last place, and its remainder times that reciprocal.  The remainder is less than nine of its
+// least steps, so exact, and the quotient is a fourteenth of a unit or more away from where the rounding changes.
 __device__ __forceinline__ float over_448(float m)
 {
     const float c = 1.f / 448.f, q = m * c;
     return fmaf(fmaf(-448.f, q, m), c, q);
+}
+
+// v / s for V numbers no larger than 448 s (or so), s >= 2^-126 or NaN, each rounded to 32 bits, so that a quotient halfway
+// between two e4m3 values is found there.  In two forms: `any_quotients` for every s, and `quotients` for those that
+// `usual` says, half the instructions, with the same e4m3 values.
+//
+// Markstein's correction, twice: the product with the rounded reciprocal is off by less than 1.5 units in the last place, the
+// first correction leaves one of the two neighbours of the quotient, whose remainder is then exact, and the second rounds
+// it to the nearest.  The quotients are negated up to there, not the reciprocal, so that a remainder of 0 keeps a zero's
+// sign.  Remainders below the subnormal numbers would be lost, so a small s is scaled up, and v with it; where a quotient
+// is too small for that to help, it is less than half of the least e4m3.
+template <int V>
+__device__ __forceinline__ void any_quotients(float2 *v, float s)
+{
+    const float up = s < 0x1p-60f ? 0x1p64f : 1.f;
+    s *= up;
+    const float2 back = both(-__frcp_rn(s)), ss = both(s);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        const float2 of = __fmul2_rn(v[i], both(up));
+        float2 q = __fmul2_rn(of, back);
+        q = __ffma2_rn(__ffma2_rn(ss, q, of), back, q);
+        v[i] = __fmul2_rn(__ffma2_rn(__ffma2_rn(ss, q, of), back, q), both(-1.f));
+    }
+}
+
+// The reciprocal in two numbers, hi below it and lo the rest (both positive, which keeps a zero's sign), and v hi + (v lo): the
+// quotient to within 2^-42 of itself, then rounded.  That gives another e4m3 value than the rounded quotient only where the
+// quotient is as near to the rounding border next to a tie, with v = V 2^i, s = S 2^k (V, S of 24 bits), ties K / 16 of 4 bits
+// after the point: where S (K 2^20 +- 1) is within 2^49 2^-42 of a multiple of 2^24, so S within 128 of one of 2^20.
+// Such S, one in 4096, are not `usual`, nor those whose lo, or remainder, would be below the normal numbers.
+// 16384 x 4096 bf16 to e4m3 alone, a scale a 128 columns: 42.7 us, by any_quotients alone 51.8, by one product with the
+// reciprocal (whose ties fall either way) 38.8.
+__device__ __forceinline__ bool usual(float s)
+{
+    const uint32_t bits = __float_as_uint(s);
+    return bits - 0x21800000u < 0x3c000000u /* 2^-60 .. 2^60 */ && ((bits + 128u) & 0xfffffu) > 256u;
+}
+
+template <int V>
+__device__ __forceinline__ void quotients(float2 *v, float s)
+{
+    float x;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(s));   // off by up to two units in the last place: below 1 / s by
+    const float hi = __uint_as_float(__float_as_uint(x) - 3u);   // one to five of them, e 2^-20.6 at most
+    const float e = fmaf(-s, hi, 1.f), lo = fmaf(e, e, e) * hi;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i)
+        v[i] = __ffma2_rn(v[i], both(hi), __fmul2_rn(v[i], both(lo)));
+}
+
+// V numbers as e4m3, four in a word.
+template <int V>
+__device__ __forceinline__ void to_e4m3(const float2 *v, uint32_t *bytes)
+{
+#pragma unroll
+    for (int i = 0; i < V / 2; i += 2)
+        bytes[i / 2] = e4m3_pair(v[i].x, v[i].y) | e4m3_pair(v[i + 1].x, v[i + 1].y) << 16;
 }
 
 // Groups of a CTA: enough for 128 threads where a warp or less takes a row, for 256 in the gradient, whose CTAs each
@@ -534,8 +593,8 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
             if (p.y)
                 store_vec<D, WIDE, kLanes>(y.at, (j * G + g) * V, width, s_rows, pack_pairs<D>(v[j]));
         }
-        float largest[HOLD];
         if (p.q) {
+            float largest[HOLD];
 #pragma unroll
             for (int j = 0; j < HOLD; ++j) {
                 largest[j] = whole ? top : 0.f;
@@ -549,46 +608,58 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
 #pragma unroll
                 for (int j = 0; j < HOLD; ++j)
                     largest[j] = max_nan(largest[j], __shfl_xor_sync(kFullWarp, largest[j], d));
-        }
-#pragma unroll
-        for (int j = 0; j < HOLD; ++j) {
-            if (!p.q)
-                break;
-            const int e = (j * G + g) * V;
-            const float m = largest[j];
-            const bool write = writes && e < width && (j == 0 || !whole);
-            const int64_t at = scale_at + (j * G * V >> shift);
-            float inverse;
+            const auto write = [&](int j) { return writes && (j * G + g) * V < width && (j == 0 || !whole); };
+            const auto at = [&](int j) { return scale_at + (j * G * V >> shift); };
             if (p.power) {
-                // m = c 2^a with c in [1, 2), 448 = 1.75 * 2^8: the exponent is a - 8, and one more where c > 1.75
-                const int biased = max(static_cast<int>((__float_as_uint(m) + 0x1fffffu) >> 23) - 8, 0);
-                const bool finite = m < INFINITY;
-                inverse = __uint_as_float(finite ? static_cast<uint32_t>(254 - biased) << 23 : 0x7fffffffu);
-                if (write)
-                    static_cast<uint8_t *>(p.scales)[at] = finite ? static_cast<uint8_t>(biased) : 255u;
-            } else {
-                constexpr float kLeast = 1.17549435e-38f;   // 2^-126
-                const float scale = m <= 448.f * kLeast ? kLeast : m < INFINITY ? over_448(m) : __uint_as_float(0x7fffffffu);
-                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(scale));
-                inverse = fmaf(fmaf(-scale, inverse, 1.f), inverse, inverse);
-                if (write)
-                    static_cast<float *>(p.scales)[at] = scale;
-            }
-            uint32_t bytes[V / 4];
 #pragma unroll
-            for (int i = 0; i < V / 2; i += 2) {
-                const float2 low = __fmul2_rn(v[j][i], both(inverse)), high = __fmul2_rn(v[j][i + 1], both(inverse));
-                bytes[i / 2] = e4m3_pair(low.x, low.y) | e4m3_pair(high.x, high.y) << 16;
+                for (int j = 0; j < HOLD; ++j) {
+                    // m = c 2^a with c in [1, 2), 448 = 1.75 * 2^8: the exponent is a - 8, and one more where c > 1.75
+                    const float m = largest[j];
+                    const int biased = max(static_cast<int>((__float_as_uint(m) + 0x1fffffu) >> 23) - 8, 0);
+                    const bool finite = m < INFINITY;
+                    if (write(j))
+                        static_cast<uint8_t *>(p.scales)[at(j)] = finite ? static_cast<uint8_t>(biased) : 255u;
+                    const float inverse = __uint_as_float(finite ? static_cast<uint32_t>(254 - biased) << 23 : 0x7fffffffu);
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i)
+                        v[j][i] = __fmul2_rn(v[j][i], both(inverse));   // exact
+                }
+            } else {
+                bool fast = true;
+#pragma unroll
+                for (int j = 0; j < HOLD; ++j) {
+                    constexpr float kLeast = 1.17549435e-38f;   // 2^-126
+                    const float m = largest[j];
+                    largest[j] = m <= 448.f * kLeast ? kLeast : m < INFINITY ? over_448(m) : __uint_as_float(0x7fffffffu);
+                    if (write(j))
+                        static_cast<float *>(p.scales)[at(j)] = largest[j];
+                    fast = fast && (usual(largest[j]) || m == 0.f);   // zeros: columns past the last among them
+                }
+                if (fast) {
+#pragma unroll
+                    for (int j = 0; j < HOLD; ++j)
+                        quotients<V>(v[j], largest[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < HOLD; ++j)
+                        any_quotients<V>(v[j], largest[j]);
+                }
             }
-            typename Bits<V>::type raw;
-            if constexpr (V == 8)
-                raw = make_uint2(bytes[0], bytes[1]);
-            else
-                raw = bytes[0];
-            if constexpr (!WIDE)
-                store_narrow<uint8_t, V, kLanes>(q.at, e, width, s_rows, raw);
-            else if (e < width)
-                *reinterpret_cast<typename Bits<V>::type *>(q.at + e) = raw;
+#pragma unroll
+            for (int j = 0; j < HOLD; ++j) {
+                const int e = (j * G + g) * V;
+                uint32_t bytes[V / 4];
+                to_e4m3<V>(v[j], bytes);
+                typename Bits<V>::type raw;
+                if constexpr (V == 8)
+                    raw = make_uint2(bytes[0], bytes[1]);
+                else
+                    raw = bytes[0];
+                if constexpr (!WIDE)
+                    store_narrow<uint8_t, V, kLanes>(q.at, e, width, s_rows, raw);
+                else if (e < width)
+                    *reinterpret_cast<typename Bits<V>::type *>(q.at + e) = raw;
+            }
         }
         y.next();
         q.next();

@@ -944,9 +944,10 @@ typedef enum { CNS_SCALE_F32 = 0, CNS_SCALE_E8M0 = 1 } cns_scale_t;
  *   In 8 bits (q_dev): each row's columns in blocks of scale_block (the last
  * may be shorter), or the whole row as one.  m = the block's largest |y|, of
  * the y in 32 bits:
- *   CNS_SCALE_F32   s = max(m / 448, 2^-126);
+ *   CNS_SCALE_F32   s = max(m / 448, 2^-126), the quotient rounded to 32 bits;
  *   CNS_SCALE_E8M0  s = the least power of two >= m / 448, from 2^-127 on;
- *   q = y / s rounded to the nearest e4m3 (ties to even).
+ *   q = y / s, the quotient rounded to 32 bits, then to the nearest e4m3 (ties
+ * to even).
  * A block with an infinity or a NaN has s = NaN and q = NaN throughout.
  *   But for h as said below, no output may overlap another tensor of the call. */
 typedef struct {
