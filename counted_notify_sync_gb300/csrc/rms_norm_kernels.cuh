@@ -2,7 +2,7 @@
 // (cns_rms_norm, cns_rms_norm_backward); rms_norm_{f32,bf16,f16}.cu instantiate
 // them, a type each.
 //
-//   h = round(x + residual),  r = 1 / sqrt(mean h^2 + eps),  y = h gain r,
+//   h = round(x + residual),  r = 1 / sqrt(mean h^2 + eps),  y = h r gain,
 //   per block of columns: s from the largest |y|, q = e4m3(y / s)
 //   dx = dh + r g - h r^3 mean(g h) with g = gain dy;  dgain = sum over rows dy h r
 //
@@ -357,21 +357,31 @@ struct Largest {
     __device__ __forceinline__ float operator()(float a, float b) const { return max_nan(a, b); }
 };
 
-// `a` summed, and `b`, if `second`, joined over a row's threads.
+// A value joined over a row's threads.
 template <int G, int GROUPS, class F>
-__device__ __forceinline__ void join_row(float &a, float &b, F join, bool second, Joined<G, GROUPS> &sa, Joined<G, GROUPS> &sb, int turn)
+__device__ __forceinline__ float join_row(float v, F join, Joined<G, GROUPS> &s, int turn)
+{
+    v = join_lanes<G>(v, join);
+    if constexpr (G > 32) {
+        s.put(turn, v);
+        Group<G, GROUPS>::sync();
+        v = s.get(turn, join);
+    }
+    return v;
+}
+
+// Two sums over a row's threads, with one barrier.
+template <int G, int GROUPS>
+__device__ __forceinline__ void sum_row(float &a, float &b, Joined<G, GROUPS> &sa, Joined<G, GROUPS> &sb, int turn)
 {
     a = join_lanes<G>(a, Add());
-    if (second)
-        b = join_lanes<G>(b, join);
+    b = join_lanes<G>(b, Add());
     if constexpr (G > 32) {
         sa.put(turn, a);
-        if (second)
-            sb.put(turn, b);
+        sb.put(turn, b);
         Group<G, GROUPS>::sync();
         a = sa.get(turn, Add());
-        if (second)
-            b = sb.get(turn, join);
+        b = sb.get(turn, Add());
     }
 }
 
@@ -530,7 +540,7 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
             load_gain<V, WIDE>(p.gain, p.gain_dtype, (j * G + g) * V, p.width, gain[j]);
     }
     const float share = 1.f / static_cast<float>(p.width);
-    const bool whole = p.q && p.block == 0;
+    const bool whole = p.block == 0;
     // The lanes of a block, which of them writes its scale, and that scale's number.  (The vectors of a thread are a
     // multiple of 128 columns apart where there are blocks, so this holds for each of them.)
     const int lanes = p.block / V, shift = p.block ? 31 - __clz(p.block) : 0;
@@ -564,32 +574,22 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
             stage = stage + 1 == kDepth ? 0 : stage + 1;
         }
         float2 v[HOLD][V / 2], sums = both(0.f);
-        float top = 0.f;
 #pragma unroll
         for (int j = 0; j < HOLD; ++j) {
             unpack_pairs<D>(held[j], v[j]);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i)
+                sums = __ffma2_rn(v[j][i], v[j][i], sums);
+        }
+        const float sum = join_row<G, kGroups>(sums.x + sums.y, Add(), s_first, turn);
+        const float r = root_reciprocal(fmaf(sum, share, p.eps));
+#pragma unroll
+        for (int j = 0; j < HOLD; ++j) {
             if constexpr (!kGain)
                 load_gain<V, WIDE>(p.gain, p.gain_dtype, (j * G + g) * V, p.width, gain[j]);
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                sums = __ffma2_rn(v[j][i], v[j][i], sums);
-                v[j][i] = __fmul2_rn(v[j][i], gain[j][i]);   // of 16-bit numbers exact
-            }
-            if (whole) {
-#pragma unroll
-                for (int i = 0; i < V / 2; ++i)
-                    top = max_nan(top, max_nan(fabsf(v[j][i].x), fabsf(v[j][i].y)));
-            }
-        }
-        float sum = sums.x + sums.y;
-        join_row<G, kGroups>(sum, top, Largest(), whole, s_first, s_second, turn);
-        const float r = root_reciprocal(fmaf(sum, share, p.eps));
-        top = fabsf(top * r);
-#pragma unroll
-        for (int j = 0; j < HOLD; ++j) {
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i)
-                v[j][i] = __fmul2_rn(v[j][i], both(r));
+            for (int i = 0; i < V / 2; ++i)   // h r is no more than the root of the width; h times the gain may overflow
+                v[j][i] = __fmul2_rn(__fmul2_rn(v[j][i], both(r)), gain[j][i]);
             if (p.y)
                 store_vec<D, WIDE, kLanes>(y.at, (j * G + g) * V, width, s_rows, pack_pairs<D>(v[j]));
         }
@@ -597,17 +597,26 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
             float largest[HOLD];
 #pragma unroll
             for (int j = 0; j < HOLD; ++j) {
-                largest[j] = whole ? top : 0.f;
-                if (!whole) {
+                largest[j] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < V / 2; ++i)
-                        largest[j] = max_nan(largest[j], max_nan(fabsf(v[j][i].x), fabsf(v[j][i].y)));
-                }
+                for (int i = 0; i < V / 2; ++i)
+                    largest[j] = max_nan(largest[j], max_nan(fabsf(v[j][i].x), fabsf(v[j][i].y)));
             }
-            for (int d = 1; d < lanes; d *= 2)
+            if (whole) {
+                float top = largest[0];
+#pragma unroll
+                for (int j = 1; j < HOLD; ++j)
+                    top = max_nan(top, largest[j]);
+                top = join_row<G, kGroups>(top, Largest(), s_second, turn);
 #pragma unroll
                 for (int j = 0; j < HOLD; ++j)
-                    largest[j] = max_nan(largest[j], __shfl_xor_sync(kFullWarp, largest[j], d));
+                    largest[j] = top;
+            } else {
+                for (int d = 1; d < lanes; d *= 2)
+#pragma unroll
+                    for (int j = 0; j < HOLD; ++j)
+                        largest[j] = max_nan(largest[j], __shfl_xor_sync(kFullWarp, largest[j], d));
+            }
             const auto write = [&](int j) { return writes && (j * G + g) * V < width && (j == 0 || !whole); };
             const auto at = [&](int j) { return scale_at + (j * G * V >> shift); };
             if (p.power) {
@@ -752,7 +761,7 @@ rms_norm_backward_kernel(const __grid_constant__ NormGradParams p)
             }
         }
         float sum = sums.x + sums.y, inner = inners.x + inners.y;
-        join_row<G, kGroups>(sum, inner, Add(), true, s_first, s_second, turn);
+        sum_row<G, kGroups>(sum, inner, s_first, s_second, turn);
         const float r = root_reciprocal(fmaf(sum, share, p.eps));
         const float2 back = both(-(inner * share) * r * r), rs = both(r), mine = both(width ? r : 0.f);
 #pragma unroll

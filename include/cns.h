@@ -938,8 +938,8 @@ typedef enum { CNS_SCALE_F32 = 0, CNS_SCALE_E8M0 = 1 } cns_scale_t;
 
 /* Norm of each row, with the residual's addition:
  *   h = x + residual in 32 bits, rounded to dtype (x without a residual);
- *   y = h * r * gain in 32 bits, r = 1 / sqrt(mean of h^2 + eps), rounded once
- *       to dtype where y_dev takes it.
+ *   y = (h * r) * gain in 32 bits, r = 1 / sqrt(mean of h^2 + eps), rounded
+ *       once to dtype where y_dev takes it.
  * The squares are summed in 32 bits: a row whose sum overflows gets r = 0.
  *   In 8 bits (q_dev): each row's columns in blocks of scale_block (the last
  * may be shorter), or the whole row as one.  m = the block's largest |y|, of
