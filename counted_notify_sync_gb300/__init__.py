@@ -335,9 +335,25 @@ def _matrix(x, name, index, shape, dtype):
             return 0
         (rows, cols), (step, one) = shape, x.stride()
         if (one == 1 or cols == 1) and (step >= cols or rows <= 1):
+            _no_neg(**{name: x})
             return step if rows > 1 else 0
     raise ValueError(f"{name}: {tuple(shape)} {dtype} on CUDA device {index}, rows apart and of unit stride, expected; got "
                      f"{tuple(x.shape)} {x.dtype}, strides {x.stride()}, on {x.device}")
+
+
+def _no_neg(**tensors):
+    """Refuse tensors that stand for their memory's numbers with the other sign: parts of lazy conjugates, so contiguous
+    only with a single element."""
+    for name, x in tensors.items():
+        if x is not None and x is not False and x.is_neg():
+            raise ValueError(f"{name}: a lazily negated tensor; pass its resolve_neg()")
+
+
+def _no_conj(**tensors):
+    """Refuse tensors that stand for the conjugates of what their memory holds."""
+    for name, x in tensors.items():
+        if x is not None and x.is_conj():
+            raise ValueError(f"{name}: a lazily conjugated tensor; pass its resolve_conj()")
 
 
 def _per_place(route, x, name, tokens, dtype):
@@ -376,11 +392,15 @@ def run_dispatch(route, x, *, places=None, rows=None, scales=None, row_scales=No
     `stream`'s memory); places outside it are passed over (a limited capacity), and rows that no place names stay as they
     were, in a new tensor whatever its memory held.  With `scales` [tokens, n], of any type, row_scales[places[t, j]] =
     scales[t] too.  Returns rows, with scales (rows, row_scales), no part of torch's graph: run_dispatch_backward has the
-    gradient."""
+    gradient.  (What memory holds is moved: lazily conjugated or negated tensors are refused, by the calls below too.)"""
     index, shape, dtype, size, top_k = route.index, x.shape, x.dtype, x.element_size(), route.top_k
     if route.others:
         _check_current(index)
+    if size >= 4 and dtype.is_complex:
+        _no_conj(x=x, rows=rows)
     t, width = shape
+    if width == 1:
+        _no_neg(x=x, rows=rows)
     x_step = 0 if x.is_contiguous() and x.get_device() == index else _matrix(x, "x", index, shape, dtype) * size
     if places is not None and (places.shape == (t, top_k) and places.dtype is route.types[0] and
                                places.get_device() == index and places.is_contiguous()):
@@ -396,6 +416,10 @@ def run_dispatch(route, x, *, places=None, rows=None, scales=None, row_scales=No
     each = scales_at = row_scales_at = scales_step = row_scales_step = 0
     if scales is not None:
         kind, each, cols = scales.dtype, scales.element_size(), scales.shape[-1]
+        if kind.is_complex:
+            _no_conj(scales=scales, row_scales=row_scales)
+        if cols == 1:
+            _no_neg(scales=scales, row_scales=row_scales)
         scales_step = _matrix(scales, "scales", index, (t, cols), kind) * each
         if row_scales is None:
             row_scales = _empty_on(stream, scales, (n, cols))
@@ -425,6 +449,8 @@ def _combine(route, rows, weighted, weights, places, base, y, stream, what):
     first = y if y is not None else base if base is not None else places
     t = route.tokens if first is None else first.shape[0]
     shape, per = (t, width), (t, top_k)
+    if width == 1 or t == top_k == 1:
+        _no_neg(weights=weights, base=base, **{what[0]: rows, what[1]: y})
     weights_at = base_at = base_step = y_step = 0
     if weighted:
         if weights is not None and (weights.shape == per and weights.dtype is f32 and weights.get_device() == index and
@@ -483,6 +509,8 @@ def run_combine_backward(route, rows, dy, *, weights=None, places=None, drows=No
     t, width = shape
     dy_step = 0 if dy.is_contiguous() and dy.get_device() == index else _matrix(dy, "dy", index, shape, dtype)
     per = (t, top_k)
+    if width == 1 or t == top_k == 1:
+        _no_neg(rows=rows, dy=dy, weights=weights, drows=drows, dweights=dweights)
     if weights is not None and (weights.shape == per and weights.dtype is f32 and weights.get_device() == index and
                                 weights.is_contiguous()):
         weights_at = weights.data_ptr()
@@ -580,6 +608,8 @@ def run_rms_norm(norm, x, gain=None, *, residual=None, h=None, y=None, q=None, s
         code = _dtype_code(dtype)
     t = x.shape[0]
     shape = (t, width)
+    if width == 1 or t == norm.blocks == 1:
+        _no_neg(x=x, gain=gain, residual=residual, h=h, y=y, scales=scales)
     x_step = 0 if x.shape == shape and x.get_device() == index and x.is_contiguous() else _matrix(x, "x", index, shape, dtype)
     gain_at, gain_code = (0, 0) if gain is None else _gain(norm, gain)
     residual_at = residual_step = h_at = h_step = y_at = y_step = q_at = q_step = scales_at = scales_step = 0
@@ -642,6 +672,8 @@ def run_rms_norm_backward(norm, h, gain, dy, *, dh=None, dx=None, dgain=None, wo
         code = _dtype_code(dtype)
     t = h.shape[0]
     shape = (t, width)
+    if width == 1:
+        _no_neg(h=h, gain=gain, dy=dy, dh=dh, dx=dx, dgain=dgain)
     gain_at, gain_code = (0, 0) if gain is None else _gain(norm, gain)
     h_step = 0 if h.shape == shape and h.get_device() == index and h.is_contiguous() else _matrix(h, "h", index, shape, dtype)
     dy_step = 0 if (dy.shape == shape and dy.dtype is dtype and dy.get_device() == index and
