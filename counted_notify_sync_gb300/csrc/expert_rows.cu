@@ -58,7 +58,7 @@ bool tile(int64_t count, int64_t units, int access, uint32_t tokens, Tiling *t)
         ctas = ((count + tokens - 1) / tokens * t->parts + t->per - 1) / t->per;
     }
     t->ctas = static_cast<uint32_t>(ctas);
-    return ctas <= 0x7fffffff / 8;   // warps are counted in 32 bits
+    return ctas <= (1 << 29);   // warps are counted in 32 bits; more of them than that no memory has rows for
 }
 
 // The first token of the calling thread (the others follow) and its first access (the others are 32 apart each).
@@ -452,8 +452,7 @@ cudaError_t launch(void (*kernel)(P), const P &p, uint32_t ctas, uint32_t thread
 template <int D, int A, int BATCH, int TOKENS>
 cudaError_t launch_combine_as(CombineParams &p, int sms, cudaStream_t s)
 {
-    if (!tile(p.tokens, p.data.units, A, TOKENS, &p.data))
-        return cudaErrorInvalidConfiguration;
+    tile(p.tokens, p.data.units, A, TOKENS, &p.data);   // cns_combine has seen that it fits
     uint32_t ctas = p.data.ctas;
     if constexpr (A == 16) {
         const uint32_t most = static_cast<uint32_t>(sms) * combine_ctas(A, BATCH * TOKENS);
@@ -579,9 +578,6 @@ extern "C" int cns_dispatch(const cns_dispatch_t *d)
         if (!tile(p.tokens, d->scale_bytes / p.scale_access, p.scale_access, 1, &p.scale))
             return CNS_ERR_INVALID_VALUE;
     }
-    const int64_t ctas = static_cast<int64_t>(p.data.ctas) + p.scale.ctas;
-    if (ctas > 0x7fffffff)
-        return CNS_ERR_INVALID_VALUE;
     DeviceInfo dev;
     if (int rc = current_device(&dev))
         return rc;
@@ -593,7 +589,7 @@ extern "C" int cns_dispatch(const cns_dispatch_t *d)
                     : access == 4 ? dispatch_kernel<4>
                     : access == 2 ? dispatch_kernel<2>
                                   : dispatch_kernel<1>,
-                    p, static_cast<uint32_t>(ctas), threads, to_stream(d->stream)));
+                    p, p.data.ctas + p.scale.ctas, threads, to_stream(d->stream)));
     return CNS_SUCCESS;
 }
 
@@ -625,7 +621,8 @@ extern "C" int cns_combine(const cns_combine_t *c)
     if (p.base)
         bits |= address(p.base) | (p.base_stride * e);
     const int access = access_bytes(bits);
-    p.data.units = static_cast<uint32_t>(c->width * e / access);
+    if (!tile(p.tokens, c->width * e / access, access, 1, &p.data))
+        return CNS_ERR_INVALID_VALUE;
     DeviceInfo dev;
     if (int rc = current_device(&dev))
         return rc;
