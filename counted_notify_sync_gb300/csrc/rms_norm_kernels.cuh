@@ -60,9 +60,17 @@ struct NormGradParams {
 
 // Most CTAs of a gradient, each of which leaves a part of dgain: 512 threads to an SM in CTAs of 160 or more.
 constexpr int kNormMaxParts = 3 * kStepMaxCtas;
-// Rows that a group of a gradient has at least, so that few parts are left to join: 777 x 1000 f32 takes 5.0 us with
-// four, 6.5 with one, two or eight.
-constexpr int kNormLeastRows = 4;
+// Rows that a group of a gradient has at least, so that few parts are left to join: as many as it takes for no more CTAs
+// than SMs, four at most; four where one CTA then has all rows and no join follows.  In us, with one / two / four at least:
+//   f32   64 x 1000 3.38 / 3.71 / 4.57, 256 x 1000 3.66 / 4.01 / 4.76, 777 x 1000 5.31 / 5.05 / 4.97, 256 x 4096 6.15 / 6.02 / 7.31
+//   bf16  64 x 1000 4.05 / 4.58 / 5.60, 777 x 1000 5.42 / 4.90 / 5.88, 2000 x 1000 6.65 / 6.54 / 6.10, 8 x 4096 5.16 / 5.67 / 6.64,
+//         256 x 4096 8.50 / 6.72 / 7.35
+// (there by the rule 4.53 and 4.89 for 777 x 1000, with three and two rows), and eight nowhere better.
+__host__ __device__ constexpr int norm_least_rows(int64_t rows, int groups, int sms)
+{
+    const int64_t ctas = (rows + groups - 1) / groups, each = (ctas + sms - 1) / sms;
+    return ctas <= 4 || each > 4 ? 4 : static_cast<int>(each);
+}
 // Dynamic shared memory that every kernel here may be launched with.
 constexpr int kNormMaxSmem = 200 * 1024;
 
@@ -878,7 +886,7 @@ cudaError_t launch_backward_as(const NormGradParams &p, int sms, int *parts, cud
         smem = std::max(smem, 4 * kGroups * p.width);
     const int most = std::min<int>(sms, kStepMaxCtas) * norm_ctas_per_sm(G, HOLD, true);
     static_assert(norm_ctas_per_sm(G, HOLD, true) * kStepMaxCtas <= kNormMaxParts, "room for the parts");
-    *parts = norm_ctas(p.rows, kGroups, kNormLeastRows, most);
+    *parts = norm_ctas(p.rows, kGroups, norm_least_rows(p.rows, kGroups, sms), most);
     NormGradParams with = p;
     with.joined = p.dgain && *parts > 1;
     if (!with.joined)
