@@ -169,7 +169,8 @@ struct CombineParams {
 };
 
 // CTAs to an SM that combine's registers are shared out for, by the rows that a thread has in flight: 64 registers a
-// thread where those are up to four, else 80.  Narrow accesses have three CTAs (four spill).
+// thread where those are up to four, else 80.  (Two places of two tokens in bf16 put 48 bytes a thread aside for that, one
+// place of two in f16 eight; the others fit.)  Narrow accesses have three CTAs (four spill).
 __host__ __device__ constexpr int combine_ctas(int a, int rows) { return a == 16 && rows <= 4 ? 4 : 3; }
 
 // What a thread of combine_kernel does; FULL: all its accesses are within the row.
@@ -277,10 +278,11 @@ __device__ __forceinline__ void combine_rows(const CombineParams &p, int64_t t, 
     }
 }
 
-// A thread has TOKENS tokens at a time and of each the rows of BATCH places, all in flight together; while they are on their way it loads the places of the next ones.  As many CTAs as the GPU holds, so that only a
-// thread's first rows wait for their places: 65536 x 1024 bf16 with two places takes 66.4 us, 90 % of the copy rate; a CTA
-// for every 256 accesses, each waiting for its places, took 91.  16384 x 4096 bf16, 8 places: 180 us as a dispatch's
-// gradient (99 %), 203 with weights and a base (98 %).  8192 x 2049 bf16, 4 places: 46.3 us (53 %; instructions).
+// A thread has TOKENS tokens at a time and of each the rows of BATCH places, all in flight together; while they are on
+// their way it loads the places of the next ones.  As many CTAs as the GPU holds, so that only a thread's first rows wait
+// for their places: 65536 x 1024 bf16 with two places takes 66.9 us, 89 % of the copy rate; a CTA for every 256 accesses,
+// each waiting for its places, took 91.  16384 x 4096 bf16, 8 places: 179 us as a dispatch's gradient (99 %), 201 with
+// weights and a base (98 %).  8192 x 2049 bf16, 4 places: 47.1 us (53 %; instructions).
 template <int D, int A, int BATCH, int TOKENS>
 __global__ void __launch_bounds__(kRowThreads, combine_ctas(A, BATCH * TOKENS)) combine_kernel(const __grid_constant__ CombineParams p)
 {
@@ -372,7 +374,8 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __g
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 row[i] = token && j + i < p.top_k ? static_cast<uint32_t>(place[j + i]) : 0xffffffffu;
-                const B *at = reinterpret_cast<const B *>(static_cast<const T *>(p.rows) + static_cast<uint64_t>(row[i]) * p.rows_stride) + u;
+                const T *from_row = static_cast<const T *>(p.rows) + static_cast<uint64_t>(row[i]) * p.rows_stride;
+                const B *at = reinterpret_cast<const B *>(from_row) + u;
 #pragma unroll
                 for (int k = 0; k < HELD; ++k)
                     raw[i][k] = B{};
@@ -389,7 +392,8 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __g
                 const bool there = row[i] < p.limit;
                 if (p.drows && there) {
                     const float w = p.weights ? weight[j + i] : 1.f;
-                    B *to = reinterpret_cast<B *>(static_cast<T *>(p.drows) + static_cast<uint64_t>(row[i]) * p.drows_stride) + u;
+                    T *to_row = static_cast<T *>(p.drows) + static_cast<uint64_t>(row[i]) * p.drows_stride;
+                    B *to = reinterpret_cast<B *>(to_row) + u;
 #pragma unroll
                     for (int k = 0; k < HELD; ++k) {
                         float v[V];

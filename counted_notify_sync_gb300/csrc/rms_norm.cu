@@ -15,9 +15,10 @@ namespace {
 constexpr int kJoinColumns = 8, kJoinRows = 64, kJoinHeld = 5;   // 8 columns: a sector of each part
 
 // dgain = the sum of the parts.  A CTA has 8 columns, its 64 groups of 8 threads every 64th part, so that few columns
-// have CTAs enough too and a thread's loads are in flight together: the gradient of 777 x 1000 f32 takes 5.0 us so, 5.75
-// with 32 columns and 32 groups; of 16384 x 1000 bf16 26.7, and 28.6 with 32 groups of 8.
-__global__ void __launch_bounds__(kJoinColumns * kJoinRows) join_parts_kernel(const float *parts, int count, int width, float *dgain)
+// have CTAs enough too and a thread's loads are in flight together: the gradient of 16384 x 1000 bf16 takes 26.8 us so,
+// 27.4 with 32 columns and 32 groups or with 32 groups of 8; of 777 x 1000 f32 4.55, 4.61 and 4.61.
+__global__ void __launch_bounds__(kJoinColumns * kJoinRows)
+join_parts_kernel(const float *parts, int count, int width, float *dgain)
 {
     __shared__ float s_sum[kJoinRows * kJoinColumns / 32][kJoinColumns];
     const int column = threadIdx.x % kJoinColumns, e = blockIdx.x * kJoinColumns + column;

@@ -7,18 +7,20 @@
 //   dx = dh + r g - h r^3 mean(g h) with g = gain dy;  dgain = sum over rows dy h r
 //
 // A group of threads takes a row, one pass over the operands: a thread has HOLD vectors of 16 bytes, as far apart as the
-// group is large, so that a block of 32 columns or more is the vectors of neighbouring lanes of one warp.  As many CTAs as the GPU holds go
-// through the rows in steps, so a CTA's sums of dgain stay on the SM, and the next rows are on their way while one is
-// worked on: WIDE rows, whose vectors are aligned, are copied to shared memory ahead (every thread copies what it will
-// read itself, so no thread waits for another's copies), others pass through shared memory element by element, in
-// neighbouring lanes' order on the global side and by vectors on the registers'.
+// group is large, so that a block of 32 columns or more is the vectors of neighbouring lanes of one warp.  As many CTAs
+// as the GPU holds go through the rows in steps, so a CTA's sums of dgain stay on the SM, and the next rows are on their
+// way while one is worked on: WIDE rows, whose vectors are aligned, are copied to shared memory ahead (every thread
+// copies what it will read itself, so no thread waits for another's copies), others pass through shared memory element
+// by element, in neighbouring lanes' order on the global side and by vectors on the registers'.
 //
-// Bound by HBM where a residual or y comes along, by instructions (14.5 an element of bf16, 65 % of the issue slots, by 16
-// warps an SM) where rows only become e4m3.  16384 x 4096 bf16: with a residual to h and y 84.5 us (94 % of the copy rate), and e4m3 by 32
-// columns too 99.4 us (90 %), from x to y 41.6 us (95 %), to e4m3 alone 42.7 us (70 %), with powers of two 34.4 us (86 %); the gradient 82.4 us (96 %), in
-// 32 bits at 2048 columns 78.4 us (101 %).  8192 x 2049 (narrow): 49.1 us with e4m3 (46 %), gradient 60.7 us (33 %).  The
-// products and sums by pairs (f32x2 instructions), the gain in registers and threads that fit the row took the norm with
-// all its outputs from 36 instructions an element to 25, the gradient from 36 to 19.
+// Bound by HBM where a residual or y comes along, by instructions (14.6 an element of bf16, 63 % of the issue slots, by 16
+// warps an SM) where rows only become e4m3 with scales in 32 bits.  16384 x 4096 bf16: with a residual to h and y 84.0 us
+// (94 % of the copy rate), and e4m3 with powers of two by 32 columns too 99.4 us (90 %), from x to y 41.7 us (95 %), to
+// e4m3 alone 41.0 us (73 %), with powers of two 32.4 us (92 %); the gradient 82.3 us (96 %), in 32 bits at 2048 columns
+// 78.1 us (101 %).  8192 x 2049 (narrow): 49.8 us with e4m3 (45 %), gradient 61.0 us (32 %).  More than 8192 columns of 16
+// bits: 4096 x 16384 90.8 us to h and y (87 %), gradient 146 (54 %), 2048 x 32768 86.5 and 297 (27 %; registers spill).
+// The products and sums by pairs (f32x2 instructions), the gain in registers and threads that fit the row took the norm
+// with all its outputs from 36 instructions an element to 23, the gradient from 36 to 19.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -281,26 +283,26 @@ __device__ __forceinline__ void load_gain(const void *gain, int dtype, int e, in
     for (int i = 0; i < N; ++i)
         v[i] = gain ? 0.f : 1.f;
     if (gain && e < width) {
-    if constexpr (WIDE) {
-        if (dtype == CNS_DT_F32) {
+        if constexpr (WIDE) {
+            if (dtype == CNS_DT_F32) {
 #pragma unroll
-            for (int i = 0; i < N; i += 4)
-                unpack<CNS_DT_F32, 16>(*reinterpret_cast<const uint4 *>(static_cast<const float *>(gain) + e + i), v + i);
+                for (int i = 0; i < N; i += 4)
+                    unpack<CNS_DT_F32, 16>(*reinterpret_cast<const uint4 *>(static_cast<const float *>(gain) + e + i), v + i);
+            } else {
+                const auto raw = *reinterpret_cast<const typename Bits<2 * N>::type *>(static_cast<const uint16_t *>(gain) + e);
+                if (dtype == CNS_DT_BF16)
+                    unpack<CNS_DT_BF16, 2 * N>(raw, v);
+                else
+                    unpack<CNS_DT_F16, 2 * N>(raw, v);
+            }
         } else {
-            const auto raw = *reinterpret_cast<const typename Bits<2 * N>::type *>(static_cast<const uint16_t *>(gain) + e);
-            if (dtype == CNS_DT_BF16)
-                unpack<CNS_DT_BF16, 2 * N>(raw, v);
-            else
-                unpack<CNS_DT_F16, 2 * N>(raw, v);
-        }
-    } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (e + i < width)
-                v[i] = dtype == CNS_DT_F32    ? static_cast<const float *>(gain)[e + i]
-                       : dtype == CNS_DT_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(gain)[e + i])
-                                              : __half2float(static_cast<const __half *>(gain)[e + i]);
-    }
+            for (int i = 0; i < N; ++i)
+                if (e + i < width)
+                    v[i] = dtype == CNS_DT_F32    ? static_cast<const float *>(gain)[e + i]
+                           : dtype == CNS_DT_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(gain)[e + i])
+                                                  : __half2float(static_cast<const __half *>(gain)[e + i]);
+        }
     }
 #pragma unroll
     for (int i = 0; i < N / 2; ++i)
@@ -446,7 +448,7 @@ __device__ __forceinline__ void any_quotients(float2 *v, float s)
 // quotient is as near to the rounding border next to a tie, with v = V 2^i, s = S 2^k (V, S of 24 bits), ties K / 16 of 4 bits
 // after the point: where S (K 2^20 +- 1) is within 2^49 2^-42 of a multiple of 2^24, so S within 128 of one of 2^20.
 // Such S, one in 4096, are not `usual`, nor those whose lo, or remainder, would be below the normal numbers.
-// 16384 x 4096 bf16 to e4m3 alone, a scale a 128 columns: 42.7 us, by any_quotients alone 51.8, by one product with the
+// 16384 x 4096 bf16 to e4m3 alone, a scale a 128 columns, when it came: 42.7 us, by any_quotients alone 51.8, by one product with the
 // reciprocal (whose ties fall either way) 38.8.
 __device__ __forceinline__ bool usual(float s)
 {
@@ -495,8 +497,9 @@ __host__ __device__ constexpr bool norm_sums_in_registers(int g, int hold) { ret
 
 // Rows on their way ahead of the one at hand, of `operands` tensors each (3: the gradient): two, one of a norm with a
 // residual; none where the shared memory lacks the room.  More of them cost time, presumably because the DRAM's pages are
-// left and opened again in between: 16384 x 4096 bf16 takes the norm with a residual 84.5 us with one, 85.8 with two and
-// 88.5 with four, without one 46.9, 41.7 and (three) 45.5; its gradient 89.5, 82.6 and (four) 88.5.
+// left and opened again in between: 16384 x 4096 bf16 takes the norm with a residual 84.0 us with one, 85.2 with two and
+// 89.2 with four (and with e4m3 99.4, 103.5 and 106.5), without one 47.2, 41.7 and (three) 44.9; its gradient 89.5, 82.6
+// and (four) 88.5.
 __host__ __device__ constexpr int norm_depth(bool wide, int g, int hold, int operands)
 {
     const bool grad = operands == 3;
@@ -897,8 +900,8 @@ cudaError_t launch_backward_as(const NormGradParams &p, int sms, int *parts, cud
 // Calls what(G, HOLD) for rows of `vecs` vectors.  Two vectors a thread up to 1024 (8192 columns of 16 bits), and as few
 // warps as hold them; four vectors beyond.  Blocks of columns need a warp to a row at least (a block's vectors are
 // neighbouring lanes').  `few`: four vectors a thread from 128 on; where little memory traffic comes with much arithmetic
-// it pays that half as many threads do what each does once a row (16384 x 4096 bf16 to e4m3 alone 40.3 us, with two
-// vectors 47.5; with a residual and y 101.2 against 98.9).
+// it pays that half as many threads do what each does once a row (16384 x 4096 bf16 to e4m3 alone 41.0 us, with two
+// vectors 47.4, with powers of two 32.4 and 40.6; with a residual and y, when it was tried, 101.2 against 98.9).
 template <int V, bool FEW, class F>
 cudaError_t with_shape(int vecs, bool blocks, bool few, F what)
 {

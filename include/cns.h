@@ -902,7 +902,8 @@ int cns_combine(const cns_combine_t *c);
 /* Combine's gradient: drows[places[t][j]] = weights[t][j] * dy[t], the product
  * in 32 bits, rounded once; dweights[t][j] = the sum over the columns of
  * dy[t] * rows[places[t][j]] in 32 bits, in an order that depends on the width
- * and the rows' alignment alone, 0 for a place without a row.  The base's gradient is dy itself. */
+ * and on how dy, rows and drows (if given) are aligned, addresses and strides,
+ * alone; 0 for a place without a row.  The base's gradient is dy itself. */
 typedef struct {
     const void *rows_dev;       /* (in) [rows][width], the forward call's; NULL without dweights_dev */
     const void *dy_dev;         /* (in) [tokens][width] */
@@ -940,7 +941,9 @@ typedef enum { CNS_SCALE_F32 = 0, CNS_SCALE_E8M0 = 1 } cns_scale_t;
  *   h = x + residual in 32 bits, rounded to dtype (x without a residual);
  *   y = (h * r) * gain in 32 bits, r = 1 / sqrt(mean of h^2 + eps), rounded
  *       once to dtype where y_dev takes it.
- * The squares are summed in 32 bits: a row whose sum overflows gets r = 0.
+ * The squares are summed in 32 bits, in an order that depends on the width, on
+ * which tensors the call has and how they are aligned (addresses and strides)
+ * alone: a row whose sum overflows gets r = 0.
  *   In 8 bits (q_dev): each row's columns in blocks of scale_block (the last
  * may be shorter), or the whole row as one.  m = the block's largest |y|, of
  * the y in 32 bits:
@@ -986,7 +989,8 @@ int cns_rms_norm(const cns_rms_norm_t *n);
  *   dx = dh + r * g - h * r^3 * mean of (g * h),  g = gain * dy,
  * in 32 bits, rounded once; it is the residual's gradient too; and
  *   dgain = sum over the rows of dy * h * r, in 32 bits, in an order that
- * depends on the sizes and the rows' alignment alone. */
+ * depends on the sizes, on how the operands are aligned (addresses and
+ * strides) and on the GPU's number of SMs alone. */
 typedef struct {
     const void *h_dev;         /* (in) [rows][width], the forward call's h (its x without a residual) */
     const void *gain_dev;      /* (in, optional) */

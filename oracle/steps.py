@@ -1,6 +1,6 @@
 """The device-wide steps of a training step in 64 bits, plain numpy: routing to experts, its gradient, the
-global gradient norm and clipping, rows to their experts and back, the root-mean-square norm.  Written from the definitions in include/cns.h, row by row where a loop is
-plainer than an array expression; test infrastructure only."""
+global gradient norm and clipping, rows to their experts and back, the root-mean-square norm.  Written from the
+definitions in include/cns.h, row by row where a loop is plainer than an array expression; test infrastructure only."""
 from __future__ import annotations
 
 import numpy as np
