@@ -64,10 +64,12 @@ struct NormGradParams {
 constexpr int kNormMaxParts = 3 * kStepMaxCtas;
 // Rows that a group of a gradient has at least, so that few parts are left to join: as many as it takes for no more CTAs
 // than SMs, four at most; four where one CTA then has all rows and no join follows.  In us, with one / two / four at least:
-//   f32   64 x 1000 3.38 / 3.71 / 4.57, 256 x 1000 3.66 / 4.01 / 4.76, 777 x 1000 5.31 / 5.05 / 4.97, 256 x 4096 6.15 / 6.02 / 7.31
-//   bf16  64 x 1000 4.05 / 4.58 / 5.60, 777 x 1000 5.42 / 4.90 / 5.88, 2000 x 1000 6.65 / 6.54 / 6.10, 8 x 4096 5.16 / 5.67 / 6.64,
-//         256 x 4096 8.50 / 6.72 / 7.35
-// (there by the rule 4.53 and 4.89 for 777 x 1000, with three and two rows), and eight nowhere better.
+//   f32    64 x 1000  3.38 / 3.71 / 4.57    256 x 1000  3.66 / 4.01 / 4.76    777 x 1000  5.31 / 5.05 / 4.97
+//         256 x 4096  6.15 / 6.02 / 7.31
+//   bf16   64 x 1000  4.05 / 4.58 / 5.60    777 x 1000  5.42 / 4.90 / 5.88   2000 x 1000  6.65 / 6.54 / 6.10
+//           8 x 4096  5.16 / 5.67 / 6.64    256 x 4096  8.50 / 6.72 / 7.35
+// and with eight nowhere less.
+// The rule's three rows take 777 x 1000 f32 in 4.53.
 __host__ __device__ constexpr int norm_least_rows(int64_t rows, int groups, int sms)
 {
     const int64_t ctas = (rows + groups - 1) / groups, each = (ctas + sms - 1) / sms;
@@ -443,13 +445,13 @@ __device__ __forceinline__ void any_quotients(float2 *v, float s)
     }
 }
 
-// The reciprocal in two numbers, hi below it and lo the rest (both positive, which keeps a zero's sign), and v hi + (v lo): the
-// quotient to within 2^-42 of itself, then rounded.  That gives another e4m3 value than the rounded quotient only where the
-// quotient is as near to the rounding border next to a tie, with v = V 2^i, s = S 2^k (V, S of 24 bits), ties K / 16 of 4 bits
-// after the point: where S (K 2^20 +- 1) is within 2^49 2^-42 of a multiple of 2^24, so S within 128 of one of 2^20.
-// Such S, one in 4096, are not `usual`, nor those whose lo, or remainder, would be below the normal numbers.
-// 16384 x 4096 bf16 to e4m3 alone, a scale a 128 columns, when it came: 42.7 us, by any_quotients alone 51.8, by one product with the
-// reciprocal (whose ties fall either way) 38.8.
+// The reciprocal in two numbers, hi below it and lo the rest (both positive, which keeps a zero's sign), and v hi + (v lo):
+// the quotient to within 2^-42 of itself, then rounded.  That gives another e4m3 value than the rounded quotient only where
+// the quotient is as near to the rounding border next to a tie: with v = V 2^i, s = S 2^k (V, S of 24 bits) and ties of
+// four bits after the point, K / 16, where S (K 2^20 +- 1) is within 2^49 2^-42 of a multiple of 2^24, so S within 128 of
+// one of 2^20.  Such S, one in 4096, are not `usual`, nor those whose lo, or remainder, would be below the normal numbers.
+// 16384 x 4096 bf16 to e4m3 alone, a scale for 128 columns, when this came: 42.7 us, by any_quotients alone 51.8, by one
+// product with the reciprocal (whose ties fall either way) 38.8.
 __device__ __forceinline__ bool usual(float s)
 {
     const uint32_t bits = __float_as_uint(s);
