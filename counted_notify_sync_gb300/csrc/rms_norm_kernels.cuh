@@ -68,13 +68,14 @@ constexpr int kNormMaxParts = 3 * kStepMaxCtas;
 //         256 x 4096  6.15 / 6.02 / 7.31
 //   bf16   64 x 1000  4.05 / 4.58 / 5.60    777 x 1000  5.42 / 4.90 / 5.88   2000 x 1000  6.65 / 6.54 / 6.10
 //           8 x 4096  5.16 / 5.67 / 6.64    256 x 4096  8.50 / 6.72 / 7.35
-// and with eight nowhere less.
-// The rule's three rows take 777 x 1000 f32 in 4.53.
+// and with eight less for 777 x 4096 bf16 alone (9.8, 10.7 to 11.0 with fewer).  The rule's three rows take 777 x 1000 f32
+// in 4.53.
 __host__ __device__ constexpr int norm_least_rows(int64_t rows, int groups, int sms)
 {
     const int64_t ctas = (rows + groups - 1) / groups, each = (ctas + sms - 1) / sms;
     return ctas <= 4 || each > 4 ? 4 : static_cast<int>(each);
 }
+
 // Dynamic shared memory that every kernel here may be launched with.
 constexpr int kNormMaxSmem = 200 * 1024;
 
